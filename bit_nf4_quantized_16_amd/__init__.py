@@ -29,8 +29,14 @@ __all__ = [
     "qlora_linear_bwd",
     "qlora_linear_bwd_group",
     "quantize_weight",
+    "Act8",
+    "act8_quantize",
+    "act8_dequantize",
+    "swiglu_fwd",
+    "swiglu_bwd",
     "QLoRALinearFunction",
     "QLoRAGroupFunction",
+    "SwiGLUFunction",
     "KernelTimer",
     "lib",
 ]
@@ -354,6 +360,123 @@ def qlora_linear_bwd_group(ws, X, dYs, As=None, Bs=None, scale=1.0, Us=None, nee
     return dX, dAs, dBs
 
 
+# ---- 8-bit activation checkpoints ----------------------------------------
+def _refuse(status, message):
+    raise QLoraError(status, message)
+
+
+def _tensor(t, name, dtype, shape, device=None):
+    """t, checked: a contiguous device tensor of this dtype and shape (on
+    ``device`` where given)."""
+    if not isinstance(t, torch.Tensor):
+        _refuse(_lib.QL_ERR_NULL, "%s is no tensor" % name)
+    if t.dtype != dtype:
+        _refuse(_lib.QL_ERR_UNSUPPORTED, "%s is %s, expected %s" % (name, t.dtype, dtype))
+    if tuple(t.shape) != tuple(shape):
+        _refuse(_lib.QL_ERR_SHAPE, "%s is %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if not t.is_contiguous():
+        _refuse(_lib.QL_ERR_UNSUPPORTED, "%s is not contiguous" % name)
+    if not t.is_cuda or (device is not None and t.device != device):
+        _refuse(_lib.QL_ERR_UNSUPPORTED, "%s is on %s, expected %s" % (name, t.device, device or "a GPU"))
+    return t
+
+
+def _matrix(t, name, dtype=torch.bfloat16):
+    """t, checked: a contiguous 2-D device tensor."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        _refuse(_lib.QL_ERR_SHAPE, "%s is not 2-D" % name)
+    return _tensor(t, name, dtype, t.shape)
+
+
+def _launch(device, call, *args):
+    """call(*args, stream) on ``device`` and its current stream."""
+    if device.index == torch.cuda.current_device():
+        _check(call(*args, torch.cuda.current_stream().cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            _check(call(*args, torch.cuda.current_stream().cuda_stream))
+
+
+@dataclass
+class Act8:
+    """An activation in 8 bits: E4M3 codes uint8 [rows, cols] with one scale
+    2^(scale - 127) per 32 values of a row, uint8 [rows, cols / 32]."""
+
+    rows: int
+    cols: int
+    codes: torch.Tensor
+    scale: torch.Tensor
+
+    def nbytes(self):
+        return self.codes.numel() + self.scale.numel()
+
+    def descriptor(self):
+        _tensor(self.codes, "codes", torch.uint8, (self.rows, self.cols))
+        _tensor(self.scale, "scale", torch.uint8, (self.rows, self.cols // _lib.QL_ACT8_BLOCK), self.codes.device)
+        return _lib.QlAct8(self.rows, self.cols, self.codes.data_ptr(), self.scale.data_ptr())
+
+
+def _act8_empty(rows, cols, device):
+    if cols % _lib.QL_ACT8_BLOCK:
+        _refuse(_lib.QL_ERR_SHAPE, "%d columns, not a multiple of %d" % (cols, _lib.QL_ACT8_BLOCK))
+    return Act8(rows, cols, torch.empty(rows, cols, dtype=torch.uint8, device=device),
+                torch.empty(rows, cols // _lib.QL_ACT8_BLOCK, dtype=torch.uint8, device=device))
+
+
+def act8_quantize(X, out=None):
+    """8-bit checkpoint (an Act8) of a bf16 activation [rows, cols], cols a
+    multiple of 32: nearest E4M3 value under one power-of-two scale per 32
+    values; NaN and infinities become NaN. ``out``: an Act8 to write into."""
+    rows, cols = _matrix(X, "X").shape
+    a = _act8_empty(rows, cols, X.device) if out is None else out
+    d = a.descriptor()
+    if (a.rows, a.cols) != (rows, cols) or a.codes.device != X.device:
+        _refuse(_lib.QL_ERR_SHAPE, "out is %d x %d on %s, X %d x %d on %s"
+                % (a.rows, a.cols, a.codes.device, rows, cols, X.device))
+    _launch(X.device, lib.act8_quantize, X.data_ptr(), d)
+    return a
+
+
+def act8_dequantize(a, dtype=torch.bfloat16, out=None):
+    """The stored values of an Act8 as a bf16 or fp32 tensor (exact)."""
+    if dtype not in (torch.bfloat16, torch.float32):
+        _refuse(_lib.QL_ERR_UNSUPPORTED, "output dtype %s" % dtype)
+    d = a.descriptor()
+    dev = a.codes.device
+    if out is None:
+        out = torch.empty(a.rows, a.cols, dtype=dtype, device=dev)
+    else:
+        _tensor(out, "out", dtype, (a.rows, a.cols), dev)
+    _launch(dev, lib.act8_dequantize, d, out.data_ptr(), _lib.QL_BF16 if dtype == torch.bfloat16 else _lib.QL_F32)
+    return out
+
+
+def swiglu_fwd(gate, up, checkpoint=True, h8=False):
+    """H = gate sigmoid(gate) up (bf16 [rows, cols], cols a multiple of 32).
+    Returns (H, gate8, up8, h8): the Act8 checkpoints of gate and up that
+    swiglu_bwd takes (None without ``checkpoint``) and, with ``h8``, that of H
+    for the down projection's backward."""
+    rows, cols = _matrix(gate, "gate").shape
+    dev = gate.device
+    _tensor(up, "up", torch.bfloat16, (rows, cols), dev)
+    H = torch.empty_like(gate)
+    acts = [_act8_empty(rows, cols, dev) if want else None for want in (checkpoint, checkpoint, h8)]
+    _launch(dev, lib.qlora_swiglu_fwd, gate.data_ptr(), up.data_ptr(), rows, cols, H.data_ptr(),
+            *[a.descriptor() if a is not None else None for a in acts])
+    return (H, *acts)
+
+
+def swiglu_bwd(gate8, up8, dH):
+    """(dgate, dup) bf16 of swiglu_fwd from its checkpoints and dH bf16."""
+    dg, du = gate8.descriptor(), up8.descriptor()
+    dev = gate8.codes.device
+    _tensor(dH, "dH", torch.bfloat16, (gate8.rows, gate8.cols), dev)
+    _tensor(up8.codes, "up8", torch.uint8, (gate8.rows, gate8.cols), dev)
+    dgate, dup = torch.empty_like(dH), torch.empty_like(dH)
+    _launch(dev, lib.qlora_swiglu_bwd, dg, du, dH.data_ptr(), dgate.data_ptr(), dup.data_ptr())
+    return dgate, dup
+
+
 def paged_adamw_step(param, grad, exp_avg, exp_avg_sq, step, lr=2e-4, betas=(0.9, 0.999), eps=1e-8,
                      weight_decay=0.0, param_bf16=None, copy_stream=None):
     """One AdamW step (fp32 state) of a flat fp32 parameter tensor in place.
@@ -431,6 +554,23 @@ class QLoRAGroupFunction(torch.autograd.Function):
         for i in range(n):
             grads += [dAs[i].to(As[i].dtype), dBs[i].to(Bs[i].dtype)]
         return (dX, None, None, *grads)
+
+
+class SwiGLUFunction(torch.autograd.Function):
+    """autograd wrapper of the gated activation: apply(gate, up) returns H
+    and keeps gate and up as 8-bit checkpoints for the backward."""
+
+    @staticmethod
+    def forward(ctx, gate, up):
+        H, g8, u8, _ = swiglu_fwd(gate.contiguous(), up.contiguous())
+        ctx.save_for_backward(g8.codes, g8.scale, u8.codes, u8.scale)
+        return H
+
+    @staticmethod
+    def backward(ctx, dH):
+        gc, gs, uc, us = ctx.saved_tensors
+        rows, cols = gc.shape
+        return swiglu_bwd(Act8(rows, cols, gc, gs), Act8(rows, cols, uc, us), dH.contiguous().to(torch.bfloat16))
 
 
 class KernelTimer:

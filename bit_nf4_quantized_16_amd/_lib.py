@@ -33,6 +33,9 @@ QL_KERNEL_QERROR = 9
 QL_KERNEL_KEEP_APPLY = 10
 QL_KERNEL_DX_KEEP = 11
 QL_KERNEL_ADAMW = 12
+QL_KERNEL_ACT8 = 13
+QL_KERNEL_SWIGLU = 14
+QL_ACT8_BLOCK = 32
 QL_NOALLOC_SCRATCH_BYTES = 96 << 20  # include/qlora_nf4.h
 QL_GRID_NF4 = 0
 QL_GRID_UNIFORM = 1
@@ -52,6 +55,15 @@ class QlNf4Weight(ctypes.Structure):
     ]
 
 
+class QlAct8(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("codes", ctypes.c_void_p),
+        ("scale", ctypes.c_void_p),
+    ]
+
+
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
@@ -59,6 +71,7 @@ _I = ctypes.c_int
 _SZ = ctypes.c_size_t
 _F = ctypes.c_float
 _WP = ctypes.POINTER(QlNf4Weight)
+_AP = ctypes.POINTER(QlAct8)
 
 # name -> (restype, argtypes); the exported surface of include/qlora_nf4.h
 SIGNATURES = {
@@ -90,6 +103,10 @@ SIGNATURES = {
     "qlora_linear_bwd_group": (_I, [_P, _I32, _P, _P, _I64, _P, _P, _I32, _F, _P, _P, _P, _P, _I, _P, _SZ, _P]),
     "qlora_linear_bwd_dropout_workspace": (_SZ, [_I64, _I64, _I64, _I32]),
     "qlora_linear_bwd_dropout": (_I, [_WP, _P, _P, _I64, _P, _P, _I32, _F, _P, _F, _P, _P, _P, _P, _I, _P, _SZ, _P]),
+    "act8_quantize": (_I, [_P, _AP, _P]),
+    "act8_dequantize": (_I, [_AP, _P, _I, _P]),
+    "qlora_swiglu_fwd": (_I, [_P, _P, _I64, _I64, _P, _AP, _AP, _AP, _P]),
+    "qlora_swiglu_bwd": (_I, [_AP, _AP, _P, _P, _P, _P]),
     "qlora_paged_adamw_workspace": (_SZ, [_I64]),
     "qlora_paged_adamw": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _F, _F, _F, _F, _F, _P, _SZ, _P, _P]),
     "qlora_status_string": (ctypes.c_char_p, [_I]),

@@ -948,6 +948,96 @@ int qlora_linear_bwd_dropout(const ql_nf4_weight* w, const uint16_t* X, const ui
 
 }  // extern "C"
 
+// ---- 8-bit activation checkpoints ------------------------------------------
+namespace {
+
+int check_act8_shape(int64_t rows, int64_t cols) {
+    if (rows < 0 || cols <= 0) return set_error(QL_ERR_SHAPE, "activation %lld x %lld", (long long)rows, (long long)cols);
+    if (cols % QL_ACT8_BLOCK != 0)
+        return set_error(QL_ERR_SHAPE, "%lld columns, not a multiple of %d", (long long)cols, QL_ACT8_BLOCK);
+    // a kernel gives a thread eight values, and a grid holds fewer than 2^32 threads
+    if (rows > (int64_t{1} << 34) / cols)
+        return set_error(QL_ERR_SHAPE, "activation %lld x %lld too large", (long long)rows, (long long)cols);
+    return QL_OK;
+}
+
+int check_act8(const ql_act8* a, const char* name) {
+    if (a == nullptr) return set_error(QL_ERR_NULL, "%s is NULL", name);
+    int s;
+    if ((s = check_act8_shape(a->rows, a->cols)) != QL_OK) return s;
+    if (a->rows == 0) return QL_OK;
+    if ((s = check_ptr(a->codes, "codes")) != QL_OK) return s;
+    return check_ptr(a->scale, "scale");
+}
+
+// A checkpoint given beside an activation of rows x cols (NULL: none).
+int check_act8_like(const ql_act8* a, const char* name, int64_t rows, int64_t cols) {
+    if (a == nullptr) return QL_OK;
+    if (a->rows != rows || a->cols != cols)
+        return set_error(QL_ERR_SHAPE, "%s is %lld x %lld, the activation %lld x %lld", name, (long long)a->rows,
+                         (long long)a->cols, (long long)rows, (long long)cols);
+    return check_act8(a, name);
+}
+
+Act8Dev to_dev(const ql_act8* a) { return a == nullptr ? Act8Dev{} : Act8Dev{a->codes, a->scale}; }
+
+}  // namespace
+
+extern "C" {
+
+int act8_quantize(const uint16_t* X, const ql_act8* a, void* stream) {
+    g_last_error[0] = '\0';
+    int s;
+    if ((s = check_act8(a, "checkpoint")) != QL_OK) return s;
+    if (a->rows == 0) return QL_OK;
+    if ((s = check_ptr(X, "X")) != QL_OK) return s;
+    return launch_act8_quantize(X, a->rows * a->cols, to_dev(a), static_cast<hipStream_t>(stream));
+}
+
+int act8_dequantize(const ql_act8* a, void* out, int out_dtype, void* stream) {
+    g_last_error[0] = '\0';
+    int s;
+    if ((s = check_act8(a, "checkpoint")) != QL_OK) return s;
+    if (out_dtype != QL_F32 && out_dtype != QL_BF16) return set_error(QL_ERR_UNSUPPORTED, "output dtype %d", out_dtype);
+    if (a->rows == 0) return QL_OK;
+    if ((s = check_ptr(out, "out")) != QL_OK) return s;
+    return launch_act8_dequantize(to_dev(a), a->rows * a->cols, out, out_dtype == QL_BF16,
+                                  static_cast<hipStream_t>(stream));
+}
+
+int qlora_swiglu_fwd(const uint16_t* gate, const uint16_t* up, int64_t rows, int64_t cols, uint16_t* H,
+                     const ql_act8* gate8, const ql_act8* up8, const ql_act8* h8, void* stream) {
+    g_last_error[0] = '\0';
+    int s;
+    if ((s = check_act8_shape(rows, cols)) != QL_OK) return s;
+    if ((s = check_act8_like(gate8, "gate8", rows, cols)) != QL_OK) return s;
+    if ((s = check_act8_like(up8, "up8", rows, cols)) != QL_OK) return s;
+    if ((s = check_act8_like(h8, "h8", rows, cols)) != QL_OK) return s;
+    if (rows == 0) return QL_OK;
+    if ((s = check_ptr(gate, "gate")) != QL_OK) return s;
+    if ((s = check_ptr(up, "up")) != QL_OK) return s;
+    if ((s = check_ptr(H, "H")) != QL_OK) return s;
+    return launch_swiglu_fwd(gate, up, rows * cols, H, to_dev(gate8), to_dev(up8), to_dev(h8),
+                             static_cast<hipStream_t>(stream));
+}
+
+int qlora_swiglu_bwd(const ql_act8* gate8, const ql_act8* up8, const uint16_t* dH, uint16_t* dgate, uint16_t* dup,
+                     void* stream) {
+    g_last_error[0] = '\0';
+    int s;
+    if ((s = check_act8(gate8, "gate8")) != QL_OK) return s;
+    if (up8 == nullptr) return set_error(QL_ERR_NULL, "up8 is NULL");
+    if ((s = check_act8_like(up8, "up8", gate8->rows, gate8->cols)) != QL_OK) return s;
+    if (gate8->rows == 0) return QL_OK;
+    if ((s = check_ptr(dH, "dH")) != QL_OK) return s;
+    if ((s = check_ptr(dgate, "dgate")) != QL_OK) return s;
+    if ((s = check_ptr(dup, "dup")) != QL_OK) return s;
+    return launch_swiglu_bwd(to_dev(gate8), to_dev(up8), dH, gate8->rows * gate8->cols, dgate, dup,
+                             static_cast<hipStream_t>(stream));
+}
+
+}  // extern "C"
+
 // ---- the forward without a workspace -------------------------------------
 // Scratch of qlora_linear_fwd_noalloc: device memory of the library itself,
 // one copy on every GPU the library runs on, held until the process ends.

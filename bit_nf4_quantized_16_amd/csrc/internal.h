@@ -224,6 +224,20 @@ struct GradArgs {
 size_t lora_grads_part_bytes(int64_t T, int64_t C0, int64_t C1, int r);
 int launch_lora_grads(GradArgs a, float* part, hipStream_t stream);
 
+// Device view of an 8-bit activation checkpoint (codes null: none).
+struct Act8Dev {
+    uint8_t* codes;
+    uint8_t* scale;
+};
+
+// n values (whole blocks of 32) each.
+int launch_act8_quantize(const uint16_t* X, int64_t n, Act8Dev out, hipStream_t stream);
+int launch_act8_dequantize(Act8Dev a, int64_t n, void* out, bool bf16_out, hipStream_t stream);
+int launch_swiglu_fwd(const uint16_t* gate, const uint16_t* up, int64_t n, uint16_t* H, Act8Dev g8, Act8Dev u8,
+                      Act8Dev h8, hipStream_t stream);
+int launch_swiglu_bwd(Act8Dev g8, Act8Dev u8, const uint16_t* dH, int64_t n, uint16_t* dgate, uint16_t* dup,
+                      hipStream_t stream);
+
 // AdamW step (fp32 state). paged: m and v are pinned host memory and pass
 // through ws (adamw_page_ws_bytes(n) bytes of device memory) in chunks,
 // copied on copy_stream (null or stream itself: everything on stream).

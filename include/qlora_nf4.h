@@ -479,6 +479,73 @@ int qlora_linear_bwd_dropout(const ql_nf4_weight* w, const uint16_t* X, const ui
                              void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * 8-bit activation checkpoints: what the backward needs of an activation,
+ * kept from the forward in 8.25 bits a value instead of 16.
+ *
+ *   rows, cols  of the row-major activation; cols a multiple of
+ *               QL_ACT8_BLOCK (32)
+ *   codes  [rows, cols] u8, OCP FP8 E4M3FN codes
+ *   scale  [rows, cols / 32] u8, one per block of 32 consecutive values of a
+ *          row: the block's scale is 2^(scale - 127)
+ *
+ * With a the largest magnitude among the block's finite values, the scale is
+ * 2^k with k the least integer such that a 2^-k <= 448, and at least -124. A
+ * finite x is stored as E4M3FN(x 2^-k), the nearest code with ties to an even
+ * mantissa; a NaN or infinite x as NaN. The stored value code * 2^k is exact
+ * in bf16 (one exception: magnitudes from 1.9375 * 2^127 on round up to 2^128,
+ * which bf16 and fp32 hold as infinity). The struct is host memory, its pointers are device pointers,
+ * 16-byte aligned.
+ */
+#define QL_ACT8_BLOCK 32
+typedef struct ql_act8 {
+    int64_t rows;
+    int64_t cols;
+    uint8_t* codes;
+    uint8_t* scale;
+} ql_act8;
+
+/*
+ * act8_quantize / act8_dequantize — store a bf16 activation as an 8-bit
+ * checkpoint, and restore one.
+ *
+ *   X    [a->rows, a->cols] bf16; a->codes and a->scale are written
+ *   out  [a->rows, a->cols], bf16 (out_dtype QL_BF16) or fp32 (QL_F32):
+ *        code * 2^(scale - 127), exact
+ *
+ * rows == 0 is a no-op.
+ * Errors: QL_ERR_NULL, QL_ERR_SHAPE (rows < 0, cols <= 0 or not a multiple of
+ * 32, more than 2^34 values), QL_ERR_UNSUPPORTED (out_dtype), QL_ERR_ALIGN,
+ * QL_ERR_HIP.
+ */
+int act8_quantize(const uint16_t* X, const ql_act8* a, void* stream);
+int act8_dequantize(const ql_act8* a, void* out, int out_dtype, void* stream);
+
+/*
+ * qlora_swiglu_fwd / qlora_swiglu_bwd — the gated activation between an MLP
+ * block's gate and up projections and its down projection, and its backward
+ * from 8-bit checkpoints:
+ *
+ *   forward   H = g sigmoid(g) u            (fp32, rounded to bf16 once)
+ *   backward  p = sigmoid(g)
+ *             dgate = dH u p (1 + g (1 - p)),  dup = dH g p
+ *
+ *   gate, up  [rows, cols] bf16, cols a multiple of 32;  H out, the same shape
+ *   gate8, up8, h8  checkpoints of gate, up and H (of the shape rows x cols)
+ *          written by the forward, each NULL to skip it; h8 is the checkpoint
+ *          the down projection's backward takes
+ *   gate8, up8 (backward)  the forward's; g and u are their restored values
+ *   dH     [rows, cols] bf16;  dgate, dup  out, [rows, cols] bf16
+ *
+ * sigmoid(g) = 1 / (1 + e^-g) in fp32, so g = -inf gives NaN. Outputs must not
+ * alias inputs or one another. rows == 0 is a no-op.
+ * Errors: as act8_quantize, QL_ERR_SHAPE also for checkpoints of other shapes.
+ */
+int qlora_swiglu_fwd(const uint16_t* gate, const uint16_t* up, int64_t rows, int64_t cols, uint16_t* H,
+                     const ql_act8* gate8, const ql_act8* up8, const ql_act8* h8, void* stream);
+int qlora_swiglu_bwd(const ql_act8* gate8, const ql_act8* up8, const uint16_t* dH, uint16_t* dgate,
+                     uint16_t* dup, void* stream);
+
+/*
  * qlora_paged_adamw — one AdamW step of the trained adapter parameters with
  * 32-bit optimizer state that lives in device memory or, paged out, in host
  * memory ([apxml], the paged-optimizer paragraph: optimizer state moves
@@ -554,7 +621,9 @@ const char* qlora_last_error(void);
 #define QL_KERNEL_KEEP_APPLY 10
 #define QL_KERNEL_DX_KEEP 11
 #define QL_KERNEL_ADAMW 12
-#define QL_KERNEL_COUNT 13
+#define QL_KERNEL_ACT8 13
+#define QL_KERNEL_SWIGLU 14
+#define QL_KERNEL_COUNT 15
 int qlora_timer_arm(int kernel_id);
 int qlora_timer_read(int kernel_id, int64_t* launches, double* total_ms);
 int qlora_timer_disarm(int kernel_id);

@@ -34,8 +34,11 @@ __all__ = [
     "act8_dequantize",
     "swiglu_fwd",
     "swiglu_bwd",
+    "qlora_linear_bwd_act8",
+    "qlora_linear_bwd_group_act8",
     "QLoRALinearFunction",
     "QLoRAGroupFunction",
+    "QLoRAGroupAct8Function",
     "SwiGLUFunction",
     "KernelTimer",
     "lib",
@@ -477,6 +480,102 @@ def swiglu_bwd(gate8, up8, dH):
     return dgate, dup
 
 
+def _adapters(A, B, rows, cols, device):
+    """The rank of an adapter pair (0 when A is None), shapes checked."""
+    if A is None:
+        return 0
+    r = _matrix(A, "A").shape[0]
+    _tensor(A, "A", torch.bfloat16, (r, cols), device)
+    _tensor(B, "B", torch.bfloat16, (rows, r), device)
+    return r
+
+
+def _grads(want, given, shape, name, accumulate, device):
+    """The fp32 gradient to write: the caller's, a new one, or None."""
+    if not want:
+        return None
+    if given is not None:
+        return _tensor(given, name, torch.float32, shape, device)
+    return (torch.zeros if accumulate else torch.empty)(*shape, dtype=torch.float32, device=device)
+
+
+def qlora_linear_bwd_act8(w, X8, dY, A=None, B=None, scale=1.0, U=None, need_dx=True, need_da=True, need_db=True,
+                          dA=None, dB=None, accumulate=False, keep=None, p=0.0):
+    """qlora_linear_bwd with the layer's input kept as an Act8 ``X8``. ``U``
+    (fp32 [T, r], from the forward) is required for dB; X8 may be None without
+    dA. dA and dB use U and G = s dY B in fp32."""
+    T = _matrix(dY, "dY").shape[0]
+    dev = dY.device
+    _tensor(dY, "dY", torch.bfloat16, (T, w.rows), dev)
+    r = _adapters(A, B, w.rows, w.cols, dev)
+    dX = torch.empty(T, w.cols, dtype=torch.bfloat16, device=dev) if need_dx else None
+    dA = _grads(r > 0 and need_da, dA, (r, w.cols), "dA", accumulate, dev)
+    dB = _grads(r > 0 and need_db, dB, (w.rows, r), "dB", accumulate, dev)
+    if dB is not None:
+        _tensor(U, "U", torch.float32, (T, r), dev)
+    x8 = None
+    if dA is not None:
+        x8 = X8.descriptor() if X8 is not None else _refuse(_lib.QL_ERR_NULL, "X8 is None (dA needs it)")
+        _tensor(X8.codes, "X8", torch.uint8, (T, w.cols), dev)
+    if keep is not None:
+        _tensor(keep.view(T, -1), "keep", torch.uint8, (T, w.cols // 8), dev)
+    ws, wsb = _workspace(lib.qlora_linear_bwd_act8_workspace(w.rows, w.cols, max(T, 1), r, keep is not None), dev)
+    if T == 0:  # no token: the sums are empty
+        for g in (dA, dB):
+            if g is not None and not accumulate:
+                g.zero_()
+        return dX, dA, dB
+    _launch(dev, lib.qlora_linear_bwd_act8, w.descriptor(), x8, dY.data_ptr(), T, _ptr(A), _ptr(B), r, float(scale),
+            _ptr(keep), float(p), _ptr(U) if dB is not None else None, _ptr(dX), _ptr(dA), _ptr(dB),
+            1 if accumulate else 0, _ptr(ws), wsb)
+    return dX, dA, dB
+
+
+def qlora_linear_bwd_group_act8(ws, X8, dYs, As=None, Bs=None, scale=1.0, Us=None, need_dx=True, need_da=True,
+                                need_db=True, dAs=None, dBs=None, accumulate=False):
+    """qlora_linear_bwd_group with the shared input kept as an Act8 ``X8``.
+    Returns (dX, list of dA or None, list of dB or None)."""
+    nw = len(ws)
+    if nw < 1 or len(dYs) != nw:
+        _refuse(_lib.QL_ERR_SHAPE, "%d weights and %d dY" % (nw, len(dYs)))
+    T = _matrix(dYs[0], "dY").shape[0]
+    dev = dYs[0].device
+    cols = ws[0].cols
+    r = 0
+    for i, w in enumerate(ws):
+        _tensor(dYs[i], "dY", torch.bfloat16, (T, w.rows), dev)
+        ri = _adapters(As[i] if As is not None else None, Bs[i] if As is not None else None, w.rows, cols, dev)
+        if i > 0 and ri != r:
+            _refuse(_lib.QL_ERR_SHAPE, "layer %d has rank %d, layer 0 rank %d" % (i, ri, r))
+        r = ri
+    dX = torch.empty(T, cols, dtype=torch.bfloat16, device=dev) if need_dx else None
+    need_da, need_db = need_da and r > 0, need_db and r > 0
+    pick = lambda ts, i: ts[i] if ts is not None else None
+    dAs = [_grads(need_da, pick(dAs, i), (r, cols), "dA", accumulate, dev) for i in range(nw)] if need_da else None
+    dBs = [_grads(need_db, pick(dBs, i), (w.rows, r), "dB", accumulate, dev) for i, w in enumerate(ws)] if need_db else None
+    if need_db:
+        for i in range(nw):
+            _tensor(pick(Us, i), "U", torch.float32, (T, r), dev)
+    x8 = None
+    if need_da:
+        x8 = X8.descriptor() if X8 is not None else _refuse(_lib.QL_ERR_NULL, "X8 is None (dA needs it)")
+        _tensor(X8.codes, "X8", torch.uint8, (T, cols), dev)
+    if T == 0:
+        for g in (dAs or []) + (dBs or []):
+            if not accumulate:
+                g.zero_()
+        return dX, dAs, dBs
+    arr = lambda ts: (ctypes.c_void_p * nw)(*[t.data_ptr() for t in ts]) if ts is not None else None
+    descs = [w.descriptor() for w in ws]
+    wp = (ctypes.c_void_p * nw)(*[ctypes.addressof(d) for d in descs])
+    rows = (ctypes.c_int64 * nw)(*[w.rows for w in ws])
+    ws_, wsb = _workspace(lib.qlora_linear_bwd_group_act8_workspace(rows, nw, cols, T, r), dev)
+    _launch(dev, lib.qlora_linear_bwd_group_act8, wp, nw, x8, arr(dYs), T, arr(As) if r > 0 else None,
+            arr(Bs) if r > 0 else None, r, float(scale), arr(Us) if need_db else None, _ptr(dX), arr(dAs), arr(dBs),
+            1 if accumulate else 0, _ptr(ws_), wsb)
+    return dX, dAs, dBs
+
+
 def paged_adamw_step(param, grad, exp_avg, exp_avg_sq, step, lr=2e-4, betas=(0.9, 0.999), eps=1e-8,
                      weight_decay=0.0, param_bf16=None, copy_stream=None):
     """One AdamW step (fp32 state) of a flat fp32 parameter tensor in place.
@@ -505,12 +604,22 @@ def paged_adamw_step(param, grad, exp_avg, exp_avg_sq, step, lr=2e-4, betas=(0.9
 
 class QLoRALinearFunction(torch.autograd.Function):
     """autograd wrapper: forward / backward run in the HIP library; W is frozen
-    (no gradient), A and B receive fp32 gradients cast to their dtype."""
+    (no gradient), A and B receive fp32 gradients cast to their dtype.
+    ``act8``: True keeps X as an 8-bit checkpoint instead of itself, an Act8
+    of X (shared with other layers, or swiglu_fwd's h8) is kept as it is; dA
+    then comes from the checkpoint."""
 
     @staticmethod
-    def forward(ctx, X, A, B, w, scale, keep=None, p=0.0):
+    def forward(ctx, X, A, B, w, scale, keep=None, p=0.0, act8=None):
         Y, U = qlora_linear_fwd(w, X.contiguous(), A.contiguous(), B.contiguous(), scale, save_u=True, keep=keep, p=p)
-        ctx.save_for_backward(X, A, B, U)
+        ctx.act8 = act8 is not None and act8 is not False
+        if ctx.act8:
+            X8 = act8_quantize(X.contiguous()) if act8 is True else act8
+            if (X8.rows, X8.cols) != tuple(X.shape):
+                _refuse(_lib.QL_ERR_SHAPE, "act8 is %d x %d, X %s" % (X8.rows, X8.cols, tuple(X.shape)))
+            ctx.save_for_backward(X8.codes, X8.scale, A, B, U)
+        else:
+            ctx.save_for_backward(X, A, B, U)
         ctx.w = w
         ctx.scale = scale
         ctx.keep = keep
@@ -519,6 +628,14 @@ class QLoRALinearFunction(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dY):
+        if ctx.act8:
+            codes, xs, A, B, U = ctx.saved_tensors
+            need = ctx.needs_input_grad
+            dX, dA, dB = qlora_linear_bwd_act8(ctx.w, Act8(*codes.shape, codes, xs), dY.contiguous().to(torch.bfloat16),
+                                               A.contiguous(), B.contiguous(), ctx.scale, U=U, need_dx=need[0],
+                                               need_da=need[1], need_db=need[2], keep=ctx.keep, p=ctx.p)
+            return (dX, dA.to(A.dtype) if need[1] else None, dB.to(B.dtype) if need[2] else None,
+                    None, None, None, None, None)
         X, A, B, U = ctx.saved_tensors
         dX, dA, dB = qlora_linear_bwd(ctx.w, X, dY.contiguous().to(torch.bfloat16), A, B, ctx.scale, U=U,
                                       need_dx=ctx.needs_input_grad[0], keep=ctx.keep, p=ctx.p)
@@ -554,6 +671,38 @@ class QLoRAGroupFunction(torch.autograd.Function):
         for i in range(n):
             grads += [dAs[i].to(As[i].dtype), dBs[i].to(Bs[i].dtype)]
         return (dX, None, None, *grads)
+
+
+class QLoRAGroupAct8Function(torch.autograd.Function):
+    """QLoRAGroupFunction with the shared X kept as one 8-bit checkpoint:
+    apply(X, act8, scale, ws, A_0, B_0, A_1, B_1, ...), ``act8`` an Act8 of X
+    or None to make one here."""
+
+    @staticmethod
+    def forward(ctx, X, act8, scale, ws, *adapters):
+        As, Bs = [a.contiguous() for a in adapters[0::2]], [b.contiguous() for b in adapters[1::2]]
+        outs = qlora_linear_fwd_group(ws, X.contiguous(), As, Bs, scale)
+        X8 = act8 if act8 is not None else act8_quantize(X.contiguous())
+        if (X8.rows, X8.cols) != tuple(X.shape):
+            _refuse(_lib.QL_ERR_SHAPE, "act8 is %d x %d, X %s" % (X8.rows, X8.cols, tuple(X.shape)))
+        ctx.save_for_backward(X8.codes, X8.scale, *As, *Bs, *[U for _, U in outs])
+        ctx.ws = ws
+        ctx.scale = scale
+        return tuple(Y for Y, _ in outs)
+
+    @staticmethod
+    def backward(ctx, *dYs):
+        n = len(ctx.ws)
+        codes, xs, *rest = ctx.saved_tensors
+        As, Bs, Us = rest[:n], rest[n:2 * n], rest[2 * n:]
+        dYs = [(d if d is not None else torch.zeros(codes.shape[0], w.rows, device=codes.device)).contiguous()
+               .to(torch.bfloat16) for d, w in zip(dYs, ctx.ws)]
+        dX, dAs, dBs = qlora_linear_bwd_group_act8(ctx.ws, Act8(*codes.shape, codes, xs), dYs, As, Bs, ctx.scale,
+                                                   Us=Us, need_dx=ctx.needs_input_grad[0])
+        grads = []
+        for i in range(n):
+            grads += [dAs[i].to(As[i].dtype), dBs[i].to(Bs[i].dtype)]
+        return (dX, None, None, None, *grads)
 
 
 class SwiGLUFunction(torch.autograd.Function):

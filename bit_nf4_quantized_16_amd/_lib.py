@@ -35,6 +35,7 @@ QL_KERNEL_DX_KEEP = 11
 QL_KERNEL_ADAMW = 12
 QL_KERNEL_ACT8 = 13
 QL_KERNEL_SWIGLU = 14
+QL_KERNEL_ACT8_GRAD = 15
 QL_ACT8_BLOCK = 32
 QL_NOALLOC_SCRATCH_BYTES = 96 << 20  # include/qlora_nf4.h
 QL_GRID_NF4 = 0
@@ -107,6 +108,10 @@ SIGNATURES = {
     "act8_dequantize": (_I, [_AP, _P, _I, _P]),
     "qlora_swiglu_fwd": (_I, [_P, _P, _I64, _I64, _P, _AP, _AP, _AP, _P]),
     "qlora_swiglu_bwd": (_I, [_AP, _AP, _P, _P, _P, _P]),
+    "qlora_linear_bwd_act8_workspace": (_SZ, [_I64, _I64, _I64, _I32, _I]),
+    "qlora_linear_bwd_act8": (_I, [_WP, _AP, _P, _I64, _P, _P, _I32, _F, _P, _F, _P, _P, _P, _P, _I, _P, _SZ, _P]),
+    "qlora_linear_bwd_group_act8_workspace": (_SZ, [_P, _I32, _I64, _I64, _I32]),
+    "qlora_linear_bwd_group_act8": (_I, [_P, _I32, _AP, _P, _I64, _P, _P, _I32, _F, _P, _P, _P, _P, _I, _P, _SZ, _P]),
     "qlora_paged_adamw_workspace": (_SZ, [_I64]),
     "qlora_paged_adamw": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _F, _F, _F, _F, _F, _P, _SZ, _P, _P]),
     "qlora_status_string": (ctypes.c_char_p, [_I]),

@@ -979,7 +979,160 @@ int check_act8_like(const ql_act8* a, const char* name, int64_t rows, int64_t co
     return check_act8(a, name);
 }
 
-Act8Dev to_dev(const ql_act8* a) { return a == nullptr ? Act8Dev{} : Act8Dev{a->codes, a->scale}; }
+Act8Dev act8_dev(const ql_act8* a) { return a == nullptr ? Act8Dev{} : Act8Dev{a->codes, a->scale}; }
+
+// ---- the layer's backward from a checkpoint of its input --------------------
+struct Bwd8Ws {
+    uint16_t* Gp[kGemmMaxGroup] = {};  // bf16 [T, rp64] = G per layer, dX's LoRA operand
+    float* G = nullptr;                // fp32 [T, r] = G of the layer being processed, dA's operand
+    float* gpart = nullptr;            // fp32 token-split partials of dA and dB
+    void* proj = nullptr;              // split partials of the G projection
+    float* split = nullptr;            // fp32 split-K partials of the dX GEMM
+    uint64_t* gword = nullptr;         // one layer, G inside the dX launch: G words and the epoch word
+    size_t bytes = 0;
+};
+
+// One layer (group false) or layers that share X (group true: their dX is
+// summed by one launch, which takes G from projections of their own).
+Bwd8Ws carve_bwd8(void* ws, const int64_t* N, int nw, int64_t K, int64_t T, int32_t r, bool group, bool want_dx,
+                  bool want_da, bool want_db, bool drop) {
+    Carver c(ws);
+    Bwd8Ws b;
+    if (r > 0) {
+        if (want_dx && !group && !drop && gemm_dx_g_in_launch(N[0], K, T, r))
+            b.gword = c.take<uint64_t>(gemm_fwd_u_words(T, r));
+        else if (want_dx)
+            for (int i = 0; i < nw; ++i) b.Gp[i] = c.take<uint16_t>(static_cast<size_t>(T) * rank_pad64(r));
+        if (want_da) b.G = c.take<float>(static_cast<size_t>(T) * r);
+        size_t gb = 0, pb = 0;
+        for (int i = 0; i < nw; ++i) {
+            // a layer may be asked for one gradient only: the larger need
+            const bool one[3][2] = {{want_da, want_db}, {want_da, false}, {false, want_db}};
+            for (const auto& o : one) gb = std::max(gb, act8_grads_part_bytes(T, o[0] ? K : 0, o[1] ? N[i] : 0, r));
+            pb = std::max(pb, lora_proj_ws_bytes(T, r, N[i], true));
+        }
+        if (gb) b.gpart = c.take<float>(gb / sizeof(float));
+        if (pb) b.proj = c.take<char>(pb);
+    }
+    if (want_dx) {
+        const size_t sb = group ? gemm_split_bytes(K, T, int64_t{64} * gemm_group_steps(N, nw)) : gemm_split_bytes(K, T, N[0]);
+        if (sb) b.split = c.take<float>(sb / sizeof(float));
+    }
+    b.bytes = align_up(c.off, 256);
+    return b;
+}
+
+int check_ws(const void* ws, size_t ws_bytes, size_t need) {
+    if (need == 0) return QL_OK;
+    if (ws == nullptr || ws_bytes < need)
+        return set_error(QL_ERR_WORKSPACE, "workspace %zu bytes, need %zu", ws == nullptr ? 0 : ws_bytes, need);
+    if (!aligned16(ws)) return set_error(QL_ERR_ALIGN, "workspace is not 16-byte aligned");
+    return QL_OK;
+}
+
+// Everything of a backward from checkpoints, for one layer (group false,
+// nw 1) or several: the arrays hold nw entries.
+int linear_bwd8(const ql_nf4_weight* const* w, int32_t nw, bool group, const ql_act8* X8, const uint16_t* const* dY,
+                int64_t T, const uint16_t* const* A, const uint16_t* const* B, int32_t r, float scale,
+                const uint8_t* keep, float p, const float* const* U, uint16_t* dX, float* const* dA, float* const* dB,
+                int accumulate, void* ws, size_t ws_bytes, void* stream) {
+    g_last_error[0] = '\0';
+    int s;
+    if (nw < 1 || nw > kGemmMaxGroup) return set_error(QL_ERR_SHAPE, "%d weights in a group (1 to %d)", nw, kGemmMaxGroup);
+    if (w == nullptr || dY == nullptr) return set_error(QL_ERR_NULL, "%s array is NULL", w == nullptr ? "w" : "dY");
+    if (r > 0 && (A == nullptr || B == nullptr))
+        return set_error(QL_ERR_NULL, "%s array is NULL", A == nullptr ? "A" : "B");
+    if (accumulate != 0 && accumulate != 1) return set_error(QL_ERR_UNSUPPORTED, "accumulate = %d", accumulate);
+    const bool drop = keep != nullptr;
+    if (drop && (s = check_dropout(keep, p)) != QL_OK) return s;
+    if (!drop && p != 0.0f) return set_error(QL_ERR_UNSUPPORTED, "dropout p = %g without a keep mask", (double)p);
+    const float c = drop ? 1.0f / (1.0f - p) : 1.0f;
+    int64_t rows[kGemmMaxGroup];
+    bool want_da = false, want_db = false;
+    auto at = [](auto* const* a, int i) { return a != nullptr ? a[i] : nullptr; };
+    for (int i = 0; i < nw; ++i) {
+        if ((s = check_weight(w[i])) != QL_OK) return s;
+        if ((s = check_linear_shape(w[i], T, r)) != QL_OK) return s;
+        if (w[i]->cols != w[0]->cols)
+            return set_error(QL_ERR_SHAPE, "weight %d has %lld columns, weight 0 %lld", i, (long long)w[i]->cols,
+                             (long long)w[0]->cols);
+        if ((w[i]->dq_blocksize != 0) != (w[0]->dq_blocksize != 0))
+            return set_error(QL_ERR_UNSUPPORTED, "weight %d and weight 0 differ in double quantization", i);
+        rows[i] = w[i]->rows;
+        const bool da = at(dA, i) != nullptr, db = at(dB, i) != nullptr;
+        if (r == 0 && (da || db)) return set_error(QL_ERR_SHAPE, "dA / dB requested with rank 0");
+        if (da && (s = check_ptr(dA[i], "dA")) != QL_OK) return s;
+        if (db && (s = check_ptr(dB[i], "dB")) != QL_OK) return s;
+        if (db && T > 0 && at(U, i) == nullptr) return set_error(QL_ERR_NULL, "U_saved is NULL (dB needs it)");
+        if (db && T > 0 && (s = check_ptr(U[i], "U_saved")) != QL_OK) return s;
+        if (r > 0) {
+            if ((s = check_ptr(A[i], "A")) != QL_OK) return s;
+            if ((s = check_ptr(B[i], "B")) != QL_OK) return s;
+        }
+        want_da = want_da || da;
+        want_db = want_db || db;
+    }
+    const int64_t K = w[0]->cols;
+    if (want_da) {
+        if (X8 == nullptr) return set_error(QL_ERR_NULL, "X8 is NULL (dA needs it)");
+        if ((s = check_act8_like(X8, "X8", T, K)) != QL_OK) return s;
+    }
+    const bool want_dx = dX != nullptr;
+    if (T == 0 || (!want_dx && !want_da && !want_db)) return QL_OK;
+    for (int i = 0; i < nw; ++i)
+        if ((s = check_ptr(dY[i], "dY")) != QL_OK) return s;
+    if (want_dx && (s = check_ptr(dX, "dX")) != QL_OK) return s;
+    const Bwd8Ws b = carve_bwd8(ws, rows, nw, K, T, r, group, want_dx, want_da, want_db, drop);
+    if ((s = check_ws(ws, ws_bytes, b.bytes)) != QL_OK) return s;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    const int rp = rank_pad64(r);
+    for (int i = 0; i < nw; ++i) {
+        const bool da = at(dA, i) != nullptr, db = at(dB, i) != nullptr;
+        ProjArgs g{};  // G = s dY B: fp32 for dA, bf16 padded to rp for dX
+        g.proj = 1;
+        g.P = dY[i];
+        g.ldp = rows[i];
+        g.Q = r > 0 ? B[i] : nullptr;
+        g.ldq = r;
+        g.rq = r;
+        g.T = T;
+        g.kred = rows[i];
+        g.alpha_f = scale;
+        g.out_f = da ? b.G : nullptr;
+        g.ld_f = r;
+        g.alpha_b = scale;
+        g.out_b = want_dx ? b.Gp[i] : nullptr;
+        g.ld_b = rp;
+        if (r > 0 && b.gword == nullptr && (want_dx || da) && (s = launch_lora_proj(g, true, b.proj, st)) != QL_OK)
+            return s;
+        if (want_dx && !group) {
+            if (b.gword != nullptr) {
+                s = launch_gemm_dx_g(to_dev(w[0]), dY[0], A[0], r, dX, T, rows[0], K, g, b.gword, st);
+            } else {
+                s = launch_gemm_dx(to_dev(w[0]), dY[0], b.Gp[0], r > 0 ? A[0] : nullptr, r, drop ? 0 : rp, dX, T, rows[0],
+                                   K, b.split, st);
+                if (s == QL_OK && drop && r > 0) s = launch_lora_dx_keep(b.Gp[0], rp, A[0], r, keep, c, T, K, dX, st);
+            }
+            if (s != QL_OK) return s;
+        }
+        if (da || db) {
+            Act8GradArgs a{};
+            a.r = r;
+            a.T = T;
+            a.accumulate = accumulate;
+            if (da) a.pb[0] = Act8GradProblem{X8->codes, X8->scale, keep, K, b.G, dA[i], 1, c, nullptr};
+            if (db) a.pb[1] = Act8GradProblem{dY[i], nullptr, nullptr, rows[i], U[i], dB[i], 0, scale, nullptr};
+            if ((s = launch_act8_grads(a, b.gpart, st)) != QL_OK) return s;
+        }
+    }
+    if (want_dx && group) {
+        GemmLayer layers[kGemmMaxGroup];
+        for (int i = 0; i < nw; ++i)
+            layers[i] = GemmLayer{to_dev(w[i]), dY[i], rows[i], r > 0 ? b.Gp[i] : nullptr, r > 0 ? A[i] : nullptr, nullptr};
+        return launch_gemm_dx_group(layers, nw, r, rp, dX, T, K, b.split, st);
+    }
+    return QL_OK;
+}
 
 }  // namespace
 
@@ -991,7 +1144,7 @@ int act8_quantize(const uint16_t* X, const ql_act8* a, void* stream) {
     if ((s = check_act8(a, "checkpoint")) != QL_OK) return s;
     if (a->rows == 0) return QL_OK;
     if ((s = check_ptr(X, "X")) != QL_OK) return s;
-    return launch_act8_quantize(X, a->rows * a->cols, to_dev(a), static_cast<hipStream_t>(stream));
+    return launch_act8_quantize(X, a->rows * a->cols, act8_dev(a), static_cast<hipStream_t>(stream));
 }
 
 int act8_dequantize(const ql_act8* a, void* out, int out_dtype, void* stream) {
@@ -1001,7 +1154,7 @@ int act8_dequantize(const ql_act8* a, void* out, int out_dtype, void* stream) {
     if (out_dtype != QL_F32 && out_dtype != QL_BF16) return set_error(QL_ERR_UNSUPPORTED, "output dtype %d", out_dtype);
     if (a->rows == 0) return QL_OK;
     if ((s = check_ptr(out, "out")) != QL_OK) return s;
-    return launch_act8_dequantize(to_dev(a), a->rows * a->cols, out, out_dtype == QL_BF16,
+    return launch_act8_dequantize(act8_dev(a), a->rows * a->cols, out, out_dtype == QL_BF16,
                                   static_cast<hipStream_t>(stream));
 }
 
@@ -1017,7 +1170,7 @@ int qlora_swiglu_fwd(const uint16_t* gate, const uint16_t* up, int64_t rows, int
     if ((s = check_ptr(gate, "gate")) != QL_OK) return s;
     if ((s = check_ptr(up, "up")) != QL_OK) return s;
     if ((s = check_ptr(H, "H")) != QL_OK) return s;
-    return launch_swiglu_fwd(gate, up, rows * cols, H, to_dev(gate8), to_dev(up8), to_dev(h8),
+    return launch_swiglu_fwd(gate, up, rows * cols, H, act8_dev(gate8), act8_dev(up8), act8_dev(h8),
                              static_cast<hipStream_t>(stream));
 }
 
@@ -1032,8 +1185,36 @@ int qlora_swiglu_bwd(const ql_act8* gate8, const ql_act8* up8, const uint16_t* d
     if ((s = check_ptr(dH, "dH")) != QL_OK) return s;
     if ((s = check_ptr(dgate, "dgate")) != QL_OK) return s;
     if ((s = check_ptr(dup, "dup")) != QL_OK) return s;
-    return launch_swiglu_bwd(to_dev(gate8), to_dev(up8), dH, gate8->rows * gate8->cols, dgate, dup,
+    return launch_swiglu_bwd(act8_dev(gate8), act8_dev(up8), dH, gate8->rows * gate8->cols, dgate, dup,
                              static_cast<hipStream_t>(stream));
+}
+
+size_t qlora_linear_bwd_act8_workspace(int64_t rows, int64_t cols, int64_t T, int32_t r, int dropout) {
+    if (rows <= 0 || cols <= 0 || T <= 0 || r < 0 || r > QL_MAX_RANK) return 0;
+    return carve_bwd8(nullptr, &rows, 1, cols, T, r, false, true, true, true, dropout != 0).bytes;
+}
+
+int qlora_linear_bwd_act8(const ql_nf4_weight* w, const ql_act8* X8, const uint16_t* dY, int64_t T, const uint16_t* A,
+                          const uint16_t* B, int32_t r, float scale, const uint8_t* keep, float p,
+                          const float* U_saved, uint16_t* dX, float* dA, float* dB, int accumulate, void* ws,
+                          size_t ws_bytes, void* stream) {
+    return linear_bwd8(&w, 1, false, X8, &dY, T, &A, &B, r, scale, keep, p, &U_saved, dX, &dA, &dB, accumulate, ws,
+                       ws_bytes, stream);
+}
+
+size_t qlora_linear_bwd_group_act8_workspace(const int64_t* rows, int32_t nw, int64_t cols, int64_t T, int32_t r) {
+    if (rows == nullptr || nw < 1 || nw > kGemmMaxGroup || cols <= 0 || T <= 0 || r < 0 || r > QL_MAX_RANK) return 0;
+    for (int i = 0; i < nw; ++i)
+        if (rows[i] <= 0) return 0;
+    return carve_bwd8(nullptr, rows, nw, cols, T, r, true, true, true, true, false).bytes;
+}
+
+int qlora_linear_bwd_group_act8(const ql_nf4_weight* const* w, int32_t nw, const ql_act8* X8, const uint16_t* const* dY,
+                                int64_t T, const uint16_t* const* A, const uint16_t* const* B, int32_t r, float scale,
+                                const float* const* U_saved, uint16_t* dX, float* const* dA, float* const* dB,
+                                int accumulate, void* ws, size_t ws_bytes, void* stream) {
+    return linear_bwd8(w, nw, true, X8, dY, T, A, B, r, scale, nullptr, 0.0f, U_saved, dX, dA, dB, accumulate, ws,
+                       ws_bytes, stream);
 }
 
 }  // extern "C"

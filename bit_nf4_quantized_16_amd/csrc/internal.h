@@ -238,6 +238,35 @@ int launch_swiglu_fwd(const uint16_t* gate, const uint16_t* up, int64_t n, uint1
 int launch_swiglu_bwd(Act8Dev g8, Act8Dev u8, const uint16_t* dH, int64_t n, uint16_t* dgate, uint16_t* dup,
                       hipStream_t stream);
 
+// Adapter gradients from an 8-bit checkpoint: out = (accumulate ? out : 0) +
+// scale * sum_t V[t][j] M[t][c], written as out[j][c] (layout_jc) or
+// out[c][j], j < r, c < C (C % 8 == 0; % 64 for a checkpoint). V fp32 [T, r];
+// M bf16 [T, C], or E4M3 codes [T, C] with scale8 [T, C / 32] and, where keep
+// is given, masked by its bits [T, C / 8]. A problem with out == NULL is
+// skipped.
+struct Act8GradProblem {
+    const void* M;
+    const uint8_t* scale8;  // null: M is bf16
+    const uint8_t* keep;
+    int64_t C;
+    const float* V;
+    float* out;
+    int layout_jc;
+    float scale;
+    float* part;  // set by the launcher
+};
+struct Act8GradArgs {
+    Act8GradProblem pb[2];
+    int nblk0;  // set by the launcher
+    int r;
+    int64_t T;
+    int64_t t_per;  // set by the launcher
+    int accumulate;
+};
+// fp32 workspace for token-split partials (0 when one split suffices)
+size_t act8_grads_part_bytes(int64_t T, int64_t C0, int64_t C1, int r);
+int launch_act8_grads(Act8GradArgs a, float* part, hipStream_t stream);
+
 // AdamW step (fp32 state). paged: m and v are pinned host memory and pass
 // through ws (adamw_page_ws_bytes(n) bytes of device memory) in chunks,
 // copied on copy_stream (null or stream itself: everything on stream).

@@ -546,6 +546,50 @@ int qlora_swiglu_bwd(const ql_act8* gate8, const ql_act8* up8, const uint16_t* d
                      uint16_t* dup, void* stream);
 
 /*
+ * qlora_linear_bwd_act8 — qlora_linear_bwd with the layer's input kept as an
+ * 8-bit checkpoint (only dA reads it):
+ *
+ *   dX = dY W' + c (G A) * keep,   G = s dY B
+ *   dA = c G^T (X8 * keep),        dB = s dY^T U_saved
+ *
+ *   X8       checkpoint of X, [T, K] (read for dA only; NULL if dA is NULL)
+ *   keep, p  the dropout mask and probability of qlora_linear_fwd_dropout;
+ *            keep NULL: no dropout (c = 1, p must be 0)
+ *   U_saved  [T, r] fp32 from the forward, required for dB: it is not
+ *            recomputed from the rounded X8
+ *
+ * dA and dB use G and U in fp32 (qlora_linear_bwd rounds both to bf16 first),
+ * so against the exact sums over X8, dY and U they carry fp32 rounding only;
+ * dX is bitwise qlora_linear_bwd's (qlora_linear_bwd_dropout's). Other
+ * arguments, layouts and errors as qlora_linear_bwd, with QL_ERR_SHAPE for a
+ * checkpoint of another shape and QL_ERR_UNSUPPORTED for p outside [0, 1) or
+ * nonzero without a mask. The workspace is
+ * qlora_linear_bwd_act8_workspace(...) bytes, dropout nonzero when keep is
+ * given.
+ */
+size_t qlora_linear_bwd_act8_workspace(int64_t rows, int64_t cols, int64_t T, int32_t r, int dropout);
+int qlora_linear_bwd_act8(const ql_nf4_weight* w, const ql_act8* X8, const uint16_t* dY, int64_t T,
+                          const uint16_t* A, const uint16_t* B, int32_t r, float scale, const uint8_t* keep,
+                          float p, const float* U_saved, uint16_t* dX, float* dA, float* dB, int accumulate,
+                          void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * qlora_linear_bwd_group_act8 — qlora_linear_bwd_group with the shared input
+ * kept as one 8-bit checkpoint: dX bitwise qlora_linear_bwd_group's, dA[i]
+ * and dB[i] bitwise those of qlora_linear_bwd_act8 for layer i. U_saved[i] is
+ * required where dB[i] is wanted, X8 where any dA[i] is. Other arguments and
+ * errors as qlora_linear_bwd_group; the workspace is
+ * qlora_linear_bwd_group_act8_workspace(...) bytes.
+ */
+size_t qlora_linear_bwd_group_act8_workspace(const int64_t* rows, int32_t nw, int64_t cols, int64_t T,
+                                             int32_t r);
+int qlora_linear_bwd_group_act8(const ql_nf4_weight* const* w, int32_t nw, const ql_act8* X8,
+                                const uint16_t* const* dY, int64_t T, const uint16_t* const* A,
+                                const uint16_t* const* B, int32_t r, float scale,
+                                const float* const* U_saved, uint16_t* dX, float* const* dA,
+                                float* const* dB, int accumulate, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * qlora_paged_adamw — one AdamW step of the trained adapter parameters with
  * 32-bit optimizer state that lives in device memory or, paged out, in host
  * memory ([apxml], the paged-optimizer paragraph: optimizer state moves
@@ -623,7 +667,8 @@ const char* qlora_last_error(void);
 #define QL_KERNEL_ADAMW 12
 #define QL_KERNEL_ACT8 13
 #define QL_KERNEL_SWIGLU 14
-#define QL_KERNEL_COUNT 15
+#define QL_KERNEL_ACT8_GRAD 15
+#define QL_KERNEL_COUNT 16
 int qlora_timer_arm(int kernel_id);
 int qlora_timer_read(int kernel_id, int64_t* launches, double* total_ms);
 int qlora_timer_disarm(int kernel_id);

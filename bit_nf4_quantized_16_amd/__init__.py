@@ -36,6 +36,10 @@ __all__ = [
     "swiglu_bwd",
     "qlora_linear_bwd_act8",
     "qlora_linear_bwd_group_act8",
+    "Q4GWeight",
+    "q4g_quantize",
+    "q4g_dequantize",
+    "q4g_linear_fwd",
     "QLoRALinearFunction",
     "QLoRAGroupFunction",
     "QLoRAGroupAct8Function",
@@ -574,6 +578,88 @@ def qlora_linear_bwd_group_act8(ws, X8, dYs, As=None, Bs=None, scale=1.0, Us=Non
             arr(Bs) if r > 0 else None, r, float(scale), arr(Us) if need_db else None, _ptr(dX), arr(dAs), arr(dBs),
             1 if accumulate else 0, _ptr(ws_), wsb)
     return dX, dAs, dBs
+
+
+# ---- 4-bit weights with group scales ---------------------------------------
+@dataclass
+class Q4GWeight:
+    """A weight in 4 bits with group scales: w' = scale (q - zero)."""
+
+    rows: int
+    cols: int
+    group: int  # 32, 64 or 128 values along a row
+    packed: torch.Tensor  # uint8 [rows, 16 ceil(cols / 32)]
+    scale: torch.Tensor  # bf16 or fp32 [rows, ceil(cols / group)]
+    zero: torch.Tensor = None  # uint8 like scale, or None: 8 throughout
+
+    @property
+    def shape(self):
+        return (self.rows, self.cols)
+
+    def nbytes(self):
+        n = self.packed.numel() + self.scale.numel() * self.scale.element_size()
+        return n + (self.zero.numel() if self.zero is not None else 0)
+
+    def descriptor(self):
+        dev = self.packed.device
+        if self.scale.dtype not in _DTYPES:
+            _refuse(_lib.QL_ERR_UNSUPPORTED, "scale is %s, expected bf16 or fp32" % self.scale.dtype)
+        groups = (self.rows, -(-self.cols // self.group))
+        _tensor(self.packed, "packed", torch.uint8, (self.rows, 16 * -(-self.cols // 32)))
+        _tensor(self.scale, "scale", self.scale.dtype, groups, dev)
+        if self.zero is not None:
+            _tensor(self.zero, "zero", torch.uint8, groups, dev)
+        return _lib.QlQ4GWeight(self.rows, self.cols, self.group, _DTYPES[self.scale.dtype], self.packed.data_ptr(),
+                                self.scale.data_ptr(), self.zero.data_ptr() if self.zero is not None else None)
+
+
+_DTYPES = {torch.float32: _lib.QL_F32, torch.bfloat16: _lib.QL_BF16}
+
+
+def q4g_quantize(W, group=128, symmetric=False, scale_dtype=torch.bfloat16):
+    """Round a 2-D fp32 or bf16 weight to 4 bits with one scale (and, unless
+    ``symmetric``, one zero point) per ``group`` values of a row."""
+    if not isinstance(W, torch.Tensor) or W.dtype not in _DTYPES or scale_dtype not in _DTYPES:
+        _refuse(_lib.QL_ERR_UNSUPPORTED, "W and its scales are bf16 or fp32")
+    rows, cols = _matrix(W, "W", W.dtype).shape
+    if group not in (32, 64, 128):
+        _refuse(_lib.QL_ERR_UNSUPPORTED, "group %s (32, 64 or 128)" % (group,))
+    dev = W.device
+    groups = (rows, -(-cols // group))
+    packed = torch.empty(rows, 16 * -(-cols // 32), dtype=torch.uint8, device=dev)
+    scale = torch.empty(groups, dtype=scale_dtype, device=dev)
+    zero = None if symmetric else torch.empty(groups, dtype=torch.uint8, device=dev)
+    _launch(dev, lib.q4g_quantize, W.data_ptr(), _DTYPES[W.dtype], rows, cols, group, packed.data_ptr(),
+            scale.data_ptr(), _DTYPES[scale_dtype], zero.data_ptr() if zero is not None else None)
+    return Q4GWeight(rows, cols, group, packed, scale, zero)
+
+
+def q4g_dequantize(w, dtype=torch.bfloat16, out=None):
+    """Expand a Q4GWeight to a [rows, cols] bf16 (or fp32) tensor."""
+    if dtype not in _DTYPES:
+        _refuse(_lib.QL_ERR_UNSUPPORTED, "output dtype %s" % dtype)
+    d = w.descriptor()
+    dev = w.packed.device
+    if out is None:
+        out = torch.empty(w.rows, w.cols, dtype=dtype, device=dev)
+    else:
+        _tensor(out, "out", dtype, (w.rows, w.cols), dev)
+    _launch(dev, lib.q4g_dequantize, d, out.data_ptr(), _DTYPES[dtype])
+    return out
+
+
+def q4g_linear_fwd(w, X, out=None):
+    """Y = X W'^T (bf16 [T, rows]) on a Q4GWeight, X bf16 [T, cols]; made for
+    decoding (up to 64 tokens read the weight once)."""
+    T = _matrix(X, "X").shape[0]
+    dev = w.packed.device
+    _tensor(X, "X", torch.bfloat16, (T, w.cols), dev)
+    if out is None:
+        out = torch.empty(T, w.rows, dtype=torch.bfloat16, device=dev)
+    else:
+        _tensor(out, "out", torch.bfloat16, (T, w.rows), dev)
+    _launch(dev, lib.q4g_linear_fwd, w.descriptor(), X.data_ptr(), T, out.data_ptr())
+    return out
 
 
 def paged_adamw_step(param, grad, exp_avg, exp_avg_sq, step, lr=2e-4, betas=(0.9, 0.999), eps=1e-8,

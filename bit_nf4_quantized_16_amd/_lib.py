@@ -36,6 +36,9 @@ QL_KERNEL_ADAMW = 12
 QL_KERNEL_ACT8 = 13
 QL_KERNEL_SWIGLU = 14
 QL_KERNEL_ACT8_GRAD = 15
+QL_KERNEL_Q4G_QUANTIZE = 16
+QL_KERNEL_Q4G_DEQUANTIZE = 17
+QL_KERNEL_Q4G_LINEAR = 18
 QL_ACT8_BLOCK = 32
 QL_NOALLOC_SCRATCH_BYTES = 96 << 20  # include/qlora_nf4.h
 QL_GRID_NF4 = 0
@@ -65,6 +68,18 @@ class QlAct8(ctypes.Structure):
     ]
 
 
+class QlQ4GWeight(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("group", ctypes.c_int32),
+        ("scale_dtype", ctypes.c_int32),
+        ("packed", ctypes.c_void_p),
+        ("scale", ctypes.c_void_p),
+        ("zero", ctypes.c_void_p),
+    ]
+
+
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
@@ -73,6 +88,7 @@ _SZ = ctypes.c_size_t
 _F = ctypes.c_float
 _WP = ctypes.POINTER(QlNf4Weight)
 _AP = ctypes.POINTER(QlAct8)
+_GP = ctypes.POINTER(QlQ4GWeight)
 
 # name -> (restype, argtypes); the exported surface of include/qlora_nf4.h
 SIGNATURES = {
@@ -112,6 +128,11 @@ SIGNATURES = {
     "qlora_linear_bwd_act8": (_I, [_WP, _AP, _P, _I64, _P, _P, _I32, _F, _P, _F, _P, _P, _P, _P, _I, _P, _SZ, _P]),
     "qlora_linear_bwd_group_act8_workspace": (_SZ, [_P, _I32, _I64, _I64, _I32]),
     "qlora_linear_bwd_group_act8": (_I, [_P, _I32, _AP, _P, _I64, _P, _P, _I32, _F, _P, _P, _P, _P, _I, _P, _SZ, _P]),
+    "q4g_packed_bytes": (_SZ, [_I64, _I64]),
+    "q4g_num_groups": (_I64, [_I64, _I64, _I32]),
+    "q4g_quantize": (_I, [_P, _I, _I64, _I64, _I32, _P, _P, _I, _P, _P]),
+    "q4g_dequantize": (_I, [_GP, _P, _I, _P]),
+    "q4g_linear_fwd": (_I, [_GP, _P, _I64, _P, _P]),
     "qlora_paged_adamw_workspace": (_SZ, [_I64]),
     "qlora_paged_adamw": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _F, _F, _F, _F, _F, _P, _SZ, _P, _P]),
     "qlora_status_string": (ctypes.c_char_p, [_I]),

@@ -1219,6 +1219,85 @@ int qlora_linear_bwd_group_act8(const ql_nf4_weight* const* w, int32_t nw, const
 
 }  // extern "C"
 
+// ---- 4-bit weights with group scales ---------------------------------------
+namespace {
+
+int check_q4g_shape(int64_t rows, int64_t cols, int32_t group, int scale_dtype) {
+    if (rows <= 0 || cols <= 0) return set_error(QL_ERR_SHAPE, "shape %lld x %lld", (long long)rows, (long long)cols);
+    if (cols % 8 != 0) return set_error(QL_ERR_SHAPE, "K = %lld is not a multiple of 8", (long long)cols);
+    if (group != 32 && group != 64 && group != 128) return set_error(QL_ERR_UNSUPPORTED, "group %d (32, 64 or 128)", group);
+    if (scale_dtype != QL_F32 && scale_dtype != QL_BF16) return set_error(QL_ERR_UNSUPPORTED, "scale dtype %d", scale_dtype);
+    // a grid holds fewer than 2^32 threads: 32 a row in the linear kernel, one per eight values in the others
+    if (cols > (int64_t{1} << 33) || rows > (int64_t{1} << 33) / (ceil_div(cols, 128) * 128))
+        return set_error(QL_ERR_SHAPE, "shape %lld x %lld too large", (long long)rows, (long long)cols);
+    return QL_OK;
+}
+
+int check_q4g(const ql_q4g_weight* w) {
+    if (w == nullptr) return set_error(QL_ERR_NULL, "weight descriptor is NULL");
+    int s;
+    if ((s = check_q4g_shape(w->rows, w->cols, w->group, w->scale_dtype)) != QL_OK) return s;
+    if ((s = check_ptr(w->packed, "packed")) != QL_OK) return s;
+    if ((s = check_ptr(w->scale, "scale")) != QL_OK) return s;
+    if (w->zero != nullptr && (s = check_ptr(w->zero, "zero")) != QL_OK) return s;
+    return QL_OK;
+}
+
+Q4GDev q4g_dev(const ql_q4g_weight* w) {
+    return Q4GDev{w->packed, w->scale, w->zero, w->group, w->scale_dtype == QL_F32 ? 1 : 0};
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t q4g_packed_bytes(int64_t rows, int64_t cols) {
+    if (check_q4g_shape(rows, cols, 32, QL_F32) != QL_OK) return 0;
+    return static_cast<size_t>(rows) * ceil_div(cols, 32) * 16;
+}
+
+int64_t q4g_num_groups(int64_t rows, int64_t cols, int32_t group) {
+    if (check_q4g_shape(rows, cols, group, QL_F32) != QL_OK) return 0;
+    return rows * ceil_div(cols, group);
+}
+
+int q4g_quantize(const void* W, int w_dtype, int64_t rows, int64_t cols, int32_t group, uint8_t* packed, void* scale,
+                 int scale_dtype, uint8_t* zero, void* stream) {
+    g_last_error[0] = '\0';
+    int s;
+    if ((s = check_q4g_shape(rows, cols, group, scale_dtype)) != QL_OK) return s;
+    if (w_dtype != QL_F32 && w_dtype != QL_BF16) return set_error(QL_ERR_UNSUPPORTED, "input dtype %d", w_dtype);
+    if ((s = check_ptr(W, "W")) != QL_OK) return s;
+    if ((s = check_ptr(packed, "packed")) != QL_OK) return s;
+    if ((s = check_ptr(scale, "scale")) != QL_OK) return s;
+    if (zero != nullptr && (s = check_ptr(zero, "zero")) != QL_OK) return s;
+    return launch_q4g_quantize(W, w_dtype == QL_F32, rows, cols, group, packed, scale, scale_dtype == QL_F32, zero,
+                               static_cast<hipStream_t>(stream));
+}
+
+int q4g_dequantize(const ql_q4g_weight* w, void* out, int out_dtype, void* stream) {
+    g_last_error[0] = '\0';
+    int s;
+    if ((s = check_q4g(w)) != QL_OK) return s;
+    if (out_dtype != QL_F32 && out_dtype != QL_BF16) return set_error(QL_ERR_UNSUPPORTED, "output dtype %d", out_dtype);
+    if ((s = check_ptr(out, "out")) != QL_OK) return s;
+    return launch_q4g_dequantize(q4g_dev(w), w->rows, w->cols, out, out_dtype == QL_BF16,
+                                 static_cast<hipStream_t>(stream));
+}
+
+int q4g_linear_fwd(const ql_q4g_weight* w, const uint16_t* X, int64_t T, uint16_t* Y, void* stream) {
+    g_last_error[0] = '\0';
+    int s;
+    if ((s = check_q4g(w)) != QL_OK) return s;
+    if (T < 0 || T > (int64_t{1} << 21)) return set_error(QL_ERR_SHAPE, "T = %lld", (long long)T);
+    if (T == 0) return QL_OK;
+    if ((s = check_ptr(X, "X")) != QL_OK) return s;
+    if ((s = check_ptr(Y, "Y")) != QL_OK) return s;
+    return launch_q4g_linear(q4g_dev(w), X, T, w->rows, w->cols, Y, static_cast<hipStream_t>(stream));
+}
+
+}  // extern "C"
+
 // ---- the forward without a workspace -------------------------------------
 // Scratch of qlora_linear_fwd_noalloc: device memory of the library itself,
 // one copy on every GPU the library runs on, held until the process ends.

@@ -267,6 +267,21 @@ struct Act8GradArgs {
 size_t act8_grads_part_bytes(int64_t T, int64_t C0, int64_t C1, int r);
 int launch_act8_grads(Act8GradArgs a, float* part, hipStream_t stream);
 
+// Device view of a 4-bit weight with group scales.
+struct Q4GDev {
+    const uint8_t* packed;
+    const void* scale;    // fp32 or bf16
+    const uint8_t* zero;  // null: 8 throughout
+    int group;
+    int scale_f32;
+};
+
+int launch_q4g_quantize(const void* W, bool w_f32, int64_t N, int64_t K, int group, uint8_t* packed, void* scale,
+                        bool scale_f32, uint8_t* zero, hipStream_t stream);
+int launch_q4g_dequantize(const Q4GDev& w, int64_t N, int64_t K, void* out, bool bf16_out, hipStream_t stream);
+int launch_q4g_linear(const Q4GDev& w, const uint16_t* X, int64_t T, int64_t N, int64_t K, uint16_t* Y,
+                      hipStream_t stream);
+
 // AdamW step (fp32 state). paged: m and v are pinned host memory and pass
 // through ws (adamw_page_ws_bytes(n) bytes of device memory) in chunks,
 // copied on copy_stream (null or stream itself: everything on stream).

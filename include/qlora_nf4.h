@@ -590,6 +590,76 @@ int qlora_linear_bwd_group_act8(const ql_nf4_weight* const* w, int32_t nw, const
                                 float* const* dB, int accumulate, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * 4-bit weights with group scales: a weight for serving, e.g. the bf16 weight
+ * qlora_merge gives. W [rows, cols] (cols a multiple of 8) is cut along its
+ * rows into groups of `group` values (32, 64 or 128; the last of a row may be
+ * shorter); a value is held as a code q in 0..15 and stands for
+ * w' = s (q - z), s and z its group's scale and zero point.
+ *
+ *   packed  [rows, 16 ceil(cols/32)] bytes: element e of a row in byte e/2,
+ *           high nibble for even e (the padding of a row is never used)
+ *   scale   [rows, ceil(cols/group)] bf16 or fp32 (scale_dtype)
+ *   zero    [rows, ceil(cols/group)] u8 in 0..15, or NULL: 8 throughout
+ *
+ * The struct is host memory; its pointers are device pointers, 16-byte
+ * aligned.
+ */
+typedef struct ql_q4g_weight {
+    int64_t rows;
+    int64_t cols;
+    int32_t group;
+    int32_t scale_dtype; /* QL_BF16 or QL_F32 */
+    const uint8_t* packed;
+    const void* scale;
+    const uint8_t* zero;
+} ql_q4g_weight;
+
+/* Bytes of the packed codes; number of groups (= scales = zero points). 0 for
+ * invalid sizes. */
+size_t q4g_packed_bytes(int64_t rows, int64_t cols);
+int64_t q4g_num_groups(int64_t rows, int64_t cols, int32_t group);
+
+/*
+ * q4g_quantize — round a weight to 4 bits with group scales, nearest value.
+ *
+ *   W     [rows, cols] row-major, fp32 (w_dtype QL_F32) or bf16 (QL_BF16)
+ *   packed, scale, zero  out, as in ql_q4g_weight; zero NULL: symmetric
+ *
+ * With zero points: lo = min(0, min w), hi = max(0, max w) over the group,
+ * s = fl32(fl32(hi - lo) / 15) rounded to scale_dtype, z = rint(fl32(-lo / s))
+ * clamped to 15. Symmetric: s = fl32(max|w| / 7) rounded, z = 8. A code is
+ * rint(fl32(w / s)) + z clamped to 0..15 (rint: nearest, ties to even). A
+ * group whose s is under 2^-126 is held as zeros (s = 0, q = z = 8). The
+ * padding of a row is written as zero. Inputs must be finite, hi - lo too.
+ * Errors: QL_ERR_NULL, QL_ERR_SHAPE (rows or cols <= 0, cols not a multiple
+ * of 8, more than 2^33 values with cols rounded up to 128), QL_ERR_UNSUPPORTED
+ * (group, dtypes), QL_ERR_ALIGN, QL_ERR_HIP.
+ */
+int q4g_quantize(const void* W, int w_dtype, int64_t rows, int64_t cols, int32_t group, uint8_t* packed,
+                 void* scale, int scale_dtype, uint8_t* zero, void* stream);
+
+/*
+ * q4g_dequantize — out [rows, cols] = fl32(s (q - z)), fp32 or rounded to
+ * bf16 (out_dtype). Errors: as q4g_quantize.
+ */
+int q4g_dequantize(const ql_q4g_weight* w, void* out, int out_dtype, void* stream);
+
+/*
+ * q4g_linear_fwd — Y = X W'^T on a 4-bit weight with group scales.
+ *
+ *   X  [T, cols] bf16;  Y  out [T, rows] bf16
+ *
+ * The codes enter the matrix product as integers and each group's sums are
+ * scaled in fp32, so W' is not rounded; sums are fp32, Y is rounded once. Made
+ * for decoding: up to 64 tokens read the weight once, more tokens take it in
+ * passes of 64. Any T and rows, cols a multiple of 8. An infinite or NaN x
+ * gives the infinities and NaN of the sum of x s (q - z). T == 0 is a no-op.
+ * Y must not alias an input.
+ * Errors: as q4g_quantize, QL_ERR_SHAPE also for T < 0 or T > 2^21.
+ */
+int q4g_linear_fwd(const ql_q4g_weight* w, const uint16_t* X, int64_t T, uint16_t* Y, void* stream);
+
+/*
  * qlora_paged_adamw — one AdamW step of the trained adapter parameters with
  * 32-bit optimizer state that lives in device memory or, paged out, in host
  * memory ([apxml], the paged-optimizer paragraph: optimizer state moves
@@ -668,7 +738,10 @@ const char* qlora_last_error(void);
 #define QL_KERNEL_ACT8 13
 #define QL_KERNEL_SWIGLU 14
 #define QL_KERNEL_ACT8_GRAD 15
-#define QL_KERNEL_COUNT 16
+#define QL_KERNEL_Q4G_QUANTIZE 16
+#define QL_KERNEL_Q4G_DEQUANTIZE 17
+#define QL_KERNEL_Q4G_LINEAR 18
+#define QL_KERNEL_COUNT 19
 int qlora_timer_arm(int kernel_id);
 int qlora_timer_read(int kernel_id, int64_t* launches, double* total_ms);
 int qlora_timer_disarm(int kernel_id);

@@ -1228,7 +1228,8 @@ int check_q4g_shape(int64_t rows, int64_t cols, int32_t group, int scale_dtype) 
     if (group != 32 && group != 64 && group != 128) return set_error(QL_ERR_UNSUPPORTED, "group %d (32, 64 or 128)", group);
     if (scale_dtype != QL_F32 && scale_dtype != QL_BF16) return set_error(QL_ERR_UNSUPPORTED, "scale dtype %d", scale_dtype);
     // a grid holds fewer than 2^32 threads: 32 a row in the linear kernel, one per eight values in the others
-    if (cols > (int64_t{1} << 33) || rows > (int64_t{1} << 33) / (ceil_div(cols, 128) * 128))
+    // (columns: 64 rows of codes and of x are reached with 32-bit offsets)
+    if (cols > (int64_t{1} << 24) || rows > (int64_t{1} << 33) / (ceil_div(cols, 128) * 128))
         return set_error(QL_ERR_SHAPE, "shape %lld x %lld too large", (long long)rows, (long long)cols);
     return QL_OK;
 }

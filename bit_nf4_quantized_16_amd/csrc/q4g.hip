@@ -12,6 +12,7 @@
 #include "common.h"
 #include "internal.h"
 #include "mm_common.h"
+#include "proj_dma.h"
 
 namespace qlnf4 {
 
@@ -153,25 +154,30 @@ __global__ __launch_bounds__(kThreads) void q4g_dequantize_kernel(Q4GDev w, int6
 // and first binade are one linear range), which the scaled conversion brings
 // to bf16 q, two values an instruction.
 //
-// A workgroup of eight waves owns 16 RT rows and 16 TT tokens; wave w takes
-// the 128-wide chunks w, w + 8, ... of K. In a chunk, lane (i = l % 16,
-// g = l / 16) loads 16 bytes of row i's codes (32 values at 32 g) and the
-// matching pieces of token i; x is the MFMA's first operand (its rows the
-// tokens), the codes the second (its columns the weight's rows), so a lane's
-// four sums are tokens 4 g .. 4 g + 3 of row i, and row i's scale is the
-// lane's own. For groups under 128 the 16 bytes are transposed over the four
-// lane groups (four lane swaps), so that MFMA m covers values 32 m .. + 31.
-// sum_k x comes from one more MFMA with ones, shared by the row tiles. The
-// waves' sums are added in order through LDS.
+// A workgroup owns 16 RT rows; its waves split K (each a contiguous run of
+// 128-wide chunks), so that every wave streams codes of its own. In a chunk,
+// lane (i = l % 16, g = l / 16) loads 16 bytes of row i's codes (values
+// 32 g .. 32 g + 31), which four lane swaps transpose over the lane groups: MFMA
+// m then covers values 32 m .. 32 m + 31, never more than one group of any
+// size. x is the MFMA's first operand (its rows the tokens), the codes the
+// second (its columns the weight's rows): a lane's sums are tokens of row i,
+// whose scale is the lane's own. sum_k x comes from one more MFMA with ones.
+// The waves' sums are added in order through LDS.
+//
+// What bounds it: at one token HBM and the time from launch to the last
+// wave's first bytes. Loads that touch one line per row cost as much as the
+// row's 64 bytes of codes, so nothing but the codes is loaded that way: scales
+// and zero points come in once, row by row, and stay in LDS (loaded per chunk
+// they took 4096 x 4096 from 4.9 to 6.0 us and 22016 x 8192 from 25 to 46 us),
+// and x comes in whole lines, to the operands through LDS. Straight-line code
+// costs fetches: four chunks in flight measured slower than two.
 //
 // Where a result is not finite (an infinite or NaN x, or sums that overflow
 // only because q and z are apart), it is formed again value by value as
 // x s (q - z): the formula's infinities, not the difference of two.
 // ---------------------------------------------------------------------------
-constexpr int kWaves = 8;
-
 template <bool SF32>
-__device__ __attribute__((noinline)) float q4g_dot(const Q4GDev& w, const uint16_t* x, int64_t n, int64_t K) {
+__device__ __forceinline__ float q4g_dot(const Q4GDev& w, const uint16_t* x, int64_t n, int64_t K) {
     float y = 0.0f;
     const int64_t ng = ceil_div(K, w.group), rowbytes = ceil_div(K, 32) * 16;
     for (int64_t k = 0; k < K; ++k) {
@@ -184,8 +190,20 @@ __device__ __attribute__((noinline)) float q4g_dot(const Q4GDev& w, const uint16
     return y;
 }
 
-// Eight codes (one packed word) -> eight bf16 integers in the order of k.
+// Eight codes (one packed word) -> eight bf16 integers, even elements before
+// odd ones (x_slot_order puts x in the same order).
 __device__ __forceinline__ bf16x8_t q4g_operand(uint32_t c) {
+    const uint32_t hi = (c >> 4) & 0x0F0F0F0Fu, lo = c & 0x0F0F0F0Fu;
+    uint4 r;
+    r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, false));
+    r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, true));
+    r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, false));
+    r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, true));
+    return as_bf16x8(r);
+}
+
+// The same in the order of k.
+__device__ __forceinline__ bf16x8_t q4g_operand_ordered(uint32_t c) {
     const uint32_t hi = (c >> 4) & 0x0F0F0F0Fu, lo = c & 0x0F0F0F0Fu;
     const uint32_t a = __builtin_amdgcn_perm(lo, hi, 0x05010400u);  // e0 e1 e2 e3
     const uint32_t b = __builtin_amdgcn_perm(lo, hi, 0x07030602u);  // e4 e5 e6 e7
@@ -197,55 +215,315 @@ __device__ __forceinline__ bf16x8_t q4g_operand(uint32_t c) {
     return as_bf16x8(r);
 }
 
+// s_waitcnt lgkmcnt(0): the wave's LDS reads have returned.
+__device__ __forceinline__ void wait_lgkmcnt0() { __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4) | (0 << 8)); }
+
+// 16 bytes a lane straight to LDS: lane l's land at dst + 16 l (dst the same
+// for the wave).
+__device__ __forceinline__ void load_lds16(const uint8_t* src, uint8_t* dst) {
+    __builtin_amdgcn_global_load_lds(src, (QL_LDS_AS void*)dst, 16, 0, 0);
+}
+
 struct Q4GLinearArgs {
     Q4GDev w;
     const uint16_t* X;
     int64_t T, N, K;
     uint16_t* Y;
+    int64_t slice;     // set by the launcher: values of a row whose constants are in LDS at a time
+    int slice_groups;  // their groups
 };
 
-// One chunk's operands of a lane.
-template <int RT, int TT>
+// One chunk's operands of a lane, as loaded.
+template <int RT, int TX>
 struct Q4GStage {
     uint4 c[RT];
-    uint4 x[TT][4];
-    float s[RT];
-    uint32_t z[RT];
+    uint4 x[TX];
 };
 
-template <int RT, int TT, int GL, bool SF32>
-__global__ __launch_bounds__(64 * kWaves) void q4g_linear_kernel(Q4GLinearArgs p) {
-    constexpr int D = 2;             // chunks in flight
-    constexpr int NG = 128 >> GL;    // groups of a chunk
-    constexpr int MG = 4 / NG;       // MFMA steps of a group
-    __shared__ float red[kWaves][TT][16][16];
+// Words of LDS that a row's scales and zero points take: an odd number, so
+// that 16 rows of a column fall into different banks.
+__host__ __device__ inline int q4g_row_words(int groups, bool scale_f32) { return (scale_f32 ? 2 * groups : groups) | 1; }
+
+// Scales and zero points of a slice (groups g0 .. of the workgroup's rows)
+// into LDS, a row's at szrow words from the last row's: bf16 scales and zero
+// points as one word, fp32 scales as two. A wave takes rows wave, wave + NW,
+// ... and 64 groups at a time; the loads of eight such pieces are issued
+// together, since each round trip to memory costs about as long as the
+// product itself.
+template <int RPW, int NW, bool SF32>
+__device__ __forceinline__ void q4g_stage_constants(const Q4GLinearArgs& p, uint32_t* sz, int szrow, int64_t n0, int nrows,
+                                                    int g0, int ng, int wave, int lane) {
+    using Scale = std::conditional_t<SF32, uint32_t, uint16_t>;
+    constexpr int U = 8;
+    const bool has_zero = p.w.zero != nullptr;
+    const Scale* const sp = static_cast<const Scale*>(p.w.scale) + n0 * ng + g0;
+    const uint8_t* const zp = (has_zero ? p.w.zero : p.w.packed) + n0 * ng + g0;  // without: a byte read and not used
+    const int gcnt = std::min(p.slice_groups, ng - g0);
+    const int pieces = RPW * ((p.slice_groups + 63) / 64);
+    for (int i = 0; i < pieces; i += U) {
+        uint32_t s[U], z[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int row = wave + NW * ((i + u) % RPW), c = lane + 64 * ((i + u) / RPW);
+            const uint32_t at = static_cast<uint32_t>(std::min(row, nrows - 1)) * static_cast<uint32_t>(ng) +
+                                static_cast<uint32_t>(std::min(c, gcnt - 1));
+            s[u] = sp[at];
+            z[u] = zp[at];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int row = wave + NW * ((i + u) % RPW), c = lane + 64 * ((i + u) / RPW);
+            if (i + u < pieces && c < p.slice_groups) {
+                const uint32_t zz = has_zero ? z[u] : 8u;
+                if constexpr (SF32) {
+                    sz[row * szrow + 2 * c] = s[u];
+                    sz[row * szrow + 2 * c + 1] = zz;
+                } else {
+                    sz[row * szrow + c] = s[u] << 16 | zz;
+                }
+            }
+        }
+    }
+}
+
+template <int RT, int TX, int D, int GL, bool SF32>
+__global__ __launch_bounds__(512) void q4g_linear_kernel(Q4GLinearArgs p) {
+    constexpr int NG = 128 >> GL;  // groups of a chunk
+    constexpr int MG = 4 / NG;     // MFMA steps of a group
+    constexpr int NW = 8;
+    constexpr int kSlot = 1024 * TX;  // x of a chunk; the wave's sums take its place at the end
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int li = lane & 15, g = lane >> 4;
+    const int64_t N = p.N, K = p.K;
+    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16 * RT;
+    const int rowbytes = static_cast<int>(ceil_div(K, 32)) * 16, ng = static_cast<int>(ceil_div(K, int64_t{1} << GL));
+    const int nrows = static_cast<int>(std::min<int64_t>(16 * RT, N - n0)), ntok = static_cast<int>(p.T);
+    uint4* const slot = reinterpret_cast<uint4*>(lds + wave * kSlot);
+    uint32_t* const sz = reinterpret_cast<uint32_t*>(lds + NW * kSlot);
+    const int szrow = q4g_row_words(p.slice_groups, SF32);
+
+    // Addresses: a base that is the same for the wave and a 32-bit offset of
+    // the lane. Rows past N and tokens past T read the last one.
+    const uint8_t* const cbase = p.w.packed + n0 * rowbytes;
+    const uint8_t* const xbase = reinterpret_cast<const uint8_t*>(p.X);
+    // The chunk that K ends in reads back from the end of a row instead.
+    const int last = static_cast<int>(ceil_div(K, 128)) - 1;
+    const bool ragged = K % 128 != 0;
+    const int cback = std::max(0, 64 * last + 16 * g + 16 - rowbytes);
+    const int xback = std::max(0, 256 * last + 16 * li + 16 - static_cast<int>(2 * K));
+    uint32_t coff[RT], xoff[TX];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+        coff[rt] = static_cast<uint32_t>(std::min(16 * rt + li, nrows - 1)) * static_cast<uint32_t>(rowbytes) + 16 * g;
+#pragma unroll
+    for (int u = 0; u < TX; ++u)
+        xoff[u] = static_cast<uint32_t>(std::min(4 * u + g, ntok - 1)) * static_cast<uint32_t>(2 * K) + 16 * li;
+
+    auto issue = [&](Q4GStage<RT, TX>& st, int ch) {
+        const uint8_t* const cp = cbase + 64 * ch;
+        const uint8_t* const xp = xbase + 256 * ch;
+        const uint32_t cb = ch == last ? cback : 0, xb = ch == last ? xback : 0;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) st.c[rt] = *reinterpret_cast<const uint4*>(cp + (coff[rt] - cb));
+#pragma unroll
+        for (int u = 0; u < TX; ++u) st.x[u] = *reinterpret_cast<const uint4*>(xp + (xoff[u] - xb));
+    };
+
+    const bf16x8_t ones = as_bf16x8(make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u));
+    float tot[RT][TX];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int rr = 0; rr < TX; ++rr) tot[rt][rr] = 0.0f;
+
+    // piece c of token j in the wave's slot: at j 16 + (c ^ j % 16), so the 16
+    // lanes that read one piece of 16 tokens hit distinct banks
+    auto put_x = [&](Q4GStage<RT, TX>& st, int ch) {
+        if (ragged && ch == last && xback > 0) {  // nothing of x past K
+#pragma unroll
+            for (int u = 0; u < TX; ++u) st.x[u] = make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < TX; ++u) {
+            const int j = 4 * u + g;
+            slot[16 * j + (li ^ (j & 15))] = x_slot_order(st.x[u]);
+        }
+    };
+    auto xin = [&](int m) {
+        const int j = std::min((li >> 2) * TX + std::min(li & 3, TX - 1), ntok - 1);
+        return as_bf16x8(slot[16 * j + ((4 * m + g) ^ (j & 15))]);
+    };
+
+    auto consume = [&](Q4GStage<RT, TX>& st, int ch, int ch0) {
+        put_x(st, ch);
+        wave_lds_sync();
+        uint32_t cw[RT][4];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            cw[rt][0] = st.c[rt].x, cw[rt][1] = st.c[rt].y, cw[rt][2] = st.c[rt].z, cw[rt][3] = st.c[rt].w;
+            // word m of lane group g <-> word g of lane group m: MFMA m then
+            // covers values 32 m .. 32 m + 31 of the chunk
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const auto sw = __builtin_amdgcn_permlane32_swap(cw[rt][q], cw[rt][q + 2], false, false);
+                cw[rt][q] = sw[0], cw[rt][q + 2] = sw[1];
+            }
+#pragma unroll
+            for (int q = 0; q < 4; q += 2) {
+                const auto sw = __builtin_amdgcn_permlane16_swap(cw[rt][q], cw[rt][q + 1], false, false);
+                cw[rt][q] = sw[0], cw[rt][q + 1] = sw[1];
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < NG; ++q) {
+            f32x4 acc[RT], xs = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) acc[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int mm = 0; mm < MG; ++mm) {
+                const int m = q * MG + mm;
+                const bf16x8_t xv = xin(m);
+                xs = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, ones, xs, 0, 0, 0);
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+                    acc[rt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, q4g_operand(cw[rt][m]), acc[rt], 0, 0, 0);
+            }
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                // the row's scale and zero point (past the last group x is zero)
+                const uint32_t* const e =
+                    sz + (16 * rt + li) * szrow + (SF32 ? 2 : 1) * std::min((ch - ch0) * NG + q, p.slice_groups - 1);
+                const float s = __uint_as_float(SF32 ? e[0] : e[0] & 0xFFFF0000u);
+                const float z = static_cast<float>((SF32 ? e[1] : e[0]) & 0xFFu);
+#pragma unroll
+                for (int rr = 0; rr < TX; ++rr)
+                    tot[rt][rr] = __builtin_fmaf(s, __builtin_fmaf(-z, xs[rr], acc[rt][rr]), tot[rt][rr]);
+            }
+        }
+        wave_lds_sync();  // the slot has been read
+    };
+
+    Q4GStage<RT, TX> ring[D];
+    const int nch = static_cast<int>(ceil_div(K, 128)), sch = static_cast<int>(p.slice / 128);
+    for (int ch0 = 0; ch0 < nch; ch0 += sch) {
+        // this slice's chunks, a contiguous run of them per wave
+        const int cnt = std::min(sch, nch - ch0);
+        const int first = ch0 + cnt * wave / NW, mine = ch0 + cnt * (wave + 1) / NW - first;
+        auto at = [&](int k) { return first + std::min(k, std::max(mine - 1, 0)); };
+#pragma unroll
+        for (int q = 0; q < D; ++q) issue(ring[q], at(q));
+        __builtin_amdgcn_sched_barrier(0);
+        // scales and zero points of the slice, row by row
+        if (ch0 > 0) __syncthreads();
+        q4g_stage_constants<16 * RT / NW, NW, SF32>(p, sz, szrow, n0, nrows, ch0 << (7 - GL), ng, wave, lane);
+        __syncthreads();
+        for (int k0 = 0; k0 < mine; k0 += D) {
+#pragma unroll
+            for (int q = 0; q < D; ++q) {
+                if (k0 + q < mine) consume(ring[q], first + k0 + q, ch0);
+                __builtin_amdgcn_sched_barrier(0);
+                issue(ring[q], at(k0 + q + D));
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    }
+
+    // the waves' sums through LDS, added in order
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        __syncthreads();
+        float* const red = reinterpret_cast<float*>(slot);
+#pragma unroll
+        for (int rr = 0; rr < TX; ++rr) red[16 * (TX * g + rr) + li] = tot[rt][rr];
+        __syncthreads();
+        for (int e = tid; e < 64 * TX; e += 64 * NW) {
+            const int tl = e >> 4, nl = 16 * rt + (e & 15);
+            if (tl >= ntok || nl >= nrows) continue;
+            float y = 0.0f;
+#pragma unroll
+            for (int ww = 0; ww < NW; ++ww) y += reinterpret_cast<const float*>(lds + ww * kSlot)[e];
+            const int64_t n = n0 + nl;
+            if (!(fabsf(y) < __builtin_inff())) y = q4g_dot<SF32>(p.w, p.X + tl * K, n, K);
+            p.Y[tl * N + n] = to_bf16_bits(y);
+        }
+    }
+}
+
+// The same product for more tokens: x, 4 KiB per 16 tokens and chunk, goes
+// straight from memory to the wave's LDS slot (global_load_lds), so that it
+// takes no registers on the way, and every x operand serves RT row tiles. The
+// next chunk's codes load while a chunk is multiplied, its x once the slot has
+// been read; the SIMD's other wave works meanwhile.
+template <int RT, int TT, int NW, int GL, bool SF32>
+__global__ __launch_bounds__(64 * NW) void q4g_linear_wide_kernel(Q4GLinearArgs p) {
+    constexpr int NG = 128 >> GL, MG = 4 / NG;
+    constexpr int kSlot = 4096 * TT;
+    // z sum_k x: a multiply-add per sum and group on the sums of x (one MFMA
+    // with ones a step, shared by the row tiles), or, where groups are short,
+    // one more MFMA per row tile with -z as the operand
+    constexpr bool kZeroOperand = NG > 1;
+    const bool has_zero = p.w.zero != nullptr;
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int li = lane & 15, g = lane >> 4;
     const int64_t N = p.N, K = p.K, T = p.T;
     const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16 * RT, t0 = static_cast<int64_t>(blockIdx.y) * 16 * TT;
-    const int64_t nch = ceil_div(K, 128), rowbytes = ceil_div(K, 32) * 16, ng = ceil_div(K, int64_t{1} << GL);
-    const bool has_zero = p.w.zero != nullptr;
+    const int rowbytes = static_cast<int>(ceil_div(K, 32)) * 16, ng = static_cast<int>(ceil_div(K, int64_t{1} << GL));
+    const int nrows = static_cast<int>(std::min<int64_t>(16 * RT, N - n0)), ntok = static_cast<int>(std::min<int64_t>(16 * TT, T - t0));
+    uint8_t* const slot = lds + wave * kSlot;
+    uint32_t* const sz = reinterpret_cast<uint32_t*>(lds + NW * kSlot);
+    const int szrow = q4g_row_words(p.slice_groups, SF32);
 
-    auto piece = [&](int m) { return GL == 7 ? 4 * g + m : 4 * m + g; };  // eight values of x
-    auto issue = [&](Q4GStage<RT, TT>& st, int64_t ch) {
-        ch = std::min(ch, nch - 1);
+    const uint8_t* const cbase = p.w.packed + n0 * rowbytes;
+    const uint8_t* const xbase = reinterpret_cast<const uint8_t*>(p.X + t0 * K);
+    const int last = static_cast<int>(ceil_div(K, 128)) - 1;
+    const bool ragged = K % 128 != 0;
+    const int cback = std::max(0, 64 * last + 16 * g + 16 - rowbytes);
+    uint32_t coff[RT];
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            const int64_t row = std::min<int64_t>(n0 + 16 * rt + li, N - 1);
-            st.c[rt] = *reinterpret_cast<const uint4*>(p.w.packed + row * rowbytes +
-                                                       std::min<int64_t>(64 * ch + 16 * g, rowbytes - 16));
-            const int64_t gi = row * ng + std::min<int64_t>(ch * NG + (g * NG) / 4, ng - 1);
-            st.s[rt] = load_scale<SF32>(p.w.scale, gi);
-            st.z[rt] = has_zero ? p.w.zero[gi] : 8;
+    for (int rt = 0; rt < RT; ++rt)
+        coff[rt] = static_cast<uint32_t>(std::min(16 * rt + li, nrows - 1)) * static_cast<uint32_t>(rowbytes) + 16 * g;
+
+    auto load_codes = [&](uint4 (&c)[RT], int ch) {
+        const uint8_t* const cp = cbase + 64 * ch;
+        const uint32_t cb = ch == last ? cback : 0;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) c[rt] = *reinterpret_cast<const uint4*>(cp + (coff[rt] - cb));
+    };
+    // load u takes tokens 4 u .. 4 u + 3; the lane's 16 bytes land at its own
+    // place, so it fetches the piece that belongs there: position c of token j
+    // holds piece c ^ j % 16
+    uint32_t xoff[4 * TT];
+#pragma unroll
+    for (int u = 0; u < 4 * TT; ++u)
+        xoff[u] = static_cast<uint32_t>(std::min(4 * u + g, ntok - 1)) * static_cast<uint32_t>(2 * K) + 16 * (li ^ ((4 * u + g) & 15));
+    auto load_x = [&](int ch) {
+        const uint8_t* const xp = xbase + 256 * ch;
+        if (ragged && ch == last) {
+            const int most = static_cast<int>(2 * K) - 256 * ch - 16;  // the last piece that a row has
+#pragma unroll
+            for (int u = 0; u < 4 * TT; ++u)
+                load_lds16(xp + (xoff[u] - std::max(16 * (li ^ ((4 * u + g) & 15)) - most, 0)), slot + 1024 * u);
+        } else {
+#pragma unroll
+            for (int u = 0; u < 4 * TT; ++u) load_lds16(xp + xoff[u], slot + 1024 * u);
         }
+    };
+    // the chunk that K ends in: x from K on is zero
+    auto clear_past = [&]() {
 #pragma unroll
-        for (int tt = 0; tt < TT; ++tt) {
-            const uint16_t* xr = p.X + std::min<int64_t>(t0 + 16 * tt + li, T - 1) * K;
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-                st.x[tt][m] = *reinterpret_cast<const uint4*>(xr + std::min<int64_t>(128 * ch + 8 * piece(m), K - 8));
+        for (int u = 0; u < 4 * TT; ++u) {
+            const int j = 4 * u + g;
+            if (128 * static_cast<int64_t>(last) + 8 * (li ^ (j & 15)) >= K)
+                *reinterpret_cast<uint4*>(slot + 1024 * u + 16 * lane) = make_uint4(0, 0, 0, 0);
         }
+    };
+    auto xin = [&](int tt, int m) {
+        const int j = 16 * tt + li;
+        return as_bf16x8(*reinterpret_cast<const uint4*>(slot + 256 * j + 16 * ((4 * m + g) ^ li)));
     };
 
     const bf16x8_t ones = as_bf16x8(make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u));
@@ -255,81 +533,69 @@ __global__ __launch_bounds__(64 * kWaves) void q4g_linear_kernel(Q4GLinearArgs p
 #pragma unroll
         for (int tt = 0; tt < TT; ++tt) tot[rt][tt] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    auto consume = [&](Q4GStage<RT, TT>& st, int64_t ch) {
-        if (128 * ch + 128 > K) {  // the last chunk: nothing past K
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-                if (128 * ch + 8 * piece(m) >= K) {
-#pragma unroll
-                    for (int tt = 0; tt < TT; ++tt) st.x[tt][m] = make_uint4(0, 0, 0, 0);
-                }
-        }
+    auto multiply = [&](const uint4 (&c)[RT], int gi0) {
         uint32_t cw[RT][4];
-        float s[RT][NG], z[RT][NG];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-            cw[rt][0] = st.c[rt].x, cw[rt][1] = st.c[rt].y, cw[rt][2] = st.c[rt].z, cw[rt][3] = st.c[rt].w;
-            if constexpr (GL == 7) {
-                s[rt][0] = st.s[rt];
-                z[rt][0] = static_cast<float>(st.z[rt]);
-            } else {
-                // word m of lane group g <-> word g of lane group m
+            cw[rt][0] = c[rt].x, cw[rt][1] = c[rt].y, cw[rt][2] = c[rt].z, cw[rt][3] = c[rt].w;
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const auto sw = __builtin_amdgcn_permlane32_swap(cw[rt][q], cw[rt][q + 2], false, false);
-                    cw[rt][q] = sw[0], cw[rt][q + 2] = sw[1];
-                }
+            for (int q = 0; q < 2; ++q) {
+                const auto sw = __builtin_amdgcn_permlane32_swap(cw[rt][q], cw[rt][q + 2], false, false);
+                cw[rt][q] = sw[0], cw[rt][q + 2] = sw[1];
+            }
 #pragma unroll
-                for (int q = 0; q < 4; q += 2) {
-                    const auto sw = __builtin_amdgcn_permlane16_swap(cw[rt][q], cw[rt][q + 1], false, false);
-                    cw[rt][q] = sw[0], cw[rt][q + 1] = sw[1];
-                }
-                // lane group g holds the constants of group g NG / 4: hand each to all
-                const uint32_t sb = __float_as_uint(st.s[rt]), zb = st.z[rt];
-                const auto s2 = __builtin_amdgcn_permlane32_swap(sb, sb, false, false);
-                const auto z2 = __builtin_amdgcn_permlane32_swap(zb, zb, false, false);
-                if constexpr (NG == 2) {
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        s[rt][q] = __uint_as_float(s2[q]);
-                        z[rt][q] = static_cast<float>(z2[q]);
-                    }
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const auto s4 = __builtin_amdgcn_permlane16_swap(s2[q], s2[q], false, false);
-                        const auto z4 = __builtin_amdgcn_permlane16_swap(z2[q], z2[q], false, false);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            s[rt][2 * q + h] = __uint_as_float(s4[h]);
-                            z[rt][2 * q + h] = static_cast<float>(z4[h]);
-                        }
-                    }
-                }
+            for (int q = 0; q < 4; q += 2) {
+                const auto sw = __builtin_amdgcn_permlane16_swap(cw[rt][q], cw[rt][q + 1], false, false);
+                cw[rt][q] = sw[0], cw[rt][q + 1] = sw[1];
             }
         }
 #pragma unroll
         for (int q = 0; q < NG; ++q) {
+            // the rows' scales and zero points (past the last group x is zero)
+            float sv[RT];
+            uint32_t zv[RT];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const uint32_t* const e = sz + (16 * rt + li) * szrow + (SF32 ? 2 : 1) * std::min(gi0 + q, p.slice_groups - 1);
+                sv[rt] = __uint_as_float(SF32 ? e[0] : e[0] & 0xFFFF0000u);
+                zv[rt] = (SF32 ? e[1] : e[0]) & 0xFFu;
+            }
             f32x4 acc[RT][TT], xs[TT];
+            bf16x8_t zop[RT];
 #pragma unroll
-            for (int tt = 0; tt < TT; ++tt) {
-                xs[tt] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int tt = 0; tt < TT; ++tt) xs[tt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) acc[rt][tt] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+                for (int tt = 0; tt < TT; ++tt) acc[rt][tt] = f32x4{0.f, 0.f, 0.f, 0.f};
+                if constexpr (kZeroOperand) {  // -z as an operand: 8 for all, or the row's
+                    uint32_t zz = 0xC100C100u;
+                    if (has_zero) {
+                        zz = __float_as_uint(-static_cast<float>(zv[rt]));
+                        zz = __builtin_amdgcn_perm(zz, zz, 0x07060302u);
+                    }
+                    zop[rt] = as_bf16x8(make_uint4(zz, zz, zz, zz));
+                }
             }
 #pragma unroll
             for (int mm = 0; mm < MG; ++mm) {
                 const int m = q * MG + mm;
+                bf16x8_t xv[TT];
 #pragma unroll
-                for (int tt = 0; tt < TT; ++tt)
-                    xs[tt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(st.x[tt][m]), ones, xs[tt], 0, 0, 0);
+                for (int tt = 0; tt < TT; ++tt) {
+                    xv[tt] = xin(tt, m);
+                    if constexpr (!kZeroOperand)
+                        xs[tt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[tt], ones, xs[tt], 0, 0, 0);
+                }
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
-                    const bf16x8_t wv = q4g_operand(cw[rt][m]);
+                    const bf16x8_t wv = q4g_operand_ordered(cw[rt][m]);
 #pragma unroll
-                    for (int tt = 0; tt < TT; ++tt)
-                        acc[rt][tt] =
-                            __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(st.x[tt][m]), wv, acc[rt][tt], 0, 0, 0);
+                    for (int tt = 0; tt < TT; ++tt) {
+                        if constexpr (kZeroOperand)
+                            acc[rt][tt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[tt], zop[rt], acc[rt][tt], 0, 0, 0);
+                        acc[rt][tt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[tt], wv, acc[rt][tt], 0, 0, 0);
+                    }
                 }
             }
 #pragma unroll
@@ -337,54 +603,127 @@ __global__ __launch_bounds__(64 * kWaves) void q4g_linear_kernel(Q4GLinearArgs p
 #pragma unroll
                 for (int tt = 0; tt < TT; ++tt)
 #pragma unroll
-                    for (int rr = 0; rr < 4; ++rr)
-                        tot[rt][tt][rr] = __builtin_fmaf(s[rt][q], __builtin_fmaf(-z[rt][q], xs[tt][rr], acc[rt][tt][rr]),
-                                                         tot[rt][tt][rr]);
+                    for (int rr = 0; rr < 4; ++rr) {
+                        const float d = kZeroOperand ? acc[rt][tt][rr]
+                                                     : __builtin_fmaf(-static_cast<float>(zv[rt]), xs[tt][rr], acc[rt][tt][rr]);
+                        tot[rt][tt][rr] = __builtin_fmaf(sv[rt], d, tot[rt][tt][rr]);
+                    }
+            if constexpr (NG > 1 && RT * TT > 4) __builtin_amdgcn_sched_barrier(0);  // one group's sums at a time
         }
     };
 
-    const int64_t mine = wave < nch ? (nch - 1 - wave) / kWaves + 1 : 0;  // chunks of this wave
-    Q4GStage<RT, TT> ring[D];
+    const int nch = last + 1, sch = static_cast<int>(p.slice / 128);
+    for (int ch0 = 0; ch0 < nch; ch0 += sch) {
+        const int cnt = std::min(sch, nch - ch0);
+        const int first = ch0 + cnt * wave / NW, end = ch0 + cnt * (wave + 1) / NW;
+        if (ch0 > 0) __syncthreads();  // the previous slice's constants have been read
+        q4g_stage_constants<16 * RT / NW, NW, SF32>(p, sz, szrow, n0, nrows, ch0 << (7 - GL), ng, wave, lane);
+        uint4 cur[RT], nxt[RT];
+        if (first < end) {
+            load_codes(cur, first);
+            load_x(first);
+        }
+        __syncthreads();
+        for (int ch = first; ch < end; ++ch) {
+            wait_vmcnt<0>();  // x and the codes of this chunk are here
+            wave_lds_sync();
+            load_codes(nxt, std::min(ch + 1, end - 1));
+            __builtin_amdgcn_sched_barrier(0);
+            if (ragged && ch == last) {
+                clear_past();
+                wave_lds_sync();
+            }
+            multiply(cur, (ch - ch0) * NG);
+            wave_lds_sync();
+            if (ch + 1 < end) {
+                wait_lgkmcnt0();  // the slot has been read
+                load_x(ch + 1);
+            }
 #pragma unroll
-    for (int q = 0; q < D; ++q) issue(ring[q], wave + kWaves * q);
-    for (int64_t k0 = 0; k0 < mine; k0 += D) {
-#pragma unroll
-        for (int q = 0; q < D; ++q) {
-            if (k0 + q < mine) consume(ring[q], wave + kWaves * (k0 + q));
-            issue(ring[q], wave + kWaves * (k0 + q + D));
+            for (int rt = 0; rt < RT; ++rt) cur[rt] = nxt[rt];
         }
     }
 
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-        if (rt > 0) __syncthreads();
+        __syncthreads();
+        float* const red = reinterpret_cast<float*>(slot);
 #pragma unroll
         for (int tt = 0; tt < TT; ++tt)
 #pragma unroll
-            for (int rr = 0; rr < 4; ++rr) red[wave][tt][4 * g + rr][li] = tot[rt][tt][rr];
+            for (int rr = 0; rr < 4; ++rr) red[256 * tt + 16 * (4 * g + rr) + li] = tot[rt][tt][rr];
         __syncthreads();
-        for (int e = tid; e < TT * 256; e += 64 * kWaves) {
-            const int tt = e >> 8, tl = (e >> 4) & 15, nl = e & 15;
-            const int64_t t = t0 + 16 * tt + tl, n = n0 + 16 * rt + nl;
-            if (t >= T || n >= N) continue;
+        for (int e = tid; e < TT * 256; e += 64 * NW) {
+            const int tl = e >> 4, nl = 16 * rt + (e & 15);
+            if (tl >= ntok || nl >= nrows) continue;
             float y = 0.0f;
 #pragma unroll
-            for (int ww = 0; ww < kWaves; ++ww) y += red[ww][tt][tl][nl];
+            for (int ww = 0; ww < NW; ++ww) y += reinterpret_cast<const float*>(lds + ww * kSlot)[e];
+            const int64_t t = t0 + tl, n = n0 + nl;
             if (!(fabsf(y) < __builtin_inff())) y = q4g_dot<SF32>(p.w, p.X + t * K, n, K);
             p.Y[t * N + n] = to_bf16_bits(y);
         }
     }
 }
 
-template <int RT, int TT, bool SF32>
-void launch_linear(const Q4GLinearArgs& a, hipStream_t stream) {
+// Values of a row whose constants a workgroup keeps in LDS at a time: the
+// whole row where 16 RT rows of them fit the budget, else a slice of whole
+// chunks that does.
+void set_slice(Q4GLinearArgs& a, int rows, bool sf32, size_t budget) {
+    const int64_t words = static_cast<int64_t>(budget / sizeof(uint32_t)) / rows - 1;
+    const int64_t most = std::max<int64_t>((sf32 ? words / 2 : words) * a.w.group / 128 * 128, 128);
+    a.slice = std::min(ceil_div(a.K, 128) * 128, most);
+    a.slice_groups = static_cast<int>(a.slice / a.w.group);
+}
+
+// LDS may pass the 64 KiB that a launch gets unasked.
+template <typename Kernel>
+int launch_lds(Kernel kern, dim3 grid, int threads, size_t lds, const Q4GLinearArgs& a, hipStream_t stream) {
+    if (lds > 65536 && hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                           static_cast<int>(lds)) != hipSuccess)
+        return set_error(QL_ERR_HIP, "4-bit group linear: %zu bytes of LDS refused", lds);
+    hipLaunchKernelGGL(kern, grid, dim3(threads), static_cast<uint32_t>(lds), stream, a);
+    return QL_OK;
+}
+
+constexpr size_t kLdsBytes = 163840, kConstBytes = 32768;
+
+template <int RT, int TX, int D, int GL, bool SF32>
+int launch_narrow(Q4GLinearArgs a, hipStream_t stream) {
+    set_slice(a, 16 * RT, SF32, kConstBytes);
+    const size_t lds = 8 * 1024 * TX + 16 * RT * sizeof(uint32_t) * q4g_row_words(a.slice_groups, SF32);
+    return launch_lds(q4g_linear_kernel<RT, TX, D, GL, SF32>, dim3(static_cast<uint32_t>(ceil_div(a.N, 16 * RT))), 512, lds,
+                      a, stream);
+}
+
+template <int RT, int TT, int NW, int GL, bool SF32>
+int launch_wide(Q4GLinearArgs a, hipStream_t stream) {
+    constexpr size_t slots = NW * 4096 * TT;
+    set_slice(a, 16 * RT, SF32, std::min(kConstBytes, kLdsBytes - slots));
+    const size_t lds = slots + 16 * RT * sizeof(uint32_t) * q4g_row_words(a.slice_groups, SF32);
     const dim3 grid(static_cast<uint32_t>(ceil_div(a.N, 16 * RT)), static_cast<uint32_t>(ceil_div(a.T, 16 * TT)));
-    const dim3 block(64 * kWaves);
-    switch (a.w.group) {
-        case 32: hipLaunchKernelGGL((q4g_linear_kernel<RT, TT, 5, SF32>), grid, block, 0, stream, a); break;
-        case 64: hipLaunchKernelGGL((q4g_linear_kernel<RT, TT, 6, SF32>), grid, block, 0, stream, a); break;
-        default: hipLaunchKernelGGL((q4g_linear_kernel<RT, TT, 7, SF32>), grid, block, 0, stream, a); break;
-    }
+    return launch_lds(q4g_linear_wide_kernel<RT, TT, NW, GL, SF32>, grid, 64 * NW, lds, a, stream);
+}
+
+// The variant by tokens and rows. One row tile a workgroup gives the most
+// workgroups and the least code, two read x (and fetch instructions) half as
+// often; what was measured (us, one | two row tiles, groups of 128 unless said):
+//   T = 1   4096 x 4096 5.0 | 6.5, 11008 x 4096 (32) 9.5 | 11.0, 22016 x 8192 26.8 | 24.4
+//   T = 8   4096 x 4096 5.3 | 7.0, 22016 x 8192 36.9 | 28.0
+//   T = 16  4096 x 4096 5.9 | 9.5, 11008 x 4096 (64) 11.6 | 13.2, 22016 x 8192 41.4 | 31.2
+//   T = 37  4096 x 4096 9.2 | 12.9, 11008 x 4096 (32) 28.2 | 23.4
+//   T = 64  4096 x 11008 24.4 | 31.9, 11008 x 4096 29.7 | 21.9, 22016 x 8192 (64) 106 | 83
+// so two from four workgroups a CU on (1024), from two (512) for more than a
+// tile of tokens.
+template <int GL, bool SF32>
+int launch_linear_variant(const Q4GLinearArgs& a, hipStream_t stream) {
+    const bool two = ceil_div(a.N, 16) > (a.T <= 16 ? 1024 : 512);
+    if (a.T <= 4) return two ? launch_narrow<2, 1, 1, GL, SF32>(a, stream) : launch_narrow<1, 1, 2, GL, SF32>(a, stream);
+    if (a.T <= 8) return two ? launch_narrow<2, 2, 1, GL, SF32>(a, stream) : launch_narrow<1, 2, 2, GL, SF32>(a, stream);
+    if (a.T <= 16) return two ? launch_wide<2, 1, 4, GL, SF32>(a, stream) : launch_wide<1, 1, 8, GL, SF32>(a, stream);
+    if (a.T <= 32) return two ? launch_wide<2, 2, 4, GL, SF32>(a, stream) : launch_wide<1, 2, 8, GL, SF32>(a, stream);
+    if (a.T <= 48) return two ? launch_wide<2, 3, 4, GL, SF32>(a, stream) : launch_wide<1, 3, 8, GL, SF32>(a, stream);
+    return two ? launch_wide<2, 4, 4, GL, SF32>(a, stream) : launch_wide<1, 4, 8, GL, SF32>(a, stream);
 }
 
 template <bool WF32, bool SF32>
@@ -439,18 +778,16 @@ int launch_q4g_dequantize(const Q4GDev& w, int64_t N, int64_t K, void* out, bool
 
 int launch_q4g_linear(const Q4GDev& w, const uint16_t* X, int64_t T, int64_t N, int64_t K, uint16_t* Y,
                       hipStream_t stream) {
-    const Q4GLinearArgs a{w, X, T, N, K, Y};
+    const Q4GLinearArgs a{w, X, T, N, K, Y, 0, 0};
     timer_begin(QL_KERNEL_Q4G_LINEAR, stream);
-    with_flags(w.scale_f32 != 0, false, [&](auto sf, auto) {
-        constexpr bool SF32 = decltype(sf)::value;
-        if (T <= 16)
-            launch_linear<1, 1, SF32>(a, stream);
-        else if (T <= 32)
-            launch_linear<1, 2, SF32>(a, stream);
-        else
-            launch_linear<1, 4, SF32>(a, stream);
-    });
+    int s;
+    switch (w.group) {
+        case 32: s = w.scale_f32 ? launch_linear_variant<5, true>(a, stream) : launch_linear_variant<5, false>(a, stream); break;
+        case 64: s = w.scale_f32 ? launch_linear_variant<6, true>(a, stream) : launch_linear_variant<6, false>(a, stream); break;
+        default: s = w.scale_f32 ? launch_linear_variant<7, true>(a, stream) : launch_linear_variant<7, false>(a, stream); break;
+    }
     timer_end(QL_KERNEL_Q4G_LINEAR, stream);
+    if (s != QL_OK) return s;
     return check_launch("4-bit group linear");
 }
 

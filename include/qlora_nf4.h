@@ -632,7 +632,7 @@ int64_t q4g_num_groups(int64_t rows, int64_t cols, int32_t group);
  * group whose s is under 2^-126 is held as zeros (s = 0, q = z = 8). The
  * padding of a row is written as zero. Inputs must be finite, hi - lo too.
  * Errors: QL_ERR_NULL, QL_ERR_SHAPE (rows or cols <= 0, cols not a multiple
- * of 8, more than 2^33 values with cols rounded up to 128), QL_ERR_UNSUPPORTED
+ * of 8 or over 2^24, more than 2^33 values with cols rounded up to 128), QL_ERR_UNSUPPORTED
  * (group, dtypes), QL_ERR_ALIGN, QL_ERR_HIP.
  */
 int q4g_quantize(const void* W, int w_dtype, int64_t rows, int64_t cols, int32_t group, uint8_t* packed,

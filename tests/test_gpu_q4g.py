@@ -158,6 +158,55 @@ def test_non_finite_tokens(qn):
     assert np.all(np.abs(_f64(Y[7]) - want) <= np.abs(want) * 2.0 ** -8)
 
 
+@pytest.mark.parametrize("T", [2, 7])
+def test_non_finite_tokens_decode(qn, T):
+    """The same with few tokens (and one of them infinite throughout)."""
+    N, K = 40, 520
+    w, q, s, z = _quantized(qn, _weight(N, K, 12, False), 32, True, torch.float32)
+    wd = og.dequantize(q, s, z, 32).astype(np.float64)
+    X = workloads.bf16_normal((T, K), 1.0, 3)
+    clean = qn.q4g_linear_fwd(w, X.cuda()).cpu()
+    X[1] = 0.0
+    X[1, 300] = float("inf")
+    Y = qn.q4g_linear_fwd(w, X.cuda()).cpu()
+    with np.errstate(invalid="ignore"):
+        assert np.array_equal(_f64(Y[1]), np.inf * wd[:, 300], equal_nan=True)
+    rest = [t for t in range(T) if t != 1]
+    assert torch.equal(Y[rest], clean[rest])
+
+
+@pytest.mark.parametrize("T,N,K,group,sd", [
+    (1, 16500, 520, 64, torch.bfloat16),     # rows for two row tiles a workgroup, the last one ragged
+    (7, 16500, 392, 32, torch.float32),
+    (13, 16500, 264, 128, torch.bfloat16),
+    (29, 8210, 520, 32, torch.float32),
+    (45, 8210, 264, 64, torch.bfloat16),
+    (70, 8210, 392, 128, torch.float32),
+    (3, 40, 34000, 32, torch.bfloat16),      # more groups than a workgroup holds at a time
+    (3, 40, 34000, 32, torch.float32),
+    (12, 40, 34000, 64, torch.float32),
+    (50, 40, 34000, 32, torch.float32),
+    (40, 8210, 9000, 32, torch.float32),
+    (2, 16500, 9000, 32, torch.float32),
+])
+@pytest.mark.parametrize("sym", [False, True])
+def test_linear_variants(qn, T, N, K, group, sd, sym):
+    """Each variant of the kernels against the expanded weight (tested above
+    to be exact) in fp64."""
+    W = (torch.randn(N, K, device="cuda", generator=torch.Generator("cuda").manual_seed(N + K)) * 0.02)
+    w = qn.q4g_quantize(W, group=group, symmetric=sym, scale_dtype=sd)
+    X = workloads.bf16_normal((T, K), 1.0, T).cuda()
+    wd = qn.q4g_dequantize(w, torch.float32)
+    y = X.double() @ wd.double().t().contiguous()
+    z = (w.zero.double() if w.zero is not None else torch.full(w.scale.shape, 8.0, device="cuda", dtype=torch.float64))
+    at = torch.arange(K, device="cuda") // group
+    # s (q + z) |x| = (s (q - z) + 2 s z) |x|
+    mag = X.double().abs() @ (wd.double() + 2 * (w.scale.double() * z)[:, at]).t().contiguous()
+    err = (qn.q4g_linear_fwd(w, X).double() - y).abs()
+    assert bool((err <= y.abs() * 2.0 ** -8 + mag * (K + 8) * 2.0 ** -23).all())
+    assert float(err.norm()) <= 2.0 ** -8 * float(y.norm())
+
+
 def test_padding_and_memory_behind_the_arrays(qn):
     """Codes past K, rows behind the last token and behind the output do not
     matter and stay as they were."""

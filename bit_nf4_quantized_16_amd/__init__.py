@@ -395,13 +395,19 @@ def _matrix(t, name, dtype=torch.bfloat16):
     return _tensor(t, name, dtype, t.shape)
 
 
+# The handle of a device's current stream. torch's own accessor makes a Stream
+# object first: 2.8 us a call against 0.1 us, a third of a small call's time.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _launch(device, call, *args):
     """call(*args, stream) on ``device`` and its current stream."""
     if device.index == torch.cuda.current_device():
-        _check(call(*args, torch.cuda.current_stream().cuda_stream))
+        _check(call(*args, _raw_stream(device.index)))
     else:
         with torch.cuda.device(device):
-            _check(call(*args, torch.cuda.current_stream().cuda_stream))
+            _check(call(*args, _raw_stream(device.index)))
 
 
 @dataclass
@@ -420,6 +426,9 @@ class Act8:
     def descriptor(self):
         _tensor(self.codes, "codes", torch.uint8, (self.rows, self.cols))
         _tensor(self.scale, "scale", torch.uint8, (self.rows, self.cols // _lib.QL_ACT8_BLOCK), self.codes.device)
+        return self._struct()
+
+    def _struct(self):
         return _lib.QlAct8(self.rows, self.cols, self.codes.data_ptr(), self.scale.data_ptr())
 
 
@@ -435,11 +444,14 @@ def act8_quantize(X, out=None):
     multiple of 32: nearest E4M3 value under one power-of-two scale per 32
     values; NaN and infinities become NaN. ``out``: an Act8 to write into."""
     rows, cols = _matrix(X, "X").shape
-    a = _act8_empty(rows, cols, X.device) if out is None else out
-    d = a.descriptor()
-    if (a.rows, a.cols) != (rows, cols) or a.codes.device != X.device:
-        _refuse(_lib.QL_ERR_SHAPE, "out is %d x %d on %s, X %d x %d on %s"
-                % (a.rows, a.cols, a.codes.device, rows, cols, X.device))
+    if out is None:
+        a = _act8_empty(rows, cols, X.device)
+        d = a._struct()
+    else:
+        a, d = out, out.descriptor()
+        if (a.rows, a.cols) != (rows, cols) or a.codes.device != X.device:
+            _refuse(_lib.QL_ERR_SHAPE, "out is %d x %d on %s, X %d x %d on %s"
+                    % (a.rows, a.cols, a.codes.device, rows, cols, X.device))
     _launch(X.device, lib.act8_quantize, X.data_ptr(), d)
     return a
 
@@ -469,7 +481,7 @@ def swiglu_fwd(gate, up, checkpoint=True, h8=False):
     H = torch.empty_like(gate)
     acts = [_act8_empty(rows, cols, dev) if want else None for want in (checkpoint, checkpoint, h8)]
     _launch(dev, lib.qlora_swiglu_fwd, gate.data_ptr(), up.data_ptr(), rows, cols, H.data_ptr(),
-            *[a.descriptor() if a is not None else None for a in acts])
+            *[a._struct() if a is not None else None for a in acts])
     return (H, *acts)
 
 

@@ -5,19 +5,25 @@
 //
 // with M = X (8-bit checkpoint, the dropout mask applied where there is one)
 // and V = G = s dY B for dA; M = dY (bf16) and V = U for dB. V comes as fp32
-// and is not rounded: it is split into three bf16 terms v = h + m + l (each
-// the rounding of what the ones before it leave, 24 bits in all), multiplied
-// by the exact bf16 values of M and summed in fp32, so dA and dB carry fp32
-// rounding only. One grid holds both problems: workgroups [0, nblk0) take
-// 64-column blocks of the first, the rest those of the second.
+// and is not rounded: it is split into three bf16 terms v = h + m + l (8
+// significant bits each, 24 in all), multiplied by the exact bf16 values of M
+// and summed in fp32, so dA and dB carry fp32 rounding only. One grid holds
+// both problems: workgroups [0, nblk0) take column blocks of the first, the
+// rest those of the second.
 //
-// A workgroup's eight waves take 32-token chunks in turn. A wave expands its
+// The waves of a workgroup take 32-token chunks in turn. A wave expands its
 // chunk of M to bf16 in a private LDS tile and reads it back column-wise
-// (eight consecutive tokens of one column per lane: the MFMA B operand); its
-// chunk of V goes through a second tile, one term at a time, and is read the
-// same way (the A operand). With one token split the workgroup writes the
-// gradient itself (fixed-order sum of the waves); with several, fp32 partials
-// go to the workspace and a second kernel adds them in order.
+// (eight consecutive tokens of one column per lane: the MFMA B operand). The
+// next chunk's loads are issued before a chunk is multiplied and kept as they
+// come (codes, not values), so nothing waits for them until they are used.
+// V up to rank 16 is split by every workgroup for itself, through a second
+// tile, one term at a time (read like M: the A operand). Larger ranks would
+// spend most of their instructions on that (rank 64, T = 4096: 102 us), so
+// their terms are written once, by a small kernel before, in the order of the
+// A operand: 1 KiB per 32 tokens, 16 ranks and term, read in one load.
+// With one token split the workgroup writes the gradient itself (fixed-order
+// sum of the waves); with several, fp32 partials in the output's layout go to
+// the workspace and a second kernel adds them in order.
 #include <algorithm>
 
 #include "act8.h"
@@ -29,10 +35,7 @@ namespace qlnf4 {
 
 namespace {
 
-constexpr int kCols = 64;   // columns of M per workgroup
-constexpr int kRows = 32;   // tokens per MFMA step
-constexpr int kWaves = 8;
-constexpr int kLdM = kCols + 8;
+constexpr int kRows = 32;  // tokens per MFMA step
 
 // 16-bit lane masks of eight elements from their eight keep bits.
 __device__ __forceinline__ uint4 keep_mask(uint32_t bits) {
@@ -43,198 +46,355 @@ __device__ __forceinline__ uint4 keep_mask(uint32_t bits) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The next bf16 term of v and what it leaves (exact; nothing once a term is
-// infinite or NaN, so that an infinite v stays infinite).
-__device__ __forceinline__ float split_term(float& v) {
-    const float h = __uint_as_float(pack_bf16x2(v, 0.0f) << 16);
-    v = fabsf(h) < __builtin_inff() ? v - h : 0.0f;
-    return h;
+// What v's leading 8 significant bits (its top half) leave, exactly. Infinity
+// less itself would be NaN: with check it leaves nothing.
+__device__ __forceinline__ float split_rest(float v, bool check) {
+    const float rest = v - __uint_as_float(__float_as_uint(v) & 0xFFFF0000u);
+    return check && fabsf(v) == __builtin_inff() ? 0.0f : rest;
 }
 
-template <int RT>
-__global__ __launch_bounds__(64 * kWaves) void act8_grads_kernel(Act8GradArgs a) {
-    constexpr int LdV = 16 * RT + 8;
-    constexpr int kTile = kRows * (kLdM + LdV);
-    __shared__ __attribute__((aligned(16))) uint16_t sm[kWaves][kTile];
-    __shared__ float red[kWaves / 2][16][kCols];
+// Tiles of a rank of RT x 16: the columns a workgroup takes (16 CB), its
+// waves, and whether V's terms come prepared.
+template <int RT, int CB_>
+struct GradTile {
+    static constexpr int CB = CB_;
+    static constexpr bool kTerms = RT > 1;
+    static constexpr int NW = RT == 1 ? 16 : 8;
+    static constexpr int LdM = 16 * CB + 8, LdV = kTerms ? 0 : 16 * RT + 8;
+    static constexpr int kTile = kRows * (LdM + LdV);  // 16-bit words of one wave
+};
+
+// A wave's chunk of M as loaded: MI pieces of eight columns a lane (codes,
+// scale and keep byte of a checkpoint; or bf16 values).
+template <int MI, bool ACT8>
+struct GradStage {
+    uint4 m[ACT8 ? 1 : MI];
+    uint2 c[ACT8 ? MI : 1];
+    uint32_t s[ACT8 ? MI : 1];
+    uint32_t k[ACT8 ? MI : 1];
+};
+
+template <int RT, int CB_, bool ACT8>
+__device__ __forceinline__ void grads_block(const Act8GradArgs& a, const Act8GradProblem& pb, int64_t c0, uint16_t* sm) {
+    using G = GradTile<RT, CB_>;
+    constexpr bool kTerms = G::kTerms;
+    constexpr int CB = G::CB, NW = G::NW, LdM = G::LdM, LdV = G::LdV;
+    constexpr int PR = 2 * CB;        // pieces of a token's row
+    constexpr int MI = kRows * PR / 64;
+    using Stage = GradStage<MI, ACT8>;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int li = lane & 15, g = lane >> 4;
-    const bool second = static_cast<int>(blockIdx.x) >= a.nblk0;
-    const Act8GradProblem& pb = second ? a.pb[1] : a.pb[0];
     const int64_t C = pb.C;
-    const int64_t c0 = static_cast<int64_t>(second ? blockIdx.x - a.nblk0 : blockIdx.x) * kCols;
+    const int r = a.r;
     const int64_t tb = blockIdx.y * a.t_per;
     const int64_t te = std::min<int64_t>(tb + a.t_per, a.T);
-    const int r = a.r;
-    f32x4 acc[RT][4];
+    f32x4 acc[RT][CB];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-        for (int cb = 0; cb < 4; ++cb) acc[rt][cb] = f32x4{0.f, 0.f, 0.f, 0.f};
-    uint16_t* const tm = sm[wave];
-    uint16_t* const tv = sm[wave] + kRows * kLdM;
+        for (int cb = 0; cb < CB; ++cb) acc[rt][cb] = f32x4{0.f, 0.f, 0.f, 0.f};
+    uint16_t* const tm = sm + wave * G::kTile;
+    uint16_t* const tv = tm + kRows * LdM;
+    const bool masked = ACT8 && pb.keep != nullptr;
+    const uint8_t* const kp = masked ? pb.keep : static_cast<const uint8_t*>(pb.M);  // without a mask: read and not used
+    const bool quads = (r & 3) == 0;
+    constexpr int RI = 64 / PR;  // tokens of a load
 
-    // lane: row (lane / 8) + 8 i of the chunk, columns c0 + 8 (lane % 8) ..
-    const int64_t c = c0 + 8 * (lane & 7);
-    auto load_m = [&](int64_t t, uint4 (&v)[4]) {
+    // A base that is the same for the wave and an offset of the lane. Out of
+    // range (tokens from te on, columns from C on, ranks from r on) the nearest
+    // element in range is read, and zeroed or left out when it is used.
+    const int64_t col = std::min<int64_t>(c0 + 8 * (lane % PR), C - 8), moff = (lane / PR) * C + col;
+    auto load_m = [&](Stage& st, int64_t t) {
+        const bool tail = t + kRows > te;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t row = t + (lane >> 3) + 8 * i;
-            v[i] = make_uint4(0, 0, 0, 0);
-            if (row < te && c < C) {
-                const int64_t e = row * C + c;
-                if (pb.scale8 != nullptr) {
-                    v[i] = act8_decode8(*reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(pb.M) + e),
-                                        pb.scale8[e / kAct8Block]);
-                    if (pb.keep != nullptr) {
-                        const uint4 m = keep_mask(pb.keep[e / 8]);
-                        v[i] = make_uint4(v[i].x & m.x, v[i].y & m.y, v[i].z & m.z, v[i].w & m.w);
-                    }
-                } else {
-                    v[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(pb.M) + e);
-                }
+        for (int i = 0; i < MI; ++i) {
+            int64_t at = (t + RI * i) * C + moff;
+            if (tail) at = std::min<int64_t>(t + RI * i + lane / PR, te - 1) * C + col;
+            if constexpr (ACT8) {
+                st.c[i] = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(pb.M) + at);
+                st.s[i] = pb.scale8[at / kAct8Block];
+                st.k[i] = kp[at / 8];
+            } else {
+                st.m[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(pb.M) + at);
             }
         }
     };
-    // V of the chunk: quads of ranks, 4 RT a token (zero past the rank and the tokens)
-    auto load_v = [&](int64_t t, float (&v)[2 * RT][4]) {
+    // V of the chunk: quads of ranks, 4 RT a token
+    auto load_v = [&](float (&v)[2 * RT][4], int64_t t) {
+        const int left = static_cast<int>(std::min<int64_t>(te - t, kRows)) - 1;
+        const float* const base = pb.V + t * r;
 #pragma unroll
         for (int i = 0; i < 2 * RT; ++i) {
-            const int q = lane + 64 * i;
-            const int64_t row = t + q / (4 * RT);
-            const int j = 4 * (q % (4 * RT));
-            const float* p = pb.V + row * r + j;
+            const int q = lane + 64 * i, j = 4 * (q % (4 * RT));
+            const float* const p = base + std::min(q / (4 * RT), left) * r;
+            if (quads) {
+                const float4 f = *reinterpret_cast<const float4*>(p + std::min(j, r - 4));
+                v[i][0] = f.x, v[i][1] = f.y, v[i][2] = f.z, v[i][3] = f.w;
+            } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[i][e] = 0.0f;
-            if (row < te) {
-                if ((r & 3) == 0) {
-                    if (j < r) {
-                        const float4 f = *reinterpret_cast<const float4*>(p);
-                        v[i][0] = f.x, v[i][1] = f.y, v[i][2] = f.z, v[i][3] = f.w;
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (j + e < r) v[i][e] = p[e];
-                }
+                for (int e = 0; e < 4; ++e) v[i][e] = p[std::min(j + e, r - 1)];
             }
         }
     };
-
-    uint4 mcur[4];
-    float vcur[2 * RT][4];
-    int64_t t = tb + kRows * wave;
-    if (t < te) {
-        load_m(t, mcur);
-        load_v(t, vcur);
-    }
-    for (; t < te; t += kWaves * kRows) {
+    // M of a chunk to the wave's tile
+    auto put_m = [&](const Stage& st, int64_t t) {
+        const bool tail = t + kRows > te;
         wave_lds_sync();  // the previous chunk's reads are done
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint4*>(tm + ((lane >> 3) + 8 * i) * kLdM + 8 * (lane & 7)) = mcur[i];
-        bf16x8_t bv[4];
+        for (int i = 0; i < MI; ++i) {
+            const int e = lane + 64 * i;
+            uint4 x;
+            if constexpr (ACT8) {
+                x = act8_decode8(st.c[i], st.s[i]);
+                if (masked) {
+                    const uint4 k = keep_mask(st.k[i]);
+                    x = make_uint4(x.x & k.x, x.y & k.y, x.z & k.z, x.w & k.w);
+                }
+            } else {
+                x = st.m[i];
+            }
+            if (tail && t + e / PR >= te) x = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(tm + (e / PR) * LdM + 8 * (e % PR)) = x;
+        }
+    };
+    bf16x8_t bv[CB];
+    auto get_m = [&]() {
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) bv[cb] = lds_col8(tm, LdM, 8 * g, 16 * cb, li);
+    };
+    // the chunk's products with V's terms as prepared
+    auto multiply_terms = [&](const Stage& st, int64_t t) {
+        const uint4* const vop = reinterpret_cast<const uint4*>(pb.terms) + (t / kRows) * (3 * RT * 64) + lane;
+        put_m(st, t);
+        wave_lds_sync();
+        get_m();
+        constexpr int RS = RT <= 4 ? RT : (RT + 1) / 2;  // rank tiles whose operands are in registers together
+#pragma unroll
+        for (int r0 = 0; r0 < RT; r0 += RS) {
+            uint4 av[RS][3];
+#pragma unroll
+            for (int rt = 0; rt < RS; ++rt)
+#pragma unroll
+                for (int term = 0; term < 3; ++term)
+                    if (r0 + rt < RT) av[rt][term] = vop[((r0 + rt) * 3 + term) * 64];
+#pragma unroll
+            for (int rt = 0; rt < RS; ++rt)
+#pragma unroll
+                for (int term = 0; term < 3; ++term)
+                    if (r0 + rt < RT) {
+#pragma unroll
+                        for (int cb = 0; cb < CB; ++cb)
+                            acc[r0 + rt][cb] =
+                                __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(av[rt][term]), bv[cb], acc[r0 + rt][cb], 0, 0, 0);
+                    }
+        }
+    };
+    // the same with V split here
+    auto multiply_split = [&](const Stage& st, float (&v)[2 * RT][4], int64_t t) {
+        put_m(st, t);
+        if (t + kRows > te || (r & 15) != 0) {  // nothing past the tokens and the rank
+#pragma unroll
+            for (int i = 0; i < 2 * RT; ++i) {
+                const int q = lane + 64 * i, j = 4 * (q % (4 * RT));
+                const bool out = t + q / (4 * RT) >= te;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (out || j + e >= r) v[i][e] = 0.0f;
+            }
+        }
+        float most = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2 * RT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) most = fmaxf(most, fabsf(v[i][e]));
+        const bool inf = __any(most == __builtin_inff());
 #pragma unroll
         for (int term = 0; term < 3; ++term) {
             if (term > 0) wave_lds_sync();
 #pragma unroll
             for (int i = 0; i < 2 * RT; ++i) {
                 const int q = lane + 64 * i;
-                float h[4];
+                uint32_t h[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) h[e] = split_term(vcur[i][e]);
+                for (int e = 0; e < 4; ++e) {
+                    h[e] = __float_as_uint(v[i][e]);
+                    if (term < 2) v[i][e] = split_rest(v[i][e], inf);
+                }
                 *reinterpret_cast<uint2*>(tv + (q / (4 * RT)) * LdV + 4 * (q % (4 * RT))) =
-                    make_uint2(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]));
+                    make_uint2(__builtin_amdgcn_perm(h[1], h[0], 0x07060302u), __builtin_amdgcn_perm(h[3], h[2], 0x07060302u));
             }
             wave_lds_sync();
-            if (term == 0) {
-#pragma unroll
-                for (int cb = 0; cb < 4; ++cb) bv[cb] = lds_col8(tm, kLdM, 8 * g, 16 * cb, li);
-            }
+            if (term == 0) get_m();
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
                 const bf16x8_t av = lds_col8(tv, LdV, 8 * g, 16 * rt, li);
 #pragma unroll
-                for (int cb = 0; cb < 4; ++cb)
+                for (int cb = 0; cb < CB; ++cb)
                     acc[rt][cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, bv[cb], acc[rt][cb], 0, 0, 0);
             }
         }
-        const int64_t tn = t + kWaves * kRows;
-        if (tn < te) {
-            load_m(tn, mcur);
-            load_v(tn, vcur);
+    };
+
+    Stage cur, nxt;
+    int64_t t = tb + kRows * wave;
+    if (t < te) {
+        load_m(cur, t);
+        if constexpr (kTerms) {
+            for (; t < te; t += NW * kRows) {
+                load_m(nxt, std::min<int64_t>(t + NW * kRows, te - 1));
+                __builtin_amdgcn_sched_barrier(0);
+                multiply_terms(cur, t);
+                cur = nxt;
+            }
+        } else {
+            float vcur[2 * RT][4], vnxt[2 * RT][4];
+            load_v(vcur, t);
+            for (; t < te; t += NW * kRows) {
+                const int64_t tn = std::min<int64_t>(t + NW * kRows, te - 1);
+                load_m(nxt, tn);
+                load_v(vnxt, tn);
+                __builtin_amdgcn_sched_barrier(0);
+                multiply_split(cur, vcur, t);
+                cur = nxt;
+#pragma unroll
+                for (int i = 0; i < 2 * RT; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) vcur[i][e] = vnxt[i][e];
+            }
         }
     }
-    // D[j = 4 g + q][column li] of each tile: waves 4..7 hand theirs to waves
-    // 0..3, whose sums are then added in order
+
+    // D[j = 4 g + q][column li] of each tile, rank tile by rank tile: the upper
+    // half of the waves hand theirs to the lower half through LDS, whose sums
+    // are then added in order
+    float* const red = reinterpret_cast<float*>(sm);
+    constexpr int W2 = NW / 2, kRed = 16 * 16 * CB;
+    static_assert(W2 * kRed * 2 <= NW * G::kTile, "the sums fit the tiles");
     const bool direct = gridDim.y == 1;
+    float* const out = direct ? pb.out : pb.part + static_cast<int64_t>(blockIdx.y) * r * C;
+    const float scale = direct ? pb.scale : 1.0f;
     for (int rt = 0; rt < RT; ++rt) {
+        __syncthreads();
 #pragma unroll
         for (int half = 1; half >= 0; --half) {
-            if ((wave >= kWaves / 2) == (half == 1)) {
-                float(*const rw)[kCols] = red[wave % (kWaves / 2)];
+            if ((wave >= W2) == (half == 1)) {
+                float* const rw = red + (wave % W2) * kRed;
 #pragma unroll
-                for (int cb = 0; cb < 4; ++cb)
+                for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        float& d = rw[4 * g + q][16 * cb + li];
-                        d = half == 1 ? acc[rt][cb][q] : acc[rt][cb][q] + d;
+                        float& d = rw[(4 * g + q) * 16 * CB + 16 * cb + li];
+                        float v = acc[0][cb][q];
+#pragma unroll
+                        for (int x = 1; x < RT; ++x) v = x == rt ? acc[x][cb][q] : v;
+                        d = half == 1 ? v : v + d;
                     }
             }
             __syncthreads();
         }
-        for (int e = tid; e < 16 * kCols; e += 64 * kWaves) {
+        for (int e = tid; e < kRed; e += 64 * NW) {
             // consecutive threads along the output's contiguous direction
-            const int jl = pb.layout_jc ? e / kCols : e % 16, cl = pb.layout_jc ? e % kCols : e / 16;
+            const int jl = pb.layout_jc ? e / (16 * CB) : e % 16, cl = pb.layout_jc ? e % (16 * CB) : e / 16;
             const int j = 16 * rt + jl;
-            const int64_t cc = c0 + cl;
-            if (cc >= C) continue;
-            float v = red[0][jl][cl];
+            const int64_t c = c0 + cl;
+            if (c >= C || j >= r) continue;
+            float v = 0.0f;
 #pragma unroll
-            for (int ww = 1; ww < kWaves / 2; ++ww) v += red[ww][jl][cl];
-            if (direct) {
-                if (j < r) {
-                    const int64_t idx = pb.layout_jc ? j * C + cc : cc * r + j;
-                    const float o = pb.scale * v;
-                    pb.out[idx] = a.accumulate ? pb.out[idx] + o : o;
-                }
-            } else {
-                pb.part[(static_cast<int64_t>(blockIdx.y) * RT * 16 + j) * C + cc] = v;
-            }
+            for (int ww = 0; ww < W2; ++ww) v += red[ww * kRed + jl * 16 * CB + cl];
+            const int64_t idx = pb.layout_jc ? j * C + c : c * r + j;
+            v *= scale;
+            out[idx] = direct && a.accumulate ? out[idx] + v : v;
         }
-        __syncthreads();
+    }
+}
+
+template <int RT, int CB>
+__global__ __launch_bounds__((64 * GradTile<RT, CB>::NW)) void act8_grads_kernel(Act8GradArgs a) {
+    using G = GradTile<RT, CB>;
+    __shared__ __attribute__((aligned(16))) uint16_t sm[G::NW * G::kTile];
+    const bool second = static_cast<int>(blockIdx.x) >= a.nblk0;
+    const Act8GradProblem& pb = second ? a.pb[1] : a.pb[0];
+    const int64_t c0 = static_cast<int64_t>(second ? blockIdx.x - a.nblk0 : blockIdx.x) * 16 * CB;
+    if (pb.scale8 != nullptr)
+        grads_block<RT, CB, true>(a, pb, c0, sm);
+    else
+        grads_block<RT, CB, false>(a, pb, c0, sm);
+}
+
+// V's terms in the order of the A operand: for 32 tokens, 16 ranks and term
+// the 64 lanes' 16 bytes, lane (li, g) holding rank li at tokens 8 g .. 8 g + 7;
+// zero past the tokens and the rank. One wave per 32 tokens and 16 ranks.
+__global__ __launch_bounds__(256) void act8_terms_kernel(Act8GradArgs a, int rt_all, int64_t units) {
+    const int lane = threadIdx.x & 63, li = lane & 15, g = lane >> 4;
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+    const Act8GradProblem& pb = a.pb[blockIdx.y];
+    if (unit >= units || pb.out == nullptr) return;
+    const int64_t t0 = unit / rt_all * kRows + 8 * g;
+    const int j = static_cast<int>(unit % rt_all) * 16 + li;
+    uint32_t h[3][8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        float v = t0 + e < a.T && j < a.r ? pb.V[(t0 + e) * a.r + j] : 0.0f;
+#pragma unroll
+        for (int term = 0; term < 3; ++term) {
+            h[term][e] = __float_as_uint(v);
+            v = split_rest(v, true);
+        }
+    }
+    uint4* const out = reinterpret_cast<uint4*>(pb.terms) + unit * (3 * 64) + lane;
+#pragma unroll
+    for (int term = 0; term < 3; ++term) {
+        uint32_t w[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) w[q] = __builtin_amdgcn_perm(h[term][2 * q + 1], h[term][2 * q], 0x07060302u);
+        out[term * 64] = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
 // Sum of the token splits of both problems, in split order.
-__global__ __launch_bounds__(256) void act8_grads_final_kernel(Act8GradArgs a, int splits, int rpad) {
+__global__ __launch_bounds__(256) void act8_grads_final_kernel(Act8GradArgs a, int splits) {
     const int64_t idx = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     const int64_t n0 = static_cast<int64_t>(a.r) * a.pb[0].C;
     const int64_t n1 = static_cast<int64_t>(a.r) * a.pb[1].C;
     if (idx >= n0 + n1) return;
     const bool second = idx >= n0;
     const Act8GradProblem& pb = second ? a.pb[1] : a.pb[0];
-    const int64_t e = second ? idx - n0 : idx;
-    const int64_t j = pb.layout_jc ? e / pb.C : e % a.r, c = pb.layout_jc ? e % pb.C : e / a.r;
+    const int64_t e = second ? idx - n0 : idx, n = second ? n1 : n0;
     float s = 0.0f;
-    for (int ts = 0; ts < splits; ++ts) s += pb.part[(static_cast<int64_t>(ts) * rpad + j) * pb.C + c];
+    for (int ts = 0; ts < splits; ++ts) s += pb.part[ts * n + e];
     const float v = pb.scale * s;
     pb.out[e] = a.accumulate ? pb.out[e] + v : v;
 }
 
-int splits_of(int64_t T, int64_t cols_total) {
-    // one split (no second kernel) while a workgroup's token loop stays short
-    if (T <= 2048 || cols_total <= 0) return 1;
-    const int64_t s = std::min(ceil_div(512, ceil_div(cols_total, kCols)), ceil_div(T, kWaves * kRows));
+constexpr int kCols = 64;  // columns a workgroup takes, but for the narrow tile below
+int grad_waves(int r) { return r <= 16 ? 16 : 8; }
+
+// Token splits: one (no second kernel) while a wave's loop stays short; else
+// about one workgroup a CU, each wave keeping two chunks at least.
+int splits_of(int64_t T, int64_t C0, int64_t C1, int r) {
+    if (T <= 2048 || C0 + C1 <= 0) return 1;
+    const int64_t blocks = ceil_div(C0, kCols) + ceil_div(C1, kCols);
+    const int64_t s = std::min<int64_t>(ceil_div(256, blocks), T / (2 * grad_waves(r) * kRows));
     return static_cast<int>(std::max<int64_t>(s, 1));
+}
+
+// Bytes of one V's terms (ranks over 16).
+size_t terms_bytes(int64_t T, int r) {
+    return r <= 16 ? 0 : static_cast<size_t>(ceil_div(T, kRows)) * (lora_grad_rp(r) / 16) * 3 * 1024;
+}
+
+template <int RT, int CB>
+void launch_grads(const Act8GradArgs& a, dim3 grid, hipStream_t stream) {
+    hipLaunchKernelGGL((act8_grads_kernel<RT, CB>), grid, dim3(64 * GradTile<RT, CB>::NW), 0, stream, a);
 }
 
 }  // namespace
 
 size_t act8_grads_part_bytes(int64_t T, int64_t C0, int64_t C1, int r) {
-    const int sp = splits_of(T, C0 + C1);
-    return sp == 1 ? 0 : static_cast<size_t>(sp) * lora_grad_rp(r) * (C0 + C1) * sizeof(float);
+    const int sp = splits_of(T, C0, C1, r);
+    const size_t part = sp == 1 ? 0 : static_cast<size_t>(sp) * r * (C0 + C1) * sizeof(float);
+    return (part + 255) / 256 * 256 + terms_bytes(T, r) * ((C0 > 0) + (C1 > 0));
 }
 
 int launch_act8_grads(Act8GradArgs a, float* part, hipStream_t stream) {
@@ -243,40 +403,56 @@ int launch_act8_grads(Act8GradArgs a, float* part, hipStream_t stream) {
         a.pb[1] = Act8GradProblem{};
     }
     if (a.pb[0].out == nullptr) return QL_OK;
+    if (a.r < 1 || a.r > QL_MAX_RANK) return set_error(QL_ERR_SHAPE, "adapter gradients: rank %d out of range", a.r);
     if (a.pb[1].out == nullptr) a.pb[1].C = 0;
     const int64_t c0 = a.pb[0].C, c1 = a.pb[1].C;
-    const int rp16 = lora_grad_rp(a.r);
-    const int splits = splits_of(a.T, c0 + c1);
-    a.t_per = ceil_div(ceil_div(a.T, splits), kWaves * kRows) * kWaves * kRows;
-    a.nblk0 = static_cast<int>(ceil_div(c0, kCols));
-    if (splits > 1) {
-        if (part == nullptr) return set_error(QL_ERR_WORKSPACE, "adapter gradients: workspace missing");
-        a.pb[0].part = part;
-        a.pb[1].part = part + static_cast<size_t>(splits) * rp16 * c0;
+    const int per = grad_waves(a.r) * kRows;
+    int splits = splits_of(a.T, c0, c1, a.r);
+    if (act8_grads_part_bytes(a.T, c0, c1, a.r) > 0 && part == nullptr)
+        return set_error(QL_ERR_WORKSPACE, "adapter gradients: workspace missing");
+    if (a.r > 16) {  // the terms sit behind the partials
+        const size_t pbytes = splits == 1 ? 0 : static_cast<size_t>(splits) * a.r * (c0 + c1) * sizeof(float);
+        char* at = reinterpret_cast<char*>(part) + (pbytes + 255) / 256 * 256;
+        a.pb[0].terms = reinterpret_cast<uint16_t*>(at);
+        a.pb[1].terms = reinterpret_cast<uint16_t*>(at + terms_bytes(a.T, a.r));
     }
-    const dim3 grid(static_cast<uint32_t>(a.nblk0 + ceil_div(c1, kCols)), static_cast<uint32_t>(splits));
+    a.pb[0].part = part;
+    a.pb[1].part = splits == 1 ? part : part + static_cast<size_t>(splits) * a.r * c0;
+    a.t_per = ceil_div(ceil_div(a.T, splits), per) * per;
+    const int want = splits;
+    splits = static_cast<int>(ceil_div(a.T, a.t_per));  // none without a token
+    if (want > 1 && splits == 1) a.t_per = a.T;
     timer_begin(QL_KERNEL_ACT8_GRAD, stream);
-    switch (rp16 / 16) {
-#define QL_CASE(R_)                                                                                  \
-    case R_:                                                                                         \
-        hipLaunchKernelGGL(act8_grads_kernel<R_>, grid, dim3(64 * kWaves), 0, stream, a);            \
-        break;
-        QL_CASE(1)
-        QL_CASE(2)
-        QL_CASE(3)
-        QL_CASE(4)
-        QL_CASE(5)
-        QL_CASE(6)
-        QL_CASE(7)
-        QL_CASE(8)
-#undef QL_CASE
-        default:
-            return set_error(QL_ERR_SHAPE, "adapter gradients: rank %d out of range", a.r);
+    const int rt = lora_grad_rp(a.r) / 16;
+    if (a.r > 16) {
+        const int64_t units = ceil_div(a.T, kRows) * rt;
+        hipLaunchKernelGGL(act8_terms_kernel, dim3(static_cast<uint32_t>(ceil_div(units, 4)), c1 > 0 ? 2 : 1), dim3(256), 0,
+                           stream, a, rt, units);
+    }
+    // Rank 16 and few columns: tiles half as wide, for workgroups on all CUs.
+    const bool narrow = rt == 1 && ceil_div(c0, kCols) + ceil_div(c1, kCols) <= 128;
+    const int cols = narrow ? 32 : kCols;
+    a.nblk0 = static_cast<int>(ceil_div(c0, cols));
+    const dim3 grid(static_cast<uint32_t>(a.nblk0 + ceil_div(c1, cols)), static_cast<uint32_t>(splits));
+    switch (rt) {
+        case 1:
+            if (narrow)
+                launch_grads<1, 2>(a, grid, stream);
+            else
+                launch_grads<1, 4>(a, grid, stream);
+            break;
+        case 2: launch_grads<2, 4>(a, grid, stream); break;
+        case 3: launch_grads<3, 4>(a, grid, stream); break;
+        case 4: launch_grads<4, 4>(a, grid, stream); break;
+        case 5: launch_grads<5, 4>(a, grid, stream); break;
+        case 6: launch_grads<6, 4>(a, grid, stream); break;
+        case 7: launch_grads<7, 4>(a, grid, stream); break;
+        default: launch_grads<8, 4>(a, grid, stream); break;
     }
     if (splits > 1)
         hipLaunchKernelGGL(act8_grads_final_kernel,
                            dim3(static_cast<uint32_t>(ceil_div(static_cast<int64_t>(a.r) * (c0 + c1), 256))),
-                           dim3(256), 0, stream, a, splits, rp16);
+                           dim3(256), 0, stream, a, splits);
     timer_end(QL_KERNEL_ACT8_GRAD, stream);
     return check_launch("adapter gradients from an 8-bit checkpoint");
 }

@@ -985,7 +985,7 @@ Act8Dev act8_dev(const ql_act8* a) { return a == nullptr ? Act8Dev{} : Act8Dev{a
 struct Bwd8Ws {
     uint16_t* Gp[kGemmMaxGroup] = {};  // bf16 [T, rp64] = G per layer, dX's LoRA operand
     float* G = nullptr;                // fp32 [T, r] = G of the layer being processed, dA's operand
-    float* gpart = nullptr;            // fp32 token-split partials of dA and dB
+    float* gpart = nullptr;            // the gradient kernels' workspace
     void* proj = nullptr;              // split partials of the G projection
     float* split = nullptr;            // fp32 split-K partials of the dX GEMM
     uint64_t* gword = nullptr;         // one layer, G inside the dX launch: G words and the epoch word
@@ -1120,8 +1120,8 @@ int linear_bwd8(const ql_nf4_weight* const* w, int32_t nw, bool group, const ql_
             a.r = r;
             a.T = T;
             a.accumulate = accumulate;
-            if (da) a.pb[0] = Act8GradProblem{X8->codes, X8->scale, keep, K, b.G, dA[i], 1, c, nullptr};
-            if (db) a.pb[1] = Act8GradProblem{dY[i], nullptr, nullptr, rows[i], U[i], dB[i], 0, scale, nullptr};
+            if (da) a.pb[0] = Act8GradProblem{X8->codes, X8->scale, keep, K, b.G, dA[i], 1, c, nullptr, nullptr};
+            if (db) a.pb[1] = Act8GradProblem{dY[i], nullptr, nullptr, rows[i], U[i], dB[i], 0, scale, nullptr, nullptr};
             if ((s = launch_act8_grads(a, b.gpart, st)) != QL_OK) return s;
         }
     }

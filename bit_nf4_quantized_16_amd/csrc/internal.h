@@ -253,7 +253,8 @@ struct Act8GradProblem {
     float* out;
     int layout_jc;
     float scale;
-    float* part;  // set by the launcher
+    float* part;      // set by the launcher
+    uint16_t* terms;  // set by the launcher: V's bf16 terms in operand order
 };
 struct Act8GradArgs {
     Act8GradProblem pb[2];
@@ -263,7 +264,8 @@ struct Act8GradArgs {
     int64_t t_per;  // set by the launcher
     int accumulate;
 };
-// fp32 workspace for token-split partials (0 when one split suffices)
+// workspace: fp32 token-split partials (none when one split suffices) and, for
+// ranks over 16, the terms; 16-byte aligned
 size_t act8_grads_part_bytes(int64_t T, int64_t C0, int64_t C1, int r);
 int launch_act8_grads(Act8GradArgs a, float* part, hipStream_t stream);
 

@@ -59,19 +59,19 @@ template <int RT, int CB_>
 struct GradTile {
     static constexpr int CB = CB_;
     static constexpr bool kTerms = RT > 1;
-    static constexpr int NW = RT == 1 ? 16 : 8;
+    static constexpr int NW = 8;
     static constexpr int LdM = 16 * CB + 8, LdV = kTerms ? 0 : 16 * RT + 8;
     static constexpr int kTile = kRows * (LdM + LdV);  // 16-bit words of one wave
 };
 
-// A wave's chunk of M as loaded: MI pieces of eight columns a lane (codes,
-// scale and keep byte of a checkpoint; or bf16 values).
+// A wave's chunk of M as loaded: MI pieces of eight columns a lane (codes or
+// bf16 values); of a checkpoint also the scale byte and the keep bits of one
+// block of 32, block b of token t in lane t CB / 2 + b.
 template <int MI, bool ACT8>
 struct GradStage {
     uint4 m[ACT8 ? 1 : MI];
     uint2 c[ACT8 ? MI : 1];
-    uint32_t s[ACT8 ? MI : 1];
-    uint32_t k[ACT8 ? MI : 1];
+    uint32_t s, k;
 };
 
 template <int RT, int CB_, bool ACT8>
@@ -97,7 +97,6 @@ __device__ __forceinline__ void grads_block(const Act8GradArgs& a, const Act8Gra
     uint16_t* const tm = sm + wave * G::kTile;
     uint16_t* const tv = tm + kRows * LdM;
     const bool masked = ACT8 && pb.keep != nullptr;
-    const uint8_t* const kp = masked ? pb.keep : static_cast<const uint8_t*>(pb.M);  // without a mask: read and not used
     const bool quads = (r & 3) == 0;
     constexpr int RI = 64 / PR;  // tokens of a load
 
@@ -105,19 +104,27 @@ __device__ __forceinline__ void grads_block(const Act8GradArgs& a, const Act8Gra
     // range (tokens from te on, columns from C on, ranks from r on) the nearest
     // element in range is read, and zeroed or left out when it is used.
     const int64_t col = std::min<int64_t>(c0 + 8 * (lane % PR), C - 8), moff = (lane / PR) * C + col;
+    constexpr int BPR = CB / 2;  // blocks of a token's row
+    static_assert(kRows * BPR <= 64, "a lane per block");
+    const int brow = std::min(lane / BPR, kRows - 1);
+    const int64_t bcol = std::min<int64_t>(c0 / kAct8Block + lane % BPR, C / kAct8Block - 1);
     auto load_m = [&](Stage& st, int64_t t) {
         const bool tail = t + kRows > te;
+        if constexpr (ACT8) {
+            // one load for the chunk's scales (and one for its mask): a byte per
+            // piece would touch a line per token again and again
+            const int64_t at = std::min<int64_t>(t + brow, te - 1) * (C / kAct8Block) + bcol;
+            if (masked) st.k = reinterpret_cast<const uint32_t*>(pb.keep)[at];
+            st.s = pb.scale8[at];
+        }
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
             int64_t at = (t + RI * i) * C + moff;
             if (tail) at = std::min<int64_t>(t + RI * i + lane / PR, te - 1) * C + col;
-            if constexpr (ACT8) {
+            if constexpr (ACT8)
                 st.c[i] = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(pb.M) + at);
-                st.s[i] = pb.scale8[at / kAct8Block];
-                st.k[i] = kp[at / 8];
-            } else {
+            else
                 st.m[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(pb.M) + at);
-            }
         }
     };
     // V of the chunk: quads of ranks, 4 RT a token
@@ -146,9 +153,10 @@ __device__ __forceinline__ void grads_block(const Act8GradArgs& a, const Act8Gra
             const int e = lane + 64 * i;
             uint4 x;
             if constexpr (ACT8) {
-                x = act8_decode8(st.c[i], st.s[i]);
+                const int from = (e / PR) * BPR + (e % PR) / 4;  // the lane with the piece's block
+                x = act8_decode8(st.c[i], __shfl(st.s, from, 64));
                 if (masked) {
-                    const uint4 k = keep_mask(st.k[i]);
+                    const uint4 k = keep_mask(__shfl(st.k, from, 64) >> (8 * (e % 4)));
                     x = make_uint4(x.x & k.x, x.y & k.y, x.z & k.z, x.w & k.w);
                 }
             } else {
@@ -163,13 +171,13 @@ __device__ __forceinline__ void grads_block(const Act8GradArgs& a, const Act8Gra
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb) bv[cb] = lds_col8(tm, LdM, 8 * g, 16 * cb, li);
     };
-    // the chunk's products with V's terms as prepared
-    auto multiply_terms = [&](const Stage& st, int64_t t) {
+    // the chunk's products with V's terms as prepared. Loads return in order:
+    // the terms (from L2) are asked for before the next chunk of M (from HBM),
+    // or every chunk would wait for that as well (rank 64, T = 4096,
+    // 4096 + 11008 columns: 63 against 57 us).
+    constexpr int RS = RT <= 4 ? RT : (RT + 1) / 2;  // rank tiles whose operands are in registers together
+    auto multiply_terms = [&](const Stage& st, Stage& next, int64_t t, int64_t tn) {
         const uint4* const vop = reinterpret_cast<const uint4*>(pb.terms) + (t / kRows) * (3 * RT * 64) + lane;
-        put_m(st, t);
-        wave_lds_sync();
-        get_m();
-        constexpr int RS = RT <= 4 ? RT : (RT + 1) / 2;  // rank tiles whose operands are in registers together
 #pragma unroll
         for (int r0 = 0; r0 < RT; r0 += RS) {
             uint4 av[RS][3];
@@ -178,6 +186,14 @@ __device__ __forceinline__ void grads_block(const Act8GradArgs& a, const Act8Gra
 #pragma unroll
                 for (int term = 0; term < 3; ++term)
                     if (r0 + rt < RT) av[rt][term] = vop[((r0 + rt) * 3 + term) * 64];
+            __builtin_amdgcn_sched_barrier(0);
+            if (r0 + RS >= RT) load_m(next, tn);
+            __builtin_amdgcn_sched_barrier(0);
+            if (r0 == 0) {
+                put_m(st, t);
+                wave_lds_sync();
+                get_m();
+            }
 #pragma unroll
             for (int rt = 0; rt < RS; ++rt)
 #pragma unroll
@@ -242,9 +258,7 @@ __device__ __forceinline__ void grads_block(const Act8GradArgs& a, const Act8Gra
         load_m(cur, t);
         if constexpr (kTerms) {
             for (; t < te; t += NW * kRows) {
-                load_m(nxt, std::min<int64_t>(t + NW * kRows, te - 1));
-                __builtin_amdgcn_sched_barrier(0);
-                multiply_terms(cur, t);
+                multiply_terms(cur, nxt, t, std::min<int64_t>(t + NW * kRows, te - 1));
                 cur = nxt;
             }
         } else {
@@ -368,14 +382,14 @@ __global__ __launch_bounds__(256) void act8_grads_final_kernel(Act8GradArgs a, i
 }
 
 constexpr int kCols = 64;  // columns a workgroup takes, but for the narrow tile below
-int grad_waves(int r) { return r <= 16 ? 16 : 8; }
+constexpr int kWaves = 8;
 
 // Token splits: one (no second kernel) while a wave's loop stays short; else
 // about one workgroup a CU, each wave keeping two chunks at least.
 int splits_of(int64_t T, int64_t C0, int64_t C1, int r) {
     if (T <= 2048 || C0 + C1 <= 0) return 1;
     const int64_t blocks = ceil_div(C0, kCols) + ceil_div(C1, kCols);
-    const int64_t s = std::min<int64_t>(ceil_div(256, blocks), T / (2 * grad_waves(r) * kRows));
+    const int64_t s = std::min<int64_t>(ceil_div(256, blocks), T / (2 * kWaves * kRows));
     return static_cast<int>(std::max<int64_t>(s, 1));
 }
 
@@ -406,7 +420,7 @@ int launch_act8_grads(Act8GradArgs a, float* part, hipStream_t stream) {
     if (a.r < 1 || a.r > QL_MAX_RANK) return set_error(QL_ERR_SHAPE, "adapter gradients: rank %d out of range", a.r);
     if (a.pb[1].out == nullptr) a.pb[1].C = 0;
     const int64_t c0 = a.pb[0].C, c1 = a.pb[1].C;
-    const int per = grad_waves(a.r) * kRows;
+    const int per = kWaves * kRows;
     int splits = splits_of(a.T, c0, c1, a.r);
     if (act8_grads_part_bytes(a.T, c0, c1, a.r) > 0 && part == nullptr)
         return set_error(QL_ERR_WORKSPACE, "adapter gradients: workspace missing");
@@ -430,20 +444,15 @@ int launch_act8_grads(Act8GradArgs a, float* part, hipStream_t stream) {
                            stream, a, rt, units);
     }
     // Rank 16 and few columns: tiles half as wide, for workgroups on all CUs.
-    const bool narrow = rt == 1 && ceil_div(c0, kCols) + ceil_div(c1, kCols) <= 128;
+    const bool narrow = rt <= 4 && ceil_div(c0, kCols) + ceil_div(c1, kCols) <= 128;
     const int cols = narrow ? 32 : kCols;
     a.nblk0 = static_cast<int>(ceil_div(c0, cols));
     const dim3 grid(static_cast<uint32_t>(a.nblk0 + ceil_div(c1, cols)), static_cast<uint32_t>(splits));
     switch (rt) {
-        case 1:
-            if (narrow)
-                launch_grads<1, 2>(a, grid, stream);
-            else
-                launch_grads<1, 4>(a, grid, stream);
-            break;
-        case 2: launch_grads<2, 4>(a, grid, stream); break;
-        case 3: launch_grads<3, 4>(a, grid, stream); break;
-        case 4: launch_grads<4, 4>(a, grid, stream); break;
+        case 1: narrow ? launch_grads<1, 2>(a, grid, stream) : launch_grads<1, 4>(a, grid, stream); break;
+        case 2: narrow ? launch_grads<2, 2>(a, grid, stream) : launch_grads<2, 4>(a, grid, stream); break;
+        case 3: narrow ? launch_grads<3, 2>(a, grid, stream) : launch_grads<3, 4>(a, grid, stream); break;
+        case 4: narrow ? launch_grads<4, 2>(a, grid, stream) : launch_grads<4, 4>(a, grid, stream); break;
         case 5: launch_grads<5, 4>(a, grid, stream); break;
         case 6: launch_grads<6, 4>(a, grid, stream); break;
         case 7: launch_grads<7, 4>(a, grid, stream); break;

@@ -375,17 +375,19 @@ def _refuse(status, message):
 def _tensor(t, name, dtype, shape, device=None):
     """t, checked: a contiguous device tensor of this dtype and shape (on
     ``device`` where given)."""
+    shape = tuple(shape)
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda
+            and (device is None or t.device == device)):
+        return t
     if not isinstance(t, torch.Tensor):
         _refuse(_lib.QL_ERR_NULL, "%s is no tensor" % name)
     if t.dtype != dtype:
         _refuse(_lib.QL_ERR_UNSUPPORTED, "%s is %s, expected %s" % (name, t.dtype, dtype))
-    if tuple(t.shape) != tuple(shape):
-        _refuse(_lib.QL_ERR_SHAPE, "%s is %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if t.shape != shape:
+        _refuse(_lib.QL_ERR_SHAPE, "%s is %s, expected %s" % (name, tuple(t.shape), shape))
     if not t.is_contiguous():
         _refuse(_lib.QL_ERR_UNSUPPORTED, "%s is not contiguous" % name)
-    if not t.is_cuda or (device is not None and t.device != device):
-        _refuse(_lib.QL_ERR_UNSUPPORTED, "%s is on %s, expected %s" % (name, t.device, device or "a GPU"))
-    return t
+    _refuse(_lib.QL_ERR_UNSUPPORTED, "%s is on %s, expected %s" % (name, t.device, device or "a GPU"))
 
 
 def _matrix(t, name, dtype=torch.bfloat16):

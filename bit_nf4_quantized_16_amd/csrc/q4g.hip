@@ -25,84 +25,133 @@ __device__ __forceinline__ float load_scale(const void* p, int64_t i) {
     return F32 ? static_cast<const float*>(p)[i] : bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
 }
 
+// Division of a thread index under 2^31 by a row's length, for a kernel whose
+// threads run through rows of units: n / d = (n m) >> (31 + s), s = ceil(log2 d),
+// m = floor(2^(31 + s) / d) + 1 < 2^32 (exact for n < 2^31).
+struct RowDivisor {
+    uint32_t d, m;
+    int s;
+};
+
+RowDivisor row_divisor(int64_t d) {
+    RowDivisor r{static_cast<uint32_t>(d), 0, 0};
+    while ((int64_t{1} << r.s) < d) ++r.s;
+    r.m = static_cast<uint32_t>((uint64_t{1} << (31 + r.s)) / static_cast<uint64_t>(d) + 1);
+    return r;
+}
+
+// row and unit within it of thread n
+__device__ __forceinline__ uint32_t row_of(uint32_t n, const RowDivisor& r, uint32_t& unit) {
+    const uint32_t row = r.d == 1 ? n : static_cast<uint32_t>((static_cast<uint64_t>(n) * r.m) >> (31 + r.s));
+    unit = n - row * r.d;
+    return row;
+}
+
 // ---------------------------------------------------------------------------
 // Quantize. A lane holds eight consecutive values, so a group is 4, 8 or 16
-// lanes and its range takes DPP maxima only. w / s is the correctly rounded
-// fp32 quotient: the product with the correctly rounded 1 / s, corrected
-// once by its exact remainder (Markstein's theorem), three operations a value
-// instead of a division's ten. HBM-bound.
+// lanes and its range takes DPP maxima only. The range is found on the bits:
+// as signed integers positive floats order like their values (and above the
+// negative ones), as unsigned integers the negative ones like their magnitudes
+// (and above the positive), so two integer maxima, packed for bf16, give both
+// ends. Quotients are correctly rounded fp32: the product with the correctly
+// rounded reciprocal, corrected once by its exact remainder (Markstein's
+// theorem), three operations instead of a division's ten; adding 1.5 2^23
+// rounds to an integer, ties to even, in the low bits. The arithmetic is what
+// bounds it next to HBM (the same with divisions, float maxima and a 64-bit
+// index division: 34 us at 11008 x 4096 from bf16).
 // ---------------------------------------------------------------------------
+__device__ __forceinline__ int imax_(int a, int b) { return a > b ? a : b; }
+
+// Maxima over a group's lanes, everywhere: hi as signed, lo as unsigned.
 template <int G>
-__device__ __forceinline__ float group_max(float v) {
-    if constexpr (G == 128) return max16(v);
-    if constexpr (G == 64) return max8(v);
-    v = fmaxf(v, dpp_f<0x4E>(v));
-    return fmaxf(v, dpp_f<0xB1>(v));
+__device__ __forceinline__ void group_range(int& hi, uint32_t& lo) {
+    auto step = [&](auto ctrl) {
+        constexpr int C = decltype(ctrl)::value;
+        hi = imax_(hi, static_cast<int>(dpp_u<C>(static_cast<uint32_t>(hi))));
+        lo = umax_(lo, dpp_u<C>(lo));
+    };
+    if constexpr (G == 128) {
+        step(std::integral_constant<int, 0x128>{});  // row_ror:8
+        step(std::integral_constant<int, 0x124>{});  // row_ror:4
+    } else if constexpr (G == 64) {
+        step(std::integral_constant<int, 0x141>{});  // row_half_mirror
+    }
+    step(std::integral_constant<int, 0x4E>{});  // quad_perm [2,3,0,1]
+    step(std::integral_constant<int, 0xB1>{});  // quad_perm [1,0,3,2]
+}
+
+// a / b, correctly rounded, from inv = fl32(1 / b).
+__device__ __forceinline__ float quotient(float a, float b, float inv) {
+    const float x = a * inv;
+    return __builtin_fmaf(__builtin_fmaf(-x, b, a), inv, x);
 }
 
 template <bool WF32, int G, bool SF32>
-__global__ __launch_bounds__(kThreads) void q4g_quantize_kernel(const void* __restrict__ W, int64_t N, int64_t K,
-                                                                uint8_t* __restrict__ packed,
+__global__ __launch_bounds__(kThreads) void q4g_quantize_kernel(const void* __restrict__ W, uint32_t N, uint32_t K,
+                                                                RowDivisor lanes, uint8_t* __restrict__ packed,
                                                                 void* __restrict__ scale, uint8_t* __restrict__ zero) {
-    const int64_t ng = ceil_div(K, G);
-    const int64_t lpr = ng * (G / 8);  // lanes of a row: whole groups
-    const int64_t base = static_cast<int64_t>(blockIdx.x) * kThreads;
-    const int64_t row0 = base / lpr;
-    const uint32_t off = static_cast<uint32_t>(base - row0 * lpr) + threadIdx.x;
-    const uint32_t rows = off / static_cast<uint32_t>(lpr);
-    const int64_t row = row0 + rows;
-    const int64_t u = off - rows * static_cast<uint32_t>(lpr);  // eight-value unit of the row
+    uint32_t u;  // eight-value unit of the row
+    const uint32_t row = row_of(blockIdx.x * kThreads + threadIdx.x, lanes, u);
     const bool in = row < N && 8 * u < K;
-    float w[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = 0.0f;
-    if (in) {
-        if constexpr (WF32) {
-            const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(W) + row * K + 8 * u);
-            const float4 a = p[0], b = p[1];
-            w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-        } else {
-            const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(W) + row * K + 8 * u);
-            const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                w[2 * e] = __uint_as_float(vw[e] << 16);
-                w[2 * e + 1] = __uint_as_float(vw[e] & 0xFFFF0000u);
-            }
+    uint32_t w[8];  // the values as fp32 bits
+    int hi = 0;
+    uint32_t lo = 0;
+    if constexpr (WF32) {
+        uint4 a = make_uint4(0, 0, 0, 0), b = a;
+        if (in) {
+            const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(W) + static_cast<int64_t>(row) * K + 8 * u);
+            a = p[0], b = p[1];
         }
-    }
-    float hi = 0.0f, lo = 0.0f;  // lo: of -w
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        hi = fmaxf(hi, w[e]);
-        lo = fmaxf(lo, -w[e]);
+        for (int e = 0; e < 8; ++e) {
+            hi = imax_(hi, static_cast<int>(w[e]));
+            lo = umax_(lo, w[e]);
+        }
+    } else {
+        typedef short i16x2 __attribute__((ext_vector_type(2)));
+        typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (in) v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(W) + static_cast<int64_t>(row) * K + 8 * u);
+        const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+        i16x2 h2 = {0, 0};
+        u16x2 l2 = {0, 0};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            h2 = __builtin_elementwise_max(h2, __builtin_bit_cast(i16x2, vw[e]));
+            l2 = __builtin_elementwise_max(l2, __builtin_bit_cast(u16x2, vw[e]));
+            w[2 * e] = vw[e] << 16;
+            w[2 * e + 1] = vw[e] & 0xFFFF0000u;
+        }
+        hi = imax_(h2[0], h2[1]) << 16;
+        lo = umax_(l2[0], l2[1]) << 16;
     }
-    hi = group_max<G>(hi);
-    lo = group_max<G>(lo);
+    group_range<G>(hi, lo);
+    const float top = __int_as_float(hi), bottom = static_cast<int>(lo) < 0 ? __uint_as_float(lo & 0x7FFFFFFFu) : 0.0f;
     const bool sym = zero == nullptr;
-    float s = sym ? fmaxf(hi, lo) / 7.0f : (hi + lo) / 15.0f;
+    float s = sym ? quotient(fmaxf(top, bottom), 7.0f, 1.0f / 7.0f) : quotient(top + bottom, 15.0f, 1.0f / 15.0f);
     if constexpr (!SF32) s = __uint_as_float(pack_bf16x2(s, 0.0f) << 16);
     const bool live = s >= 0x1p-126f;  // below: the group is held as zeros
     if (!live) s = 0.0f;
     const float inv = 1.0f / s;
-    auto quotient = [&](float a) {
-        const float x = a * inv;
-        return __builtin_fmaf(__builtin_fmaf(-x, s, a), inv, x);
-    };
-    const float z = (sym || !live) ? 8.0f : fminf(__builtin_rintf(quotient(lo)), 15.0f);
-    uint32_t c = 0;
-    if (in) {
+    constexpr float kRound = 12582912.0f;  // 1.5 2^23
+    constexpr int kRoundBits = 0x4B400000;
+    auto nearest = [&](float a) { return __float_as_int(quotient(a, s, inv) + kRound) - kRoundBits; };
+    const int z = (sym || !live) ? 8 : std::min(nearest(bottom), 15);
+    uint32_t c = 0x88888888u;
+    if (live) {
+        c = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float q = live ? fminf(fmaxf(__builtin_rintf(quotient(w[e])) + z, 0.0f), 15.0f) : 8.0f;
+            const int q = std::min(std::max(nearest(__uint_as_float(w[e])) + z, 0), 15);
             c |= static_cast<uint32_t>(q) << (8 * (e / 2) + (e % 2 ? 0 : 4));
         }
     }
-    const int64_t upr = ceil_div(K, 32) * 4;  // units a row has room for
+    const uint32_t upr = (K + 31) / 32 * 4, ng = (K + G - 1) / G;  // units a row has room for, groups of a row
     if (row < N) {
-        if (u < upr) reinterpret_cast<uint32_t*>(packed)[row * upr + u] = c;
+        if (u < upr) reinterpret_cast<uint32_t*>(packed)[static_cast<int64_t>(row) * upr + u] = in ? c : 0u;
         if (u % (G / 8) == 0) {
-            const int64_t gi = row * ng + u / (G / 8);
+            const int64_t gi = static_cast<int64_t>(row) * ng + u / (G / 8);
             if constexpr (SF32)
                 static_cast<float*>(scale)[gi] = s;
             else
@@ -117,29 +166,26 @@ __global__ __launch_bounds__(kThreads) void q4g_quantize_kernel(const void* __re
 // output. A lane expands eight values. HBM-bound.
 // ---------------------------------------------------------------------------
 template <bool BF16, bool SF32>
-__global__ __launch_bounds__(kThreads) void q4g_dequantize_kernel(Q4GDev w, int64_t N, int64_t K,
+__global__ __launch_bounds__(kThreads) void q4g_dequantize_kernel(Q4GDev w, uint32_t N, uint32_t K, RowDivisor units,
                                                                   void* __restrict__ out) {
-    const int64_t k8 = K / 8;
-    const int64_t base = static_cast<int64_t>(blockIdx.x) * kThreads;
-    const int64_t row0 = base / k8;
-    const uint32_t off = static_cast<uint32_t>(base - row0 * k8) + threadIdx.x;
-    const uint32_t rows = off / static_cast<uint32_t>(k8);
-    const int64_t row = row0 + rows;
-    const int64_t u = off - rows * static_cast<uint32_t>(k8);
+    uint32_t u;
+    const uint32_t row = row_of(blockIdx.x * kThreads + threadIdx.x, units, u);
     if (row >= N) return;
-    const uint32_t c = reinterpret_cast<const uint32_t*>(w.packed)[row * (ceil_div(K, 32) * 4) + u];
-    const int64_t gi = row * ceil_div(K, w.group) + 8 * u / w.group;
+    const uint32_t shift = __builtin_ctz(w.group);
+    const int64_t gi = static_cast<int64_t>(row) * ((K + w.group - 1) >> shift) + (8 * u >> shift);
+    const uint32_t c = reinterpret_cast<const uint32_t*>(w.packed)[static_cast<int64_t>(row) * ((K + 31) / 32 * 4) + u];
     const float s = load_scale<SF32>(w.scale, gi);
     const int z = w.zero != nullptr ? w.zero[gi] : 8;
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e)
         v[e] = static_cast<float>(static_cast<int>((c >> (8 * (e / 2) + (e % 2 ? 0 : 4))) & 15u) - z) * s;
+    const int64_t at = static_cast<int64_t>(row) * K + 8 * u;
     if constexpr (BF16) {
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + row * K + 8 * u) =
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) =
             make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
     } else {
-        float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + row * K + 8 * u);
+        float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
         o[0] = make_float4(v[0], v[1], v[2], v[3]);
         o[1] = make_float4(v[4], v[5], v[6], v[7]);
     }
@@ -726,22 +772,13 @@ int launch_linear_variant(const Q4GLinearArgs& a, hipStream_t stream) {
     return two ? launch_wide<2, 4, 4, GL, SF32>(a, stream) : launch_wide<1, 4, 8, GL, SF32>(a, stream);
 }
 
-template <bool WF32, bool SF32>
-void launch_quantize_g(const void* W, int64_t N, int64_t K, int group, uint8_t* packed, void* scale, uint8_t* zero,
+template <bool WF32, int G, bool SF32>
+void launch_quantize_g(const void* W, int64_t N, int64_t K, uint8_t* packed, void* scale, uint8_t* zero,
                        hipStream_t stream) {
-    const dim3 grid(static_cast<uint32_t>(ceil_div(N * ceil_div(K, group) * (group / 8), kThreads))), block(kThreads);
-    switch (group) {
-        case 32:
-            hipLaunchKernelGGL((q4g_quantize_kernel<WF32, 32, SF32>), grid, block, 0, stream, W, N, K, packed, scale, zero);
-            break;
-        case 64:
-            hipLaunchKernelGGL((q4g_quantize_kernel<WF32, 64, SF32>), grid, block, 0, stream, W, N, K, packed, scale, zero);
-            break;
-        default:
-            hipLaunchKernelGGL((q4g_quantize_kernel<WF32, 128, SF32>), grid, block, 0, stream, W, N, K, packed, scale,
-                               zero);
-            break;
-    }
+    const int64_t lanes = ceil_div(K, G) * (G / 8);  // of a row: whole groups
+    hipLaunchKernelGGL((q4g_quantize_kernel<WF32, G, SF32>), dim3(static_cast<uint32_t>(ceil_div(N * lanes, kThreads))),
+                       dim3(kThreads), 0, stream, W, static_cast<uint32_t>(N), static_cast<uint32_t>(K), row_divisor(lanes),
+                       packed, scale, zero);
 }
 
 }  // namespace
@@ -759,7 +796,12 @@ int launch_q4g_quantize(const void* W, bool w_f32, int64_t N, int64_t K, int gro
                         bool scale_f32, uint8_t* zero, hipStream_t stream) {
     timer_begin(QL_KERNEL_Q4G_QUANTIZE, stream);
     with_flags(w_f32, scale_f32, [&](auto wf, auto sf) {
-        launch_quantize_g<decltype(wf)::value, decltype(sf)::value>(W, N, K, group, packed, scale, zero, stream);
+        constexpr bool WF32 = decltype(wf)::value, SF32 = decltype(sf)::value;
+        switch (group) {
+            case 32: launch_quantize_g<WF32, 32, SF32>(W, N, K, packed, scale, zero, stream); break;
+            case 64: launch_quantize_g<WF32, 64, SF32>(W, N, K, packed, scale, zero, stream); break;
+            default: launch_quantize_g<WF32, 128, SF32>(W, N, K, packed, scale, zero, stream); break;
+        }
     });
     timer_end(QL_KERNEL_Q4G_QUANTIZE, stream);
     return check_launch("4-bit group quantize");
@@ -770,7 +812,7 @@ int launch_q4g_dequantize(const Q4GDev& w, int64_t N, int64_t K, void* out, bool
     timer_begin(QL_KERNEL_Q4G_DEQUANTIZE, stream);
     with_flags(bf16_out, w.scale_f32 != 0, [&](auto bf, auto sf) {
         hipLaunchKernelGGL((q4g_dequantize_kernel<decltype(bf)::value, decltype(sf)::value>), grid, block, 0, stream, w,
-                           N, K, out);
+                           static_cast<uint32_t>(N), static_cast<uint32_t>(K), row_divisor(K / 8), out);
     });
     timer_end(QL_KERNEL_Q4G_DEQUANTIZE, stream);
     return check_launch("4-bit group dequantize");

@@ -403,6 +403,10 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _launch(device, call, *args):
     """call(*args, stream) on ``device`` and its current stream."""
     if device.index == torch.cuda.current_device():
@@ -502,7 +506,7 @@ def _adapters(A, B, rows, cols, device):
     """The rank of an adapter pair (0 when A is None), shapes checked."""
     if A is None:
         return 0
-    r = _matrix(A, "A").shape[0]
+    r = A.shape[0] if isinstance(A, torch.Tensor) and A.dim() == 2 else _refuse(_lib.QL_ERR_SHAPE, "A is not 2-D")
     _tensor(A, "A", torch.bfloat16, (r, cols), device)
     _tensor(B, "B", torch.bfloat16, (rows, r), device)
     return r
@@ -522,9 +526,10 @@ def qlora_linear_bwd_act8(w, X8, dY, A=None, B=None, scale=1.0, U=None, need_dx=
     """qlora_linear_bwd with the layer's input kept as an Act8 ``X8``. ``U``
     (fp32 [T, r], from the forward) is required for dB; X8 may be None without
     dA. dA and dB use U and G = s dY B in fp32."""
-    T = _matrix(dY, "dY").shape[0]
-    dev = dY.device
-    _tensor(dY, "dY", torch.bfloat16, (T, w.rows), dev)
+    if not isinstance(dY, torch.Tensor) or dY.dim() != 2:
+        _refuse(_lib.QL_ERR_SHAPE, "dY is not 2-D")
+    T, dev = dY.shape[0], dY.device
+    _tensor(dY, "dY", torch.bfloat16, (T, w.rows))
     r = _adapters(A, B, w.rows, w.cols, dev)
     dX = torch.empty(T, w.cols, dtype=torch.bfloat16, device=dev) if need_dx else None
     dA = _grads(r > 0 and need_da, dA, (r, w.cols), "dA", accumulate, dev)
@@ -534,7 +539,9 @@ def qlora_linear_bwd_act8(w, X8, dY, A=None, B=None, scale=1.0, U=None, need_dx=
     x8 = None
     if dA is not None:
         x8 = X8.descriptor() if X8 is not None else _refuse(_lib.QL_ERR_NULL, "X8 is None (dA needs it)")
-        _tensor(X8.codes, "X8", torch.uint8, (T, w.cols), dev)
+        if (X8.rows, X8.cols) != (T, w.cols) or X8.codes.device != dev:
+            _refuse(_lib.QL_ERR_SHAPE, "X8 is %d x %d on %s, expected %d x %d on %s"
+                    % (X8.rows, X8.cols, X8.codes.device, T, w.cols, dev))
     if keep is not None:
         _tensor(keep.view(T, -1), "keep", torch.uint8, (T, w.cols // 8), dev)
     ws, wsb = _workspace(lib.qlora_linear_bwd_act8_workspace(w.rows, w.cols, max(T, 1), r, keep is not None), dev)
@@ -543,9 +550,9 @@ def qlora_linear_bwd_act8(w, X8, dY, A=None, B=None, scale=1.0, U=None, need_dx=
             if g is not None and not accumulate:
                 g.zero_()
         return dX, dA, dB
-    _launch(dev, lib.qlora_linear_bwd_act8, w.descriptor(), x8, dY.data_ptr(), T, _ptr(A), _ptr(B), r, float(scale),
-            _ptr(keep), float(p), _ptr(U) if dB is not None else None, _ptr(dX), _ptr(dA), _ptr(dB),
-            1 if accumulate else 0, _ptr(ws), wsb)
+    _launch(dev, lib.qlora_linear_bwd_act8, w.descriptor(), x8, dY.data_ptr(), T, _addr(A), _addr(B), r, scale,
+            _addr(keep), p, _addr(U) if dB is not None else None, _addr(dX), _addr(dA), _addr(dB),
+            1 if accumulate else 0, _addr(ws), wsb)
     return dX, dA, dB
 
 

@@ -751,25 +751,38 @@ int launch_wide(Q4GLinearArgs a, hipStream_t stream) {
     return launch_lds(q4g_linear_wide_kernel<RT, TT, NW, GL, SF32>, grid, 64 * NW, lds, a, stream);
 }
 
-// The variant by tokens and rows. One row tile a workgroup gives the most
+// The variant by tokens and tiles. One row tile a workgroup gives the most
 // workgroups and the least code, two read x (and fetch instructions) half as
 // often; what was measured (us, one | two row tiles, groups of 128 unless said):
 //   T = 1   4096 x 4096 5.0 | 6.5, 11008 x 4096 (32) 9.5 | 11.0, 22016 x 8192 26.8 | 24.4
 //   T = 8   4096 x 4096 5.3 | 7.0, 22016 x 8192 36.9 | 28.0
-//   T = 16  4096 x 4096 5.9 | 9.5, 11008 x 4096 (64) 11.6 | 13.2, 22016 x 8192 41.4 | 31.2
-//   T = 37  4096 x 4096 9.2 | 12.9, 11008 x 4096 (32) 28.2 | 23.4
-//   T = 64  4096 x 11008 24.4 | 31.9, 11008 x 4096 29.7 | 21.9, 22016 x 8192 (64) 106 | 83
-// so two from four workgroups a CU on (1024), from two (512) for more than a
-// tile of tokens.
+//   T = 16  4096 x 4096 6.0 | 9.5, 11008 x 4096 (64) 11.6 | 13.2, 22016 x 8192 40.1 | 31.2
+// so up to 16 tokens two from four workgroups a CU on (1024). Beyond, counting
+// the token tiles too (one, 8 waves | two, 8 waves | two, 4 waves):
+//   256 workgroups or fewer   T = 37 4096 x 4096 9.3 | 10.9 | 12.8, T = 64 4096 x 11008 23.8 | 25.3 | 31.3
+//   512                       T = 128 4096 x 4096 20.0 | 13.7 | 16.2, 4096 x 11008 43.2 | 28.0 | 32.8
+//   688                       T = 37 11008 x 4096 (32) 28.4 | 24.7 | 23.1, T = 64 29.2 | 25.2 | 21.4
+//   1024 and more             T = 200 4096 x 4096 38.4 | 25.6 | 23.5, T = 64 22016 x 8192 101 | 65.4 | 62.6,
+//                             T = 64 22016 x 4096 (64, the last two) 43.5 | 37.4, (32) 45.7 | 57.7,
+//                             T = 128 11008 x 4096 (32) 60 | 43.2 | 55.3
+// (the operands for -z of groups of 32 leave registers for fewer small workgroups).
+template <int TT, int GL, bool SF32>
+int launch_wide_variant(const Q4GLinearArgs& a, hipStream_t stream) {
+    const int64_t tiles = ceil_div(a.N, 16) * ceil_div(a.T, 16 * TT);
+    if (tiles <= 256) return launch_wide<1, TT, 8, GL, SF32>(a, stream);
+    if (tiles <= 512 || (GL == 5 && tiles >= 1024)) return launch_wide<2, TT, 8, GL, SF32>(a, stream);
+    return launch_wide<2, TT, 4, GL, SF32>(a, stream);
+}
+
 template <int GL, bool SF32>
 int launch_linear_variant(const Q4GLinearArgs& a, hipStream_t stream) {
-    const bool two = ceil_div(a.N, 16) > (a.T <= 16 ? 1024 : 512);
+    const bool two = ceil_div(a.N, 16) > 1024;
     if (a.T <= 4) return two ? launch_narrow<2, 1, 1, GL, SF32>(a, stream) : launch_narrow<1, 1, 2, GL, SF32>(a, stream);
     if (a.T <= 8) return two ? launch_narrow<2, 2, 1, GL, SF32>(a, stream) : launch_narrow<1, 2, 2, GL, SF32>(a, stream);
     if (a.T <= 16) return two ? launch_wide<2, 1, 4, GL, SF32>(a, stream) : launch_wide<1, 1, 8, GL, SF32>(a, stream);
-    if (a.T <= 32) return two ? launch_wide<2, 2, 4, GL, SF32>(a, stream) : launch_wide<1, 2, 8, GL, SF32>(a, stream);
-    if (a.T <= 48) return two ? launch_wide<2, 3, 4, GL, SF32>(a, stream) : launch_wide<1, 3, 8, GL, SF32>(a, stream);
-    return two ? launch_wide<2, 4, 4, GL, SF32>(a, stream) : launch_wide<1, 4, 8, GL, SF32>(a, stream);
+    if (a.T <= 32) return launch_wide_variant<2, GL, SF32>(a, stream);
+    if (a.T <= 48) return launch_wide_variant<3, GL, SF32>(a, stream);
+    return launch_wide_variant<4, GL, SF32>(a, stream);
 }
 
 template <bool WF32, int G, bool SF32>

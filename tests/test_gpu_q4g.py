@@ -207,6 +207,18 @@ def test_linear_variants(qn, T, N, K, group, sd, sym):
     assert float(err.norm()) <= 2.0 ** -8 * float(y.norm())
 
 
+@pytest.mark.parametrize("T,N,K,group,sd", [
+    (33, 4128, 1032, 64, torch.bfloat16),    # 259 workgroups of a row tile: two row tiles, 8 waves
+    (100, 4090, 776, 128, torch.float32),    # 512
+    (130, 4090, 776, 32, torch.bfloat16),    # 768: two row tiles, 4 waves
+    (20, 16500, 264, 32, torch.float32),     # 1032 with short groups: 8 waves again
+    (64, 16500, 1288, 32, torch.bfloat16),
+])
+@pytest.mark.parametrize("sym", [False, True])
+def test_linear_workgroup_rule(qn, T, N, K, group, sd, sym):
+    test_linear_variants(qn, T, N, K, group, sd, sym)
+
+
 def test_padding_and_memory_behind_the_arrays(qn):
     """Codes past K, rows behind the last token and behind the output do not
     matter and stay as they were."""

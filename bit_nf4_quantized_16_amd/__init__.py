@@ -529,7 +529,7 @@ def qlora_linear_bwd_act8(w, X8, dY, A=None, B=None, scale=1.0, U=None, need_dx=
     if not isinstance(dY, torch.Tensor) or dY.dim() != 2:
         _refuse(_lib.QL_ERR_SHAPE, "dY is not 2-D")
     T, dev = dY.shape[0], dY.device
-    _tensor(dY, "dY", torch.bfloat16, (T, w.rows))
+    _tensor(dY, "dY", torch.bfloat16, (T, w.rows), w.packed.device)
     r = _adapters(A, B, w.rows, w.cols, dev)
     dX = torch.empty(T, w.cols, dtype=torch.bfloat16, device=dev) if need_dx else None
     dA = _grads(r > 0 and need_da, dA, (r, w.cols), "dA", accumulate, dev)
@@ -543,15 +543,17 @@ def qlora_linear_bwd_act8(w, X8, dY, A=None, B=None, scale=1.0, U=None, need_dx=
             _refuse(_lib.QL_ERR_SHAPE, "X8 is %d x %d on %s, expected %d x %d on %s"
                     % (X8.rows, X8.cols, X8.codes.device, T, w.cols, dev))
     if keep is not None:
-        _tensor(keep.view(T, -1), "keep", torch.uint8, (T, w.cols // 8), dev)
+        if not isinstance(keep, torch.Tensor) or keep.numel() != T * (w.cols // 8):
+            _refuse(_lib.QL_ERR_SHAPE, "keep is no tensor of %d x %d bytes" % (T, w.cols // 8))
+        _tensor(keep, "keep", torch.uint8, keep.shape, dev)
     ws, wsb = _workspace(lib.qlora_linear_bwd_act8_workspace(w.rows, w.cols, max(T, 1), r, keep is not None), dev)
     if T == 0:  # no token: the sums are empty
         for g in (dA, dB):
             if g is not None and not accumulate:
                 g.zero_()
         return dX, dA, dB
-    _launch(dev, lib.qlora_linear_bwd_act8, w.descriptor(), x8, dY.data_ptr(), T, _addr(A), _addr(B), r, scale,
-            _addr(keep), p, _addr(U) if dB is not None else None, _addr(dX), _addr(dA), _addr(dB),
+    _launch(dev, lib.qlora_linear_bwd_act8, w.descriptor(), x8, dY.data_ptr(), T, _addr(A), _addr(B), r, float(scale),
+            _addr(keep), float(p), _addr(U) if dB is not None else None, _addr(dX), _addr(dA), _addr(dB),
             1 if accumulate else 0, _addr(ws), wsb)
     return dX, dA, dB
 
@@ -563,19 +565,24 @@ def qlora_linear_bwd_group_act8(ws, X8, dYs, As=None, Bs=None, scale=1.0, Us=Non
     nw = len(ws)
     if nw < 1 or len(dYs) != nw:
         _refuse(_lib.QL_ERR_SHAPE, "%d weights and %d dY" % (nw, len(dYs)))
+    for name, ts in (("As", As), ("Bs", Bs), ("Us", Us), ("dAs", dAs), ("dBs", dBs)):
+        if ts is not None and len(ts) != nw:
+            _refuse(_lib.QL_ERR_SHAPE, "%d weights and %d %s" % (nw, len(ts), name))
     T = _matrix(dYs[0], "dY").shape[0]
     dev = dYs[0].device
     cols = ws[0].cols
     r = 0
+    pick = lambda ts, i: ts[i] if ts is not None else None
     for i, w in enumerate(ws):
         _tensor(dYs[i], "dY", torch.bfloat16, (T, w.rows), dev)
-        ri = _adapters(As[i] if As is not None else None, Bs[i] if As is not None else None, w.rows, cols, dev)
+        if w.packed.device != dev:
+            _refuse(_lib.QL_ERR_UNSUPPORTED, "weight %d is on %s, dY on %s" % (i, w.packed.device, dev))
+        ri = _adapters(pick(As, i), pick(Bs, i), w.rows, cols, dev)
         if i > 0 and ri != r:
             _refuse(_lib.QL_ERR_SHAPE, "layer %d has rank %d, layer 0 rank %d" % (i, ri, r))
         r = ri
     dX = torch.empty(T, cols, dtype=torch.bfloat16, device=dev) if need_dx else None
     need_da, need_db = need_da and r > 0, need_db and r > 0
-    pick = lambda ts, i: ts[i] if ts is not None else None
     dAs = [_grads(need_da, pick(dAs, i), (r, cols), "dA", accumulate, dev) for i in range(nw)] if need_da else None
     dBs = [_grads(need_db, pick(dBs, i), (w.rows, r), "dB", accumulate, dev) for i, w in enumerate(ws)] if need_db else None
     if need_db:
@@ -625,6 +632,8 @@ class Q4GWeight:
         dev = self.packed.device
         if self.scale.dtype not in _DTYPES:
             _refuse(_lib.QL_ERR_UNSUPPORTED, "scale is %s, expected bf16 or fp32" % self.scale.dtype)
+        if self.group not in (32, 64, 128):
+            _refuse(_lib.QL_ERR_UNSUPPORTED, "group %s (32, 64 or 128)" % (self.group,))
         groups = (self.rows, -(-self.cols // self.group))
         _tensor(self.packed, "packed", torch.uint8, (self.rows, 16 * -(-self.cols // 32)))
         _tensor(self.scale, "scale", self.scale.dtype, groups, dev)
@@ -746,7 +755,7 @@ class QLoRALinearFunction(torch.autograd.Function):
         X, A, B, U = ctx.saved_tensors
         dX, dA, dB = qlora_linear_bwd(ctx.w, X, dY.contiguous().to(torch.bfloat16), A, B, ctx.scale, U=U,
                                       need_dx=ctx.needs_input_grad[0], keep=ctx.keep, p=ctx.p)
-        return dX, dA.to(A.dtype), dB.to(B.dtype), None, None, None, None
+        return dX, dA.to(A.dtype), dB.to(B.dtype), None, None, None, None, None
 
 
 class QLoRAGroupFunction(torch.autograd.Function):

@@ -56,9 +56,10 @@ __device__ __forceinline__ uint32_t row_of(uint32_t n, const RowDivisor& r, uint
 // ends. Quotients are correctly rounded fp32: the product with the correctly
 // rounded reciprocal, corrected once by its exact remainder (Markstein's
 // theorem), three operations instead of a division's ten; adding 1.5 2^23
-// rounds to an integer, ties to even, in the low bits. The arithmetic is what
-// bounds it next to HBM (the same with divisions, float maxima and a 64-bit
-// index division: 34 us at 11008 x 4096 from bf16).
+// rounds to an integer, ties to even, in the low bits. 11008 x 4096 from bf16
+// takes 24.4 us (114 MB, 4.7 TB/s: HBM), 4096 x 4096 from fp32 13.7; with
+// divisions, float maxima and a 64-bit index division the arithmetic bounds it
+// (34 us).
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ int imax_(int a, int b) { return a > b ? a : b; }
 
@@ -163,7 +164,8 @@ __global__ __launch_bounds__(kThreads) void q4g_quantize_kernel(const void* __re
 
 // ---------------------------------------------------------------------------
 // Expand: w' = s (q - z) in fp32 (one rounding), rounded to bf16 for the bf16
-// output. A lane expands eight values. HBM-bound.
+// output. A lane expands eight values. HBM-bound: 11008 x 4096 in 18.5 us
+// (114 MB, 6.2 TB/s, the codes from the last-level cache).
 // ---------------------------------------------------------------------------
 template <bool BF16, bool SF32>
 __global__ __launch_bounds__(kThreads) void q4g_dequantize_kernel(Q4GDev w, uint32_t N, uint32_t K, RowDivisor units,
@@ -220,18 +222,47 @@ __global__ __launch_bounds__(kThreads) void q4g_dequantize_kernel(Q4GDev w, uint
 //
 // Where a result is not finite (an infinite or NaN x, or sums that overflow
 // only because q and z are apart), it is formed again value by value as
-// x s (q - z): the formula's infinities, not the difference of two.
+// x s (q - z): the formula's infinities, not the difference of two. The wave
+// does so together, 512 values a step, and stops at a NaN: rows of a padded
+// batch may hold anything.
 // ---------------------------------------------------------------------------
 template <bool SF32>
-__device__ __forceinline__ float q4g_dot(const Q4GDev& w, const uint16_t* x, int64_t n, int64_t K) {
+__device__ float q4g_dot(const Q4GDev& w, const uint16_t* x, int64_t n, int64_t K, int lane) {
     float y = 0.0f;
     const int64_t ng = ceil_div(K, w.group), rowbytes = ceil_div(K, 32) * 16;
-    for (int64_t k = 0; k < K; ++k) {
-        const uint32_t b = w.packed[n * rowbytes + k / 2];
-        const int64_t gi = n * ng + k / w.group;
-        const int q = static_cast<int>(k % 2 ? b & 15u : b >> 4);
-        const int z = w.zero != nullptr ? w.zero[gi] : 8;
-        y = __builtin_fmaf(bf16_to_f32(x[k]), static_cast<float>(q - z) * load_scale<SF32>(w.scale, gi), y);
+    const int gl = __builtin_ctz(w.group);
+    for (int64_t k0 = 0; k0 < K; k0 += 512) {
+        const int64_t k = k0 + 8 * lane;
+        if (k < K) {
+            const uint32_t c = *reinterpret_cast<const uint32_t*>(w.packed + n * rowbytes + k / 2);
+            const uint4 xv = *reinterpret_cast<const uint4*>(x + k);
+            const int64_t gi = n * ng + (k >> gl);
+            const float sc = load_scale<SF32>(w.scale, gi);
+            const int z = w.zero != nullptr ? w.zero[gi] : 8;
+            const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int q = static_cast<int>(c >> (8 * (j / 2) + (j % 2 ? 0 : 4)) & 15u);
+                const uint32_t xb = j % 2 ? xw[j / 2] >> 16 : xw[j / 2] & 0xFFFFu;
+                y = __builtin_fmaf(bf16_to_f32(xb), static_cast<float>(q - z) * sc, y);
+            }
+        }
+        if (__any(y != y)) return __builtin_nanf("");
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) y += __shfl_xor(y, d);
+    return y;
+}
+
+// The wave's results y (of token tl and row nl behind X and n0, where live),
+// those that are not finite formed again, one after the other.
+template <bool SF32>
+__device__ __forceinline__ float q4g_finite(float y, bool live, const Q4GDev& w, const uint16_t* X, int tl, int64_t n0,
+                                            int nl, int64_t K, int lane) {
+    for (uint64_t bad = __ballot(live && !(fabsf(y) < __builtin_inff())); bad != 0; bad &= bad - 1) {
+        const int l = __builtin_ctzll(bad);
+        const float v = q4g_dot<SF32>(w, X + __builtin_amdgcn_readlane(tl, l) * K, n0 + __builtin_amdgcn_readlane(nl, l), K, lane);
+        if (lane == l) y = v;
     }
     return y;
 }
@@ -486,13 +517,12 @@ __global__ __launch_bounds__(512) void q4g_linear_kernel(Q4GLinearArgs p) {
         __syncthreads();
         for (int e = tid; e < 64 * TX; e += 64 * NW) {
             const int tl = e >> 4, nl = 16 * rt + (e & 15);
-            if (tl >= ntok || nl >= nrows) continue;
+            const bool live = tl < ntok && nl < nrows;
             float y = 0.0f;
 #pragma unroll
             for (int ww = 0; ww < NW; ++ww) y += reinterpret_cast<const float*>(lds + ww * kSlot)[e];
-            const int64_t n = n0 + nl;
-            if (!(fabsf(y) < __builtin_inff())) y = q4g_dot<SF32>(p.w, p.X + tl * K, n, K);
-            p.Y[tl * N + n] = to_bf16_bits(y);
+            y = q4g_finite<SF32>(y, live, p.w, p.X, tl, n0, nl, K, lane);
+            if (live) p.Y[tl * N + n0 + nl] = to_bf16_bits(y);
         }
     }
 }
@@ -502,6 +532,15 @@ __global__ __launch_bounds__(512) void q4g_linear_kernel(Q4GLinearArgs p) {
 // takes no registers on the way, and every x operand serves RT row tiles. The
 // next chunk's codes load while a chunk is multiplied, its x once the slot has
 // been read; the SIMD's other wave works meanwhile.
+//
+// What bounds it: vector instructions (unpacking, constants and the ends of
+// groups, about 160 a chunk, wave and three token tiles with groups of 32, 640
+// cycles against 384 of MFMA), and the way in and out of a workgroup. Measured
+// and not kept: x in two halves, one on its way while the other is used, codes
+// a chunk ahead (within 3 %, so the loads are not what is waited for); waves
+// side by side on one chunk's x (a quarter of x's way from L2, but a barrier a
+// step lines the waves up and fewer workgroups fill the chip less: T = 37 at
+// 11008 x 4096 23.1 -> 25.4 us, at 4096 x 4096 9.2 -> 15.8).
 template <int RT, int TT, int NW, int GL, bool SF32>
 __global__ __launch_bounds__(64 * NW) void q4g_linear_wide_kernel(Q4GLinearArgs p) {
     constexpr int NG = 128 >> GL, MG = 4 / NG;
@@ -701,13 +740,12 @@ __global__ __launch_bounds__(64 * NW) void q4g_linear_wide_kernel(Q4GLinearArgs 
         __syncthreads();
         for (int e = tid; e < TT * 256; e += 64 * NW) {
             const int tl = e >> 4, nl = 16 * rt + (e & 15);
-            if (tl >= ntok || nl >= nrows) continue;
+            const bool live = tl < ntok && nl < nrows;
             float y = 0.0f;
 #pragma unroll
             for (int ww = 0; ww < NW; ++ww) y += reinterpret_cast<const float*>(lds + ww * kSlot)[e];
-            const int64_t t = t0 + tl, n = n0 + nl;
-            if (!(fabsf(y) < __builtin_inff())) y = q4g_dot<SF32>(p.w, p.X + t * K, n, K);
-            p.Y[t * N + n] = to_bf16_bits(y);
+            y = q4g_finite<SF32>(y, live, p.w, p.X + t0 * K, tl, n0, nl, K, lane);
+            if (live) p.Y[(t0 + tl) * N + n0 + nl] = to_bf16_bits(y);
         }
     }
 }

@@ -375,16 +375,15 @@ def _refuse(status, message):
 def _tensor(t, name, dtype, shape, device=None):
     """t, checked: a contiguous device tensor of this dtype and shape (on
     ``device`` where given)."""
-    shape = tuple(shape)
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda
-            and (device is None or t.device == device)):
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            and (t.is_cuda if device is None else t.device == device)):
         return t
     if not isinstance(t, torch.Tensor):
         _refuse(_lib.QL_ERR_NULL, "%s is no tensor" % name)
     if t.dtype != dtype:
         _refuse(_lib.QL_ERR_UNSUPPORTED, "%s is %s, expected %s" % (name, t.dtype, dtype))
     if t.shape != shape:
-        _refuse(_lib.QL_ERR_SHAPE, "%s is %s, expected %s" % (name, tuple(t.shape), shape))
+        _refuse(_lib.QL_ERR_SHAPE, "%s is %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     if not t.is_contiguous():
         _refuse(_lib.QL_ERR_UNSUPPORTED, "%s is not contiguous" % name)
     _refuse(_lib.QL_ERR_UNSUPPORTED, "%s is on %s, expected %s" % (name, t.device, device or "a GPU"))
@@ -494,9 +493,11 @@ def swiglu_fwd(gate, up, checkpoint=True, h8=False):
 def swiglu_bwd(gate8, up8, dH):
     """(dgate, dup) bf16 of swiglu_fwd from its checkpoints and dH bf16."""
     dg, du = gate8.descriptor(), up8.descriptor()
-    dev = gate8.codes.device
-    _tensor(dH, "dH", torch.bfloat16, (gate8.rows, gate8.cols), dev)
-    _tensor(up8.codes, "up8", torch.uint8, (gate8.rows, gate8.cols), dev)
+    dev, shape = gate8.codes.device, (gate8.rows, gate8.cols)
+    _tensor(dH, "dH", torch.bfloat16, shape, dev)
+    if (up8.rows, up8.cols) != shape or up8.codes.device != dev:
+        _refuse(_lib.QL_ERR_SHAPE, "up8 is %d x %d on %s, gate8 %d x %d on %s"
+                % (up8.rows, up8.cols, up8.codes.device, *shape, dev))
     dgate, dup = torch.empty_like(dH), torch.empty_like(dH)
     _launch(dev, lib.qlora_swiglu_bwd, dg, du, dH.data_ptr(), dgate.data_ptr(), dup.data_ptr())
     return dgate, dup
@@ -629,18 +630,19 @@ class Q4GWeight:
         return n + (self.zero.numel() if self.zero is not None else 0)
 
     def descriptor(self):
-        dev = self.packed.device
-        if self.scale.dtype not in _DTYPES:
-            _refuse(_lib.QL_ERR_UNSUPPORTED, "scale is %s, expected bf16 or fp32" % self.scale.dtype)
-        if self.group not in (32, 64, 128):
-            _refuse(_lib.QL_ERR_UNSUPPORTED, "group %s (32, 64 or 128)" % (self.group,))
-        groups = (self.rows, -(-self.cols // self.group))
-        _tensor(self.packed, "packed", torch.uint8, (self.rows, 16 * -(-self.cols // 32)))
-        _tensor(self.scale, "scale", self.scale.dtype, groups, dev)
-        if self.zero is not None:
-            _tensor(self.zero, "zero", torch.uint8, groups, dev)
-        return _lib.QlQ4GWeight(self.rows, self.cols, self.group, _DTYPES[self.scale.dtype], self.packed.data_ptr(),
-                                self.scale.data_ptr(), self.zero.data_ptr() if self.zero is not None else None)
+        rows, cols, group, packed, scale, zero = self.rows, self.cols, self.group, self.packed, self.scale, self.zero
+        if group not in (32, 64, 128):
+            _refuse(_lib.QL_ERR_UNSUPPORTED, "group %s (32, 64 or 128)" % (group,))
+        groups = (rows, -(-cols // group))
+        _tensor(packed, "packed", torch.uint8, (rows, 16 * -(-cols // 32)))
+        dev = packed.device
+        code = _DTYPES.get(scale.dtype) if isinstance(scale, torch.Tensor) else None
+        if code is None:
+            _refuse(_lib.QL_ERR_UNSUPPORTED, "scale is no bf16 or fp32 tensor")
+        _tensor(scale, "scale", scale.dtype, groups, dev)
+        if zero is not None:
+            _tensor(zero, "zero", torch.uint8, groups, dev)
+        return _lib.QlQ4GWeight(rows, cols, group, code, packed.data_ptr(), scale.data_ptr(), _addr(zero))
 
 
 _DTYPES = {torch.float32: _lib.QL_F32, torch.bfloat16: _lib.QL_BF16}
@@ -681,14 +683,16 @@ def q4g_dequantize(w, dtype=torch.bfloat16, out=None):
 def q4g_linear_fwd(w, X, out=None):
     """Y = X W'^T (bf16 [T, rows]) on a Q4GWeight, X bf16 [T, cols]; made for
     decoding (up to 64 tokens read the weight once)."""
-    T = _matrix(X, "X").shape[0]
-    dev = w.packed.device
+    if not isinstance(X, torch.Tensor) or X.dim() != 2:
+        _refuse(_lib.QL_ERR_SHAPE, "X is not 2-D")
+    d = w.descriptor()
+    T, dev = X.shape[0], w.packed.device
     _tensor(X, "X", torch.bfloat16, (T, w.cols), dev)
     if out is None:
         out = torch.empty(T, w.rows, dtype=torch.bfloat16, device=dev)
     else:
         _tensor(out, "out", torch.bfloat16, (T, w.rows), dev)
-    _launch(dev, lib.q4g_linear_fwd, w.descriptor(), X.data_ptr(), T, out.data_ptr())
+    _launch(dev, lib.q4g_linear_fwd, d, X.data_ptr(), T, out.data_ptr())
     return out
 
 

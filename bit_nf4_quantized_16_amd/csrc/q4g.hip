@@ -533,14 +533,16 @@ __global__ __launch_bounds__(512) void q4g_linear_kernel(Q4GLinearArgs p) {
 // next chunk's codes load while a chunk is multiplied, its x once the slot has
 // been read; the SIMD's other wave works meanwhile.
 //
-// What bounds it: vector instructions (unpacking, constants and the ends of
-// groups, about 160 a chunk, wave and three token tiles with groups of 32, 640
-// cycles against 384 of MFMA), and the way in and out of a workgroup. Measured
-// and not kept: x in two halves, one on its way while the other is used, codes
-// a chunk ahead (within 3 %, so the loads are not what is waited for); waves
-// side by side on one chunk's x (a quarter of x's way from L2, but a barrier a
-// step lines the waves up and fewer workgroups fill the chip less: T = 37 at
-// 11008 x 4096 23.1 -> 25.4 us, at 4096 x 4096 9.2 -> 15.8).
+// What bounds it: vector instructions on the CU with the most row tiles
+// (unpacking, constants and the ends of groups; two row tiles and three of
+// tokens with groups of 32 take 250 a chunk, 1000 cycles against 768 of MFMA),
+// and a workgroup's way in and out, as many again over a wave's few chunks. So
+// the tiles are dealt out evenly (launch_wide_variant; T = 37 at 11008 x 4096,
+// groups of 32: 23.1 -> 19.7 us). Measured and not kept: x in two halves, one on
+// its way while the other is used, codes a chunk ahead (within 3 %, so the loads
+// are not what is waited for); waves side by side on one chunk's x (a quarter of
+// x's way from L2, but a barrier a step lines the waves up: 25.4 us, and 15.8
+// for 9.2 at 4096 x 4096).
 template <int RT, int TT, int NW, int GL, bool SF32>
 __global__ __launch_bounds__(64 * NW) void q4g_linear_wide_kernel(Q4GLinearArgs p) {
     constexpr int NG = 128 >> GL, MG = 4 / NG;
@@ -634,6 +636,20 @@ __global__ __launch_bounds__(64 * NW) void q4g_linear_wide_kernel(Q4GLinearArgs 
                 cw[rt][q] = sw[0], cw[rt][q + 1] = sw[1];
             }
         }
+        // a tile's sums of a group, times the scale, to the totals. Left alone the
+        // compiler puts this off to the chunk's end and holds the sums of all groups
+        // till then: a little faster where there are registers (1 to 5 %), but three
+        // row tiles spill (T = 64 at 11008 x 4096, groups of 32: 62 us, pinned 23)
+        auto add_part = [&](const f32x4 (&acc)[TT], float sc, int rt) {
+#pragma unroll
+            for (int tt = 0; tt < TT; ++tt) {
+#pragma unroll
+                for (int rr = 0; rr < 4; ++rr) tot[rt][tt][rr] = __builtin_fmaf(sc, acc[tt][rr], tot[rt][tt][rr]);
+                if constexpr (RT > 2 || RT * TT > 6) asm volatile("" : "+v"(tot[rt][tt]));
+            }
+        };
+        f32x4 part[2][TT];
+        float spart = 0.0f;
 #pragma unroll
         for (int q = 0; q < NG; ++q) {
             // the rows' scales and zero points (past the last group x is zero)
@@ -645,56 +661,74 @@ __global__ __launch_bounds__(64 * NW) void q4g_linear_wide_kernel(Q4GLinearArgs 
                 sv[rt] = __uint_as_float(SF32 ? e[0] : e[0] & 0xFFFF0000u);
                 zv[rt] = (SF32 ? e[1] : e[0]) & 0xFFu;
             }
-            f32x4 acc[RT][TT], xs[TT];
-            bf16x8_t zop[RT];
+            if constexpr (kZeroOperand) {
+                // -z as an operand: 8 for all, or the row's; a row tile's sums at a time
+                bf16x8_t xv[MG][TT];
 #pragma unroll
-            for (int tt = 0; tt < TT; ++tt) xs[tt] = f32x4{0.f, 0.f, 0.f, 0.f};
+                for (int mm = 0; mm < MG; ++mm)
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
+                    for (int tt = 0; tt < TT; ++tt) xv[mm][tt] = xin(tt, q * MG + mm);
 #pragma unroll
-                for (int tt = 0; tt < TT; ++tt) acc[rt][tt] = f32x4{0.f, 0.f, 0.f, 0.f};
-                if constexpr (kZeroOperand) {  // -z as an operand: 8 for all, or the row's
+                for (int rt = 0; rt < RT; ++rt) {
                     uint32_t zz = 0xC100C100u;
                     if (has_zero) {
                         zz = __float_as_uint(-static_cast<float>(zv[rt]));
                         zz = __builtin_amdgcn_perm(zz, zz, 0x07060302u);
                     }
-                    zop[rt] = as_bf16x8(make_uint4(zz, zz, zz, zz));
-                }
-            }
+                    const bf16x8_t zop = as_bf16x8(make_uint4(zz, zz, zz, zz));
+                    f32x4 (&acc)[TT] = part[(q * RT + rt) & 1];
 #pragma unroll
-            for (int mm = 0; mm < MG; ++mm) {
-                const int m = q * MG + mm;
-                bf16x8_t xv[TT];
+                    for (int tt = 0; tt < TT; ++tt) acc[tt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int mm = 0; mm < MG; ++mm) {
+                        const bf16x8_t wv = q4g_operand_ordered(cw[rt][q * MG + mm]);
+#pragma unroll
+                        for (int tt = 0; tt < TT; ++tt) {
+                            acc[tt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[mm][tt], zop, acc[tt], 0, 0, 0);
+                            acc[tt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[mm][tt], wv, acc[tt], 0, 0, 0);
+                        }
+                    }
+                    // the tile before, whose products are done by now
+                    if (q * RT + rt > 0) add_part(part[(q * RT + rt + 1) & 1], spart, (rt + RT - 1) % RT);
+                    spart = sv[rt];
+                }
+            } else {
+                f32x4 acc[RT][TT], xs[TT];
 #pragma unroll
                 for (int tt = 0; tt < TT; ++tt) {
-                    xv[tt] = xin(tt, m);
-                    if constexpr (!kZeroOperand)
-                        xs[tt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[tt], ones, xs[tt], 0, 0, 0);
+                    xs[tt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) acc[rt][tt] = f32x4{0.f, 0.f, 0.f, 0.f};
                 }
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    const bf16x8_t wv = q4g_operand_ordered(cw[rt][m]);
+                for (int mm = 0; mm < MG; ++mm) {
+                    const int m = q * MG + mm;
+                    bf16x8_t xv[TT];
 #pragma unroll
                     for (int tt = 0; tt < TT; ++tt) {
-                        if constexpr (kZeroOperand)
-                            acc[rt][tt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[tt], zop[rt], acc[rt][tt], 0, 0, 0);
-                        acc[rt][tt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[tt], wv, acc[rt][tt], 0, 0, 0);
+                        xv[tt] = xin(tt, m);
+                        xs[tt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[tt], ones, xs[tt], 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) {
+                        const bf16x8_t wv = q4g_operand_ordered(cw[rt][m]);
+#pragma unroll
+                        for (int tt = 0; tt < TT; ++tt)
+                            acc[rt][tt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[tt], wv, acc[rt][tt], 0, 0, 0);
                     }
                 }
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+                        for (int rr = 0; rr < 4; ++rr) {
+                            const float d = __builtin_fmaf(-static_cast<float>(zv[rt]), xs[tt][rr], acc[rt][tt][rr]);
+                            tot[rt][tt][rr] = __builtin_fmaf(sv[rt], d, tot[rt][tt][rr]);
+                        }
             }
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                for (int tt = 0; tt < TT; ++tt)
-#pragma unroll
-                    for (int rr = 0; rr < 4; ++rr) {
-                        const float d = kZeroOperand ? acc[rt][tt][rr]
-                                                     : __builtin_fmaf(-static_cast<float>(zv[rt]), xs[tt][rr], acc[rt][tt][rr]);
-                        tot[rt][tt][rr] = __builtin_fmaf(sv[rt], d, tot[rt][tt][rr]);
-                    }
-            if constexpr (NG > 1 && RT * TT > 4) __builtin_amdgcn_sched_barrier(0);  // one group's sums at a time
         }
+        if constexpr (kZeroOperand) add_part(part[(NG * RT + 1) & 1], spart, RT - 1);
     };
 
     const int nch = last + 1, sch = static_cast<int>(p.slice / 128);
@@ -789,34 +823,51 @@ int launch_wide(Q4GLinearArgs a, hipStream_t stream) {
     return launch_lds(q4g_linear_wide_kernel<RT, TT, NW, GL, SF32>, grid, 64 * NW, lds, a, stream);
 }
 
-// The variant by tokens and tiles. One row tile a workgroup gives the most
-// workgroups and the least code, two read x (and fetch instructions) half as
-// often; what was measured (us, one | two row tiles, groups of 128 unless said):
-//   T = 1   4096 x 4096 5.0 | 6.5, 11008 x 4096 (32) 9.5 | 11.0, 22016 x 8192 26.8 | 24.4
-//   T = 8   4096 x 4096 5.3 | 7.0, 22016 x 8192 36.9 | 28.0
-//   T = 16  4096 x 4096 6.0 | 9.5, 11008 x 4096 (64) 11.6 | 13.2, 22016 x 8192 40.1 | 31.2
-// so up to 16 tokens two from four workgroups a CU on (1024). Beyond, counting
-// the token tiles too (one, 8 waves | two, 8 waves | two, 4 waves):
-//   256 workgroups or fewer   T = 37 4096 x 4096 9.3 | 10.9 | 12.8, T = 64 4096 x 11008 23.8 | 25.3 | 31.3
-//   512                       T = 128 4096 x 4096 20.0 | 13.7 | 16.2, 4096 x 11008 43.2 | 28.0 | 32.8
-//   688                       T = 37 11008 x 4096 (32) 28.4 | 24.7 | 23.1, T = 64 29.2 | 25.2 | 21.4
-//   1024 and more             T = 200 4096 x 4096 38.4 | 25.6 | 23.5, T = 64 22016 x 8192 101 | 65.4 | 62.6,
-//                             T = 64 22016 x 4096 (64, the last two) 43.5 | 37.4, (32) 45.7 | 57.7,
-//                             T = 128 11008 x 4096 (32) 60 | 43.2 | 55.3
-// (the operands for -z of groups of 32 leave registers for fewer small workgroups).
+// The variant of the wide kernel. A CU's work is its share of the row tiles,
+// so the tiles a workgroup takes (RT) are those with the least of them on the
+// fullest CU, RT ceil(workgroups / 256); of equals the most, which read x (and
+// fetch instructions) least often. Measured (us; 16 x RT rows by NW waves
+// 1x8 | 2x8 | 2x4 | 3x8 | 3x4, groups of 128 unless said):
+//   256 tiles   T = 37 4096 x 4096 9.3 | 10.9 | 12.8, T = 64 4096 x 11008 23.8 | 25.3 | 31.3 | 30.5 | 38.1
+//   512         T = 128 4096 x 4096 20.0 | 13.7 | 16.2, T = 37 8192 x 8192 - | 19.1 | - | 22.1 | 25.5
+//   640         T = 37 10240 x 8192 - | - | 28.4 | 22.6 | 26.2, (32) 43.6 | 37.4 | 46.1 for the last three
+//   688         T = 37 11008 x 4096 (32) 28.4 | 24.7 | 23.1 | 19.8 | 22.4, T = 64 29.2 | 25.2 | 21.4 | 18.0 | 20.5
+//   1024        T = 200 4096 x 4096 38.4 | 25.6 | 23.5
+//   1376        T = 64 22016 x 8192 101 | 65.4 | 62.4 | 54.8 | 52.5, (64) 107 | 71.6 | 84 | 65 | 75,
+//               (32) - | 87 | - | 86 | 105, T = 37 - | - | 56.5 | 45.5 | 42.7
+// Eight waves where each CU gets one workgroup; beyond, four (and two of them)
+// but for short groups with many tokens, whose registers leave no room for two
+// (T = 200 4096 x 4096 (32) 31 | 37 with eight and four; T = 40 13824 x 5120 (32)
+// 31.4 | 29.5).
 template <int TT, int GL, bool SF32>
 int launch_wide_variant(const Q4GLinearArgs& a, hipStream_t stream) {
-    const int64_t tiles = ceil_div(a.N, 16) * ceil_div(a.T, 16 * TT);
-    if (tiles <= 256) return launch_wide<1, TT, 8, GL, SF32>(a, stream);
-    if (tiles <= 512 || (GL == 5 && tiles >= 1024)) return launch_wide<2, TT, 8, GL, SF32>(a, stream);
-    return launch_wide<2, TT, 4, GL, SF32>(a, stream);
+    auto blocks = [&](int rt) { return ceil_div(a.N, 16 * rt) * ceil_div(a.T, 16 * TT); };
+    auto most = [&](int rt) { return rt * ceil_div(blocks(rt), 256); };
+    if (most(3) <= std::min(most(1), most(2))) {
+        if (blocks(3) <= 256 || (TT == 4 && GL < 7)) return launch_wide<3, TT, 8, GL, SF32>(a, stream);
+        return launch_wide<3, TT, 4, GL, SF32>(a, stream);
+    }
+    if (most(2) <= most(1)) {
+        if (blocks(2) <= 256 || (TT == 4 && GL == 5)) return launch_wide<2, TT, 8, GL, SF32>(a, stream);
+        return launch_wide<2, TT, 4, GL, SF32>(a, stream);
+    }
+    return launch_wide<1, TT, 8, GL, SF32>(a, stream);
 }
 
+// The variant by tokens. Up to 8 of them (16 with short groups) two row tiles
+// from four workgroups a CU on (1024), one before (us, one | two):
+//   T = 1   4096 x 4096 5.0 | 6.5, 11008 x 4096 (32) 9.5 | 11.0, 22016 x 8192 26.8 | 24.4
+//   T = 8   4096 x 4096 5.3 | 7.0, 22016 x 8192 36.9 | 28.0
+//   T = 16  11008 x 4096 (64) 11.6 | 13.2, (32) 12.4 | 15.2, 22016 x 8192 (32) 44.6 | 42.6
+// At 16 tokens the wide kernel's rule gains with groups of 128 (10240 x 8192
+// 18.2 -> 16.2, 22016 x 8192 31.1 -> 29.2) and loses with groups of 32 (19.3 ->
+// 25.9, 41.8 -> 47.1).
 template <int GL, bool SF32>
 int launch_linear_variant(const Q4GLinearArgs& a, hipStream_t stream) {
     const bool two = ceil_div(a.N, 16) > 1024;
     if (a.T <= 4) return two ? launch_narrow<2, 1, 1, GL, SF32>(a, stream) : launch_narrow<1, 1, 2, GL, SF32>(a, stream);
     if (a.T <= 8) return two ? launch_narrow<2, 2, 1, GL, SF32>(a, stream) : launch_narrow<1, 2, 2, GL, SF32>(a, stream);
+    if (a.T <= 16 && GL == 7) return launch_wide_variant<1, GL, SF32>(a, stream);
     if (a.T <= 16) return two ? launch_wide<2, 1, 4, GL, SF32>(a, stream) : launch_wide<1, 1, 8, GL, SF32>(a, stream);
     if (a.T <= 32) return launch_wide_variant<2, GL, SF32>(a, stream);
     if (a.T <= 48) return launch_wide_variant<3, GL, SF32>(a, stream);

@@ -219,6 +219,25 @@ def test_linear_workgroup_rule(qn, T, N, K, group, sd, sym):
     test_linear_variants(qn, T, N, K, group, sd, sym)
 
 
+@pytest.mark.parametrize("T,N,K,group,sd", [
+    (60, 10250, 1288, 32, torch.bfloat16),   # 641 row tiles: three a workgroup, 8 waves, the last tile alone
+    (25, 11000, 520, 64, torch.float32),
+    (37, 9000, 4104, 32, torch.float32),     # constants in slices
+    (16, 10250, 648, 128, torch.bfloat16),
+    (9, 22000, 392, 128, torch.float32),     # 1375: three a workgroup, 4 waves
+    (30, 22000, 264, 32, torch.bfloat16),
+    (45, 22000, 392, 64, torch.float32),
+    (64, 22000, 264, 32, torch.float32),     # 8 waves
+    (64, 22000, 392, 128, torch.bfloat16),
+    (33, 32000, 264, 32, torch.float32),     # 2000: two a workgroup
+    (200, 4090, 520, 32, torch.bfloat16),
+    (100, 6140, 520, 64, torch.bfloat16),    # three, over two token tiles
+])
+@pytest.mark.parametrize("sym", [False, True])
+def test_linear_balance_rule(qn, T, N, K, group, sd, sym):
+    test_linear_variants(qn, T, N, K, group, sd, sym)
+
+
 def test_padding_and_memory_behind_the_arrays(qn):
     """Codes past K, rows behind the last token and behind the output do not
     matter and stay as they were."""

@@ -223,6 +223,8 @@ def test_linear_workgroup_rule(qn, T, N, K, group, sd, sym):
     (60, 10250, 1288, 32, torch.bfloat16),   # 641 row tiles: three a workgroup, 8 waves, the last tile alone
     (25, 11000, 520, 64, torch.float32),
     (37, 9000, 4104, 32, torch.float32),     # constants in slices
+    (64, 8210, 9000, 32, torch.float32),
+    (64, 8210, 17000, 32, torch.bfloat16),
     (16, 10250, 648, 128, torch.bfloat16),
     (9, 22000, 392, 128, torch.float32),     # 1375: three a workgroup, 4 waves
     (30, 22000, 264, 32, torch.bfloat16),

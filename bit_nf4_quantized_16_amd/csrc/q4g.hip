@@ -843,14 +843,11 @@ template <int TT, int GL, bool SF32>
 int launch_wide_variant(const Q4GLinearArgs& a, hipStream_t stream) {
     auto blocks = [&](int rt) { return ceil_div(a.N, 16 * rt) * ceil_div(a.T, 16 * TT); };
     auto most = [&](int rt) { return rt * ceil_div(blocks(rt), 256); };
-    if (most(3) <= std::min(most(1), most(2))) {
-        if (blocks(3) <= 256 || (TT == 4 && GL < 7)) return launch_wide<3, TT, 8, GL, SF32>(a, stream);
-        return launch_wide<3, TT, 4, GL, SF32>(a, stream);
-    }
-    if (most(2) <= most(1)) {
-        if (blocks(2) <= 256 || (TT == 4 && GL == 5)) return launch_wide<2, TT, 8, GL, SF32>(a, stream);
-        return launch_wide<2, TT, 4, GL, SF32>(a, stream);
-    }
+    constexpr int kWaves3 = TT == 4 && GL < 7 ? 8 : 4, kWaves2 = TT == 4 && GL == 5 ? 8 : 4;
+    if (most(3) <= std::min(most(1), most(2)))
+        return blocks(3) <= 256 ? launch_wide<3, TT, 8, GL, SF32>(a, stream) : launch_wide<3, TT, kWaves3, GL, SF32>(a, stream);
+    if (most(2) <= most(1))
+        return blocks(2) <= 256 ? launch_wide<2, TT, 8, GL, SF32>(a, stream) : launch_wide<2, TT, kWaves2, GL, SF32>(a, stream);
     return launch_wide<1, TT, 8, GL, SF32>(a, stream);
 }
 
@@ -867,8 +864,12 @@ int launch_linear_variant(const Q4GLinearArgs& a, hipStream_t stream) {
     const bool two = ceil_div(a.N, 16) > 1024;
     if (a.T <= 4) return two ? launch_narrow<2, 1, 1, GL, SF32>(a, stream) : launch_narrow<1, 1, 2, GL, SF32>(a, stream);
     if (a.T <= 8) return two ? launch_narrow<2, 2, 1, GL, SF32>(a, stream) : launch_narrow<1, 2, 2, GL, SF32>(a, stream);
-    if (a.T <= 16 && GL == 7) return launch_wide_variant<1, GL, SF32>(a, stream);
-    if (a.T <= 16) return two ? launch_wide<2, 1, 4, GL, SF32>(a, stream) : launch_wide<1, 1, 8, GL, SF32>(a, stream);
+    if (a.T <= 16) {
+        if constexpr (GL == 7)
+            return launch_wide_variant<1, GL, SF32>(a, stream);
+        else
+            return two ? launch_wide<2, 1, 4, GL, SF32>(a, stream) : launch_wide<1, 1, 8, GL, SF32>(a, stream);
+    }
     if (a.T <= 32) return launch_wide_variant<2, GL, SF32>(a, stream);
     if (a.T <= 48) return launch_wide_variant<3, GL, SF32>(a, stream);
     return launch_wide_variant<4, GL, SF32>(a, stream);

@@ -355,8 +355,8 @@ def measure_rows(torch, qn, inp, flush):
     sec = timed(8, lambda: qn.qlora_merge(w, m["A"], m["B"], m["s"]))
     rows["merge_r%d_11008x4096" % r] = _hbm_row(BPW_DEQUANT * N * K + 2 * r * (N + K), sec, timed.last_min)
     # dropout (p = 0.05) on the adapter input of the same layer: the masking
-    # pass (X and the keep bits in, X * keep out) and the masked adapter term
-    # of dX (dX, G, the bits in, dX out; A is L2-resident)
+    # pass (X and the keep bits in, X * keep out) and the dX GEMM with the
+    # masked adapter term (G from a projection of its own)
     import workloads
 
     bits = workloads.pack_keep_bits(workloads.keep_mask(T, K, 0.05, 31)).cuda()
@@ -364,8 +364,7 @@ def measure_rows(torch, qn, inp, flush):
     rows["dropout_keep_apply_T1024_K4096"] = _hbm_row(T * K * (2 + 2 + 1 / 8), sec, timed.last_min)
     sec = timed(11, lambda: qn.qlora_linear_bwd(w, m["X"], m["dY"], m["A"], m["B"], m["s"], U=U, need_da=False,
                                                need_db=False, keep=bits, p=0.05))
-    rows["dropout_dx_term_T1024_K4096"] = _hbm_row(T * K * (2 + 2 + 1 / 8) + 2 * T * 64 + 2 * r * K, sec,
-                                                   timed.last_min)
+    rows["dropout_gemm_dx_T1024_11008x4096"] = _mfma_row(dx_flops(N, K, T, r) - 2 * T * N * r, sec, timed.last_min)
     # quantization-error measurement on the uniform grid, fp32 weight read once
     sec = timed(9, lambda: qn.q4_quant_error(m["W"], "uniform"))
     rows["quant_error_uniform_f32_11008x4096"] = _hbm_row(4 * N * K, sec, timed.last_min)

@@ -719,14 +719,11 @@ int linear_bwd(const ql_nf4_weight* w, const uint16_t* X, const uint16_t* dY, in
         if ((s = launch_lora_proj(a, false, b.proj, st)) != QL_OK) return s;
     }
     if (want_dx) {
-        // with dropout the adapter term is masked per element: the GEMM takes
-        // only dY W', a second kernel adds c (G A) * keep
         if (b.gword != nullptr) {
             if ((s = launch_gemm_dx_g(wd, dY, A, r, dX, T, N, K, gproj, b.gword, st)) != QL_OK) return s;
-        } else if ((s = launch_gemm_dx(wd, dY, b.Gp, A, r, drop ? 0 : rp, dX, T, N, K, b.split, st)) != QL_OK) {
+        } else if ((s = launch_gemm_dx(wd, dY, b.Gp, A, r, rp, keep, c, dX, T, N, K, b.split, st)) != QL_OK) {
             return s;
         }
-        if (drop && r > 0 && (s = launch_lora_dx_keep(b.Gp, rp, A, r, keep, c, T, K, dX, st)) != QL_OK) return s;
     }
     if (want_da || want_db) {
         GradArgs g{};
@@ -1109,9 +1106,8 @@ int linear_bwd8(const ql_nf4_weight* const* w, int32_t nw, bool group, const ql_
             if (b.gword != nullptr) {
                 s = launch_gemm_dx_g(to_dev(w[0]), dY[0], A[0], r, dX, T, rows[0], K, g, b.gword, st);
             } else {
-                s = launch_gemm_dx(to_dev(w[0]), dY[0], b.Gp[0], r > 0 ? A[0] : nullptr, r, drop ? 0 : rp, dX, T, rows[0],
-                                   K, b.split, st);
-                if (s == QL_OK && drop && r > 0) s = launch_lora_dx_keep(b.Gp[0], rp, A[0], r, keep, c, T, K, dX, st);
+                s = launch_gemm_dx(to_dev(w[0]), dY[0], b.Gp[0], r > 0 ? A[0] : nullptr, r, rp, keep, c, dX, T, rows[0], K,
+                                   b.split, st);
             }
             if (s != QL_OK) return s;
         }

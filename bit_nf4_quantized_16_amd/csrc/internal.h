@@ -35,11 +35,8 @@ int launch_dequantize(const ql_nf4_weight& w, void* out, bool bf16_out, hipStrea
 // Adapter merge: out[n][k] = bf16(fl32(w'[n][k] + scale sum_j B[n][j] A[j][k]))
 // for 1 <= r <= QL_MAX_RANK, K % 64 == 0. Dynamic LDS merge_lds_bytes(r).
 // LoRA dropout with a bit-packed keep mask [T, K/8] (element 8i + j in bit
-// j of byte i): X_d = X * keep; dX[t][k] += fl32(c sum_j G[t][j] A[j][k]) for
-// kept (t, k) (G bf16 with row stride ldg, A [r, K]).
+// j of byte i): X_d = X * keep.
 int launch_keep_apply(const uint16_t* X, const uint8_t* keep, int64_t T, int64_t K, uint16_t* Xd, hipStream_t stream);
-int launch_lora_dx_keep(const uint16_t* G, int64_t ldg, const uint16_t* A, int r, const uint8_t* keep, float c,
-                        int64_t T, int64_t K, uint16_t* dX, hipStream_t stream);
 
 // Quantization error on a 4-bit grid (QL_GRID_*): fp64 partials in ws.
 size_t q4_error_ws_bytes(bool bf16, int64_t n);
@@ -161,8 +158,10 @@ int launch_gemm_dx_g(const NF4Dev& w, const uint16_t* dY, const uint16_t* A, int
 // Y = X W'^T + s (X A^T) B^T with U_out = X A^T (optional), one launch.
 int launch_gemm_fwd_u(const NF4Dev& w, const uint16_t* X, const uint16_t* A, const uint16_t* B, int r, float scale,
                       uint16_t* Y, float* U_out, int64_t T, int64_t N, int64_t K, uint64_t* words, hipStream_t stream);
+// dX = dY W' + G A (G bf16 [T, rp]); with a keep mask dY W' + c (G A) * keep.
 int launch_gemm_dx(const NF4Dev& w, const uint16_t* dY, const uint16_t* Gp, const uint16_t* A, int r, int rp,
-                   uint16_t* dX, int64_t T, int64_t N, int64_t K, float* split_ws, hipStream_t stream);
+                   const uint8_t* keep, float c, uint16_t* dX, int64_t T, int64_t N, int64_t K, float* split_ws,
+                   hipStream_t stream);
 // dX = sum over ng layers that read the same X of dY_L W_L' + G_L A_L, one
 // GEMM launch (+ the split reduce): the layers' rows are one reduction of
 // gemm_group_steps(N, ng) 64-row steps, planned as plan_gemm(K, T, 64 x

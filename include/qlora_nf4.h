@@ -466,11 +466,12 @@ int qlora_linear_bwd_group(const ql_nf4_weight* const* w, int32_t nw, const uint
  *   dX = dY W' + c (G A) * keep,  dA = c G^T (X * keep),  dB = s dY^T U
  *
  * with G = s dY B and U = c (X * keep) A^T (U_saved from the forward, or
- * recomputed from X and keep when NULL). dX is dY W' rounded to bf16, then
- * the kept entries get fl32(c (G A)) added and are rounded again. Other
- * arguments, layouts and errors as qlora_linear_bwd (QL_ERR_NULL for a NULL
- * keep, QL_ERR_UNSUPPORTED for p outside [0, 1)); the workspace is
- * qlora_linear_bwd_dropout_workspace(...) bytes.
+ * recomputed from X and keep when NULL). G enters dX's adapter term as bf16,
+ * as in qlora_linear_bwd; the mask and c are applied to that term's fp32 sums
+ * and dX is rounded to bf16 once. Other arguments, layouts and errors as
+ * qlora_linear_bwd (QL_ERR_NULL for a NULL keep, QL_ERR_UNSUPPORTED for p
+ * outside [0, 1)); the workspace is qlora_linear_bwd_dropout_workspace(...)
+ * bytes.
  */
 size_t qlora_linear_bwd_dropout_workspace(int64_t rows, int64_t cols, int64_t T, int32_t r);
 int qlora_linear_bwd_dropout(const ql_nf4_weight* w, const uint16_t* X, const uint16_t* dY, int64_t T,
@@ -559,9 +560,11 @@ int qlora_swiglu_bwd(const ql_act8* gate8, const ql_act8* up8, const uint16_t* d
  *            recomputed from the rounded X8
  *
  * dA and dB use G and U in fp32 (qlora_linear_bwd rounds both to bf16 first),
- * so against the exact sums over X8, dY and U they carry fp32 rounding only;
- * dX is bitwise qlora_linear_bwd's (qlora_linear_bwd_dropout's). Other
- * arguments, layouts and errors as qlora_linear_bwd, with QL_ERR_SHAPE for a
+ * so against the exact sums over X8, dY and U they carry fp32 rounding only.
+ * dX is bitwise qlora_linear_bwd's (qlora_linear_bwd_dropout's): fp32 sums
+ * rounded once, G in its adapter term a bf16 operand of the matrix product
+ * (off by 2^-8 of that term at most, under dX's own rounding unless the term
+ * is the larger part and cancels). Other arguments, layouts and errors as qlora_linear_bwd, with QL_ERR_SHAPE for a
  * checkpoint of another shape and QL_ERR_UNSUPPORTED for p outside [0, 1) or
  * nonzero without a mask. The workspace is
  * qlora_linear_bwd_act8_workspace(...) bytes, dropout nonzero when keep is
@@ -733,7 +736,7 @@ const char* qlora_last_error(void);
 #define QL_KERNEL_MERGE 8
 #define QL_KERNEL_QERROR 9
 #define QL_KERNEL_KEEP_APPLY 10
-#define QL_KERNEL_DX_KEEP 11
+#define QL_KERNEL_DX_KEEP 11 /* the dX GEMM with dropout's masked adapter term (without: QL_KERNEL_GEMM_DX) */
 #define QL_KERNEL_ADAMW 12
 #define QL_KERNEL_ACT8 13
 #define QL_KERNEL_SWIGLU 14

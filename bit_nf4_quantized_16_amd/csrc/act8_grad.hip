@@ -7,7 +7,10 @@
 // and V = G = s dY B for dA; M = dY (bf16) and V = U for dB. V comes as fp32
 // and is not rounded: it is split into three bf16 terms v = h + m + l (8
 // significant bits each, 24 in all), multiplied by the exact bf16 values of M
-// and summed in fp32, so dA and dB carry fp32 rounding only. One grid holds
+// and summed in fp32, so dA and dB carry fp32 rounding only. An infinite M
+// times a term that is zero would be NaN where v M is infinite: a wave whose
+// sums are not finite takes its tokens again with M's infinities (and NaN) in
+// the products of the leading term h alone. One grid holds
 // both problems: workgroups [0, nblk0) take column blocks of the first, the
 // rest those of the second.
 //
@@ -33,6 +36,7 @@
 // for the whole (few workgroups), two waves' loads more in flight at 128
 // registers: 107.
 #include <algorithm>
+#include <type_traits>
 
 #include "act8.h"
 #include "common.h"
@@ -59,6 +63,19 @@ __device__ __forceinline__ uint4 keep_mask(uint32_t bits) {
 __device__ __forceinline__ float split_rest(float v, bool check) {
     const float rest = v - __uint_as_float(__float_as_uint(v) & 0xFFFF0000u);
     return check && fabsf(v) == __builtin_inff() ? 0.0f : rest;
+}
+
+// The operand with its infinities and NaN as zeros.
+__device__ __forceinline__ bf16x8_t finite_only(bf16x8_t v) {
+    uint4 x = __builtin_bit_cast(uint4, v);
+    uint32_t* const w[4] = {&x.x, &x.y, &x.z, &x.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        // a magnitude of 0x7F80 or more carries into its half's sign bit, which then fills the half
+        const u16x2_act c = __builtin_bit_cast(u16x2_act, *w[q] & 0x7FFF7FFFu) + u16x2_act{0x80, 0x80};
+        *w[q] &= ~__builtin_bit_cast(uint32_t, __builtin_bit_cast(i16x2_act, c) >> i16x2_act{15, 15});
+    }
+    return as_bf16x8(x);
 }
 
 // Tiles of a rank of RT x 16: the columns a workgroup takes (16 CB), its
@@ -98,10 +115,6 @@ __device__ __forceinline__ void grads_block(const Act8GradArgs& a, const Act8Gra
     const int64_t tb = blockIdx.y * a.t_per;
     const int64_t te = std::min<int64_t>(tb + a.t_per, a.T);
     f32x4 acc[RT][CB];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int cb = 0; cb < CB; ++cb) acc[rt][cb] = f32x4{0.f, 0.f, 0.f, 0.f};
     uint16_t* const tm = sm + wave * G::kTile;
     uint16_t* const tv = tm + kRows * LdM;
     const bool masked = ACT8 && pb.keep != nullptr;
@@ -179,12 +192,18 @@ __device__ __forceinline__ void grads_block(const Act8GradArgs& a, const Act8Gra
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb) bv[cb] = lds_col8(tm, LdM, 8 * g, 16 * cb, li);
     };
+    auto drop_infinities = [&]() {
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) bv[cb] = finite_only(bv[cb]);
+    };
     // the chunk's products with V's terms as prepared. Loads return in order:
     // the terms (from L2) are asked for before the next chunk of M (from HBM),
     // or every chunk would wait for that as well (rank 64, T = 4096,
     // 4096 + 11008 columns: 63 against 57 us).
     constexpr int RS = RT <= 4 ? RT : (RT + 1) / 2;  // rank tiles whose operands are in registers together
-    auto multiply_terms = [&](const Stage& st, Stage& next, int64_t t, int64_t tn) {
+    // careful (a constant): M's infinities meet the leading terms alone, and no
+    // loads ahead.
+    auto multiply_terms = [&](auto careful, const Stage& st, Stage& next, int64_t t, int64_t tn) {
         const uint4* const vop = reinterpret_cast<const uint4*>(pb.terms) + (t / kRows) * (3 * RT * 64) + lane;
 #pragma unroll
         for (int r0 = 0; r0 < RT; r0 += RS) {
@@ -195,27 +214,31 @@ __device__ __forceinline__ void grads_block(const Act8GradArgs& a, const Act8Gra
                 for (int term = 0; term < 3; ++term)
                     if (r0 + rt < RT) av[rt][term] = vop[((r0 + rt) * 3 + term) * 64];
             __builtin_amdgcn_sched_barrier(0);
-            if (r0 + RS >= RT) load_m(next, tn);
+            if (!careful && r0 + RS >= RT) load_m(next, tn);
             __builtin_amdgcn_sched_barrier(0);
             if (r0 == 0) {
                 put_m(st, t);
                 wave_lds_sync();
                 get_m();
+            } else if (careful) {
+                get_m();
             }
 #pragma unroll
-            for (int rt = 0; rt < RS; ++rt)
+            for (int i = 0; i < RS * 3; ++i) {
+                // a rank tile's terms one after the other, or (careful) all leading terms first
+                const int rt = careful ? i % RS : i / 3, term = careful ? i / RS : i % 3;
+                if (careful && i == RS) drop_infinities();
+                if (r0 + rt < RT) {
 #pragma unroll
-                for (int term = 0; term < 3; ++term)
-                    if (r0 + rt < RT) {
-#pragma unroll
-                        for (int cb = 0; cb < CB; ++cb)
-                            acc[r0 + rt][cb] =
-                                __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(av[rt][term]), bv[cb], acc[r0 + rt][cb], 0, 0, 0);
-                    }
+                    for (int cb = 0; cb < CB; ++cb)
+                        acc[r0 + rt][cb] =
+                            __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(av[rt][term]), bv[cb], acc[r0 + rt][cb], 0, 0, 0);
+                }
+            }
         }
     };
     // the same with V split here
-    auto multiply_split = [&](const Stage& st, float (&v)[2 * RT][4], int64_t t) {
+    auto multiply_split = [&](auto careful, const Stage& st, float (&v)[2 * RT][4], int64_t t) {
         put_m(st, t);
         if (t + kRows > te || (r & 15) != 0) {  // nothing past the tokens and the rank
 #pragma unroll
@@ -250,6 +273,7 @@ __device__ __forceinline__ void grads_block(const Act8GradArgs& a, const Act8Gra
             }
             wave_lds_sync();
             if (term == 0) get_m();
+            if (term == 1 && careful) drop_infinities();
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
                 const bf16x8_t av = lds_col8(tv, LdV, 8 * g, 16 * rt, li);
@@ -260,13 +284,22 @@ __device__ __forceinline__ void grads_block(const Act8GradArgs& a, const Act8Gra
         }
     };
 
+    auto clear = [&]() {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int cb = 0; cb < CB; ++cb) acc[rt][cb] = f32x4{0.f, 0.f, 0.f, 0.f};
+    };
     Stage cur, nxt;
+    constexpr std::false_type kPlain{};
+    constexpr std::true_type kCareful{};
+    clear();
     int64_t t = tb + kRows * wave;
     if (t < te) {
         load_m(cur, t);
         if constexpr (kTerms) {
             for (; t < te; t += NW * kRows) {
-                multiply_terms(cur, nxt, t, std::min<int64_t>(t + NW * kRows, te - 1));
+                multiply_terms(kPlain, cur, nxt, t, std::min<int64_t>(t + NW * kRows, te - 1));
                 cur = nxt;
             }
         } else {
@@ -277,12 +310,33 @@ __device__ __forceinline__ void grads_block(const Act8GradArgs& a, const Act8Gra
                 load_m(nxt, tn);
                 load_v(vnxt, tn);
                 __builtin_amdgcn_sched_barrier(0);
-                multiply_split(cur, vcur, t);
+                multiply_split(kPlain, cur, vcur, t);
                 cur = nxt;
 #pragma unroll
                 for (int i = 0; i < 2 * RT; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) vcur[i][e] = vnxt[i][e];
+            }
+        }
+    }
+    bool finite = true;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) finite = finite && fabsf(acc[rt][cb][q]) < __builtin_inff();
+    if (__builtin_expect(!__all(finite), 0)) {
+        clear();
+#pragma unroll 1
+        for (t = tb + kRows * wave; t < te; t += NW * kRows) {
+            load_m(cur, t);
+            if constexpr (kTerms) {
+                multiply_terms(kCareful, cur, cur, t, t);
+            } else {
+                float v[2 * RT][4];
+                load_v(v, t);
+                multiply_split(kCareful, cur, v, t);
             }
         }
     }
@@ -332,7 +386,7 @@ __device__ __forceinline__ void grads_block(const Act8GradArgs& a, const Act8Gra
 }
 
 template <int RT, int CB>
-__global__ __launch_bounds__((64 * GradTile<RT, CB>::NW)) void act8_grads_kernel(Act8GradArgs a) {
+__global__ __launch_bounds__((64 * GradTile<RT, CB>::NW), RT <= 2 ? 4 : 2) void act8_grads_kernel(Act8GradArgs a) {
     using G = GradTile<RT, CB>;
     __shared__ __attribute__((aligned(16))) uint16_t sm[G::NW * G::kTile];
     const bool second = static_cast<int>(blockIdx.x) >= a.nblk0;

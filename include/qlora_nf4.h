@@ -560,7 +560,9 @@ int qlora_swiglu_bwd(const ql_act8* gate8, const ql_act8* up8, const uint16_t* d
  *            recomputed from the rounded X8
  *
  * dA and dB use G and U in fp32 (qlora_linear_bwd rounds both to bf16 first),
- * so against the exact sums over X8, dY and U they carry fp32 rounding only.
+ * so against the exact sums over X8, dY and U they carry fp32 rounding only
+ * (values of G and U enter as multiples of 2^-133: those under 2^-109 lose
+ * low bits). Infinities and NaN of dY, U and X8 give those of the sums.
  * dX is bitwise qlora_linear_bwd's (qlora_linear_bwd_dropout's): fp32 sums
  * rounded once, G in its adapter term a bf16 operand of the matrix product
  * (off by 2^-8 of that term at most, under dX's own rounding unless the term

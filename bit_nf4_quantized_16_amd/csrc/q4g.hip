@@ -134,10 +134,12 @@ __global__ __launch_bounds__(kThreads) void q4g_quantize_kernel(const void* __re
     if constexpr (!SF32) s = __uint_as_float(pack_bf16x2(s, 0.0f) << 16);
     const bool live = s >= 0x1p-126f;  // below: the group is held as zeros
     if (!live) s = 0.0f;
-    const float inv = 1.0f / s;
+    // the remainder of a quotient by a scale under about 2^-102 may have places under
+    // fp32's last: small scales and their values come up by 2^64 first, exactly
+    const float up = s < 0x1p-64f ? 0x1p64f : 1.0f, su = s * up, inv = 1.0f / su;
     constexpr float kRound = 12582912.0f;  // 1.5 2^23
     constexpr int kRoundBits = 0x4B400000;
-    auto nearest = [&](float a) { return __float_as_int(quotient(a, s, inv) + kRound) - kRoundBits; };
+    auto nearest = [&](float a) { return __float_as_int(quotient(a * up, su, inv) + kRound) - kRoundBits; };
     const int z = (sym || !live) ? 8 : std::min(nearest(bottom), 15);
     uint32_t c = 0x88888888u;
     if (live) {

@@ -11,6 +11,7 @@ import ctypes
 from dataclasses import dataclass
 
 import torch
+from torch.autograd.graph import increment_version
 
 from . import _lib
 
@@ -458,6 +459,8 @@ def act8_quantize(X, out=None):
             _refuse(_lib.QL_ERR_SHAPE, "out is %d x %d on %s, X %d x %d on %s"
                     % (a.rows, a.cols, a.codes.device, rows, cols, X.device))
     _launch(X.device, lib.act8_quantize, X.data_ptr(), d)
+    if out is not None:  # a backward that kept these tensors must not take the new values for the old
+        increment_version((a.codes, a.scale))
     return a
 
 
@@ -467,11 +470,14 @@ def act8_dequantize(a, dtype=torch.bfloat16, out=None):
         _refuse(_lib.QL_ERR_UNSUPPORTED, "output dtype %s" % dtype)
     d = a.descriptor()
     dev = a.codes.device
-    if out is None:
+    new = out is None
+    if new:
         out = torch.empty(a.rows, a.cols, dtype=dtype, device=dev)
     else:
         _tensor(out, "out", dtype, (a.rows, a.cols), dev)
     _launch(dev, lib.act8_dequantize, d, out.data_ptr(), _lib.QL_BF16 if dtype == torch.bfloat16 else _lib.QL_F32)
+    if not new:
+        increment_version(out)
     return out
 
 
@@ -518,7 +524,9 @@ def _grads(want, given, shape, name, accumulate, device):
     if not want:
         return None
     if given is not None:
-        return _tensor(given, name, torch.float32, shape, device)
+        _tensor(given, name, torch.float32, shape, device)
+        increment_version(given)  # written through its address
+        return given
     return (torch.zeros if accumulate else torch.empty)(*shape, dtype=torch.float32, device=device)
 
 
@@ -672,11 +680,14 @@ def q4g_dequantize(w, dtype=torch.bfloat16, out=None):
         _refuse(_lib.QL_ERR_UNSUPPORTED, "output dtype %s" % dtype)
     d = w.descriptor()
     dev = w.packed.device
-    if out is None:
+    new = out is None
+    if new:
         out = torch.empty(w.rows, w.cols, dtype=dtype, device=dev)
     else:
         _tensor(out, "out", dtype, (w.rows, w.cols), dev)
     _launch(dev, lib.q4g_dequantize, d, out.data_ptr(), _DTYPES[dtype])
+    if not new:
+        increment_version(out)
     return out
 
 
@@ -688,11 +699,14 @@ def q4g_linear_fwd(w, X, out=None):
     d = w.descriptor()
     T, dev = X.shape[0], w.packed.device
     _tensor(X, "X", torch.bfloat16, (T, w.cols), dev)
-    if out is None:
+    new = out is None
+    if new:
         out = torch.empty(T, w.rows, dtype=torch.bfloat16, device=dev)
     else:
         _tensor(out, "out", torch.bfloat16, (T, w.rows), dev)
     _launch(dev, lib.q4g_linear_fwd, d, X.data_ptr(), T, out.data_ptr())
+    if not new:
+        increment_version(out)
     return out
 
 

@@ -8,6 +8,7 @@ Importing this package fails if the library has not been built.
 """
 
 import ctypes
+import functools
 from dataclasses import dataclass
 
 import torch
@@ -736,18 +737,61 @@ def paged_adamw_step(param, grad, exp_avg, exp_avg_sq, step, lr=2e-4, betas=(0.9
     return param
 
 
+class _FirstOrderOnly(torch.autograd.Function):
+    """Hands gradients on; differentiating them raises. The first ``n`` inputs
+    are what the gradients depend on: autograd comes here on its way to them."""
+
+    @staticmethod
+    def forward(ctx, n, *ts):
+        return tuple(t.view_as(t) for t in ts[n:])
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("the gradients from 8-bit checkpoints cannot be differentiated again")
+
+
+def _tie(*inputs):
+    """Tensors without elements (and without the inputs' memory) that depend on
+    the inputs, for those that a backward does not keep."""
+    with torch.enable_grad():
+        return [t[:0].clone() for t in inputs if t.requires_grad]
+
+
+def _first_order_only(backward):
+    """A backward whose gradients raise when they are differentiated. They come
+    from a library call, constants to autograd: under create_graph a loss of
+    them would lose their part without a word, also where dY is a constant."""
+
+    @functools.wraps(backward)
+    def run(ctx, *dYs):
+        with torch.no_grad():
+            grads = backward(ctx, *dYs)
+        if not torch.is_grad_enabled():
+            return grads
+        of = [t for t in (*ctx.tie, *ctx.saved_tensors, *dYs) if t is not None and t.requires_grad]
+        at = [i for i, g in enumerate(grads) if g is not None]
+        grads = list(grads)
+        for i, g in zip(at, _FirstOrderOnly.apply(len(of), *of, *[grads[i] for i in at])):
+            grads[i] = g
+        return tuple(grads)
+
+    return run
+
+
 class QLoRALinearFunction(torch.autograd.Function):
     """autograd wrapper: forward / backward run in the HIP library; W is frozen
     (no gradient), A and B receive fp32 gradients cast to their dtype.
     ``act8``: True keeps X as an 8-bit checkpoint instead of itself, an Act8
     of X (shared with other layers, or swiglu_fwd's h8) is kept as it is; dA
-    then comes from the checkpoint."""
+    then comes from the checkpoint. First order only: with ``act8`` the
+    gradients raise when differentiated again, without they are constants."""
 
     @staticmethod
     def forward(ctx, X, A, B, w, scale, keep=None, p=0.0, act8=None):
         Y, U = qlora_linear_fwd(w, X.contiguous(), A.contiguous(), B.contiguous(), scale, save_u=True, keep=keep, p=p)
         ctx.act8 = act8 is not None and act8 is not False
         if ctx.act8:
+            ctx.tie = _tie(X)
             X8 = act8_quantize(X.contiguous()) if act8 is True else act8
             if (X8.rows, X8.cols) != tuple(X.shape):
                 _refuse(_lib.QL_ERR_SHAPE, "act8 is %d x %d, X %s" % (X8.rows, X8.cols, tuple(X.shape)))
@@ -763,17 +807,22 @@ class QLoRALinearFunction(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dY):
         if ctx.act8:
-            codes, xs, A, B, U = ctx.saved_tensors
-            need = ctx.needs_input_grad
-            dX, dA, dB = qlora_linear_bwd_act8(ctx.w, Act8(*codes.shape, codes, xs), dY.contiguous().to(torch.bfloat16),
-                                               A.contiguous(), B.contiguous(), ctx.scale, U=U, need_dx=need[0],
-                                               need_da=need[1], need_db=need[2], keep=ctx.keep, p=ctx.p)
-            return (dX, dA.to(A.dtype) if need[1] else None, dB.to(B.dtype) if need[2] else None,
-                    None, None, None, None, None)
+            return QLoRALinearFunction._backward_act8(ctx, dY)
         X, A, B, U = ctx.saved_tensors
         dX, dA, dB = qlora_linear_bwd(ctx.w, X, dY.contiguous().to(torch.bfloat16), A, B, ctx.scale, U=U,
                                       need_dx=ctx.needs_input_grad[0], keep=ctx.keep, p=ctx.p)
         return dX, dA.to(A.dtype), dB.to(B.dtype), None, None, None, None, None
+
+    @staticmethod
+    @_first_order_only
+    def _backward_act8(ctx, dY):
+        codes, xs, A, B, U = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dX, dA, dB = qlora_linear_bwd_act8(ctx.w, Act8(*codes.shape, codes, xs), dY.contiguous().to(torch.bfloat16),
+                                           A.contiguous(), B.contiguous(), ctx.scale, U=U, need_dx=need[0],
+                                           need_da=need[1], need_db=need[2], keep=ctx.keep, p=ctx.p)
+        return (dX, dA.to(A.dtype) if need[1] else None, dB.to(B.dtype) if need[2] else None,
+                None, None, None, None, None)
 
 
 class QLoRAGroupFunction(torch.autograd.Function):
@@ -810,7 +859,7 @@ class QLoRAGroupFunction(torch.autograd.Function):
 class QLoRAGroupAct8Function(torch.autograd.Function):
     """QLoRAGroupFunction with the shared X kept as one 8-bit checkpoint:
     apply(X, act8, scale, ws, A_0, B_0, A_1, B_1, ...), ``act8`` an Act8 of X
-    or None to make one here."""
+    or None to make one here. First order only."""
 
     @staticmethod
     def forward(ctx, X, act8, scale, ws, *adapters):
@@ -820,11 +869,13 @@ class QLoRAGroupAct8Function(torch.autograd.Function):
         if (X8.rows, X8.cols) != tuple(X.shape):
             _refuse(_lib.QL_ERR_SHAPE, "act8 is %d x %d, X %s" % (X8.rows, X8.cols, tuple(X.shape)))
         ctx.save_for_backward(X8.codes, X8.scale, *As, *Bs, *[U for _, U in outs])
+        ctx.tie = _tie(X, *adapters)
         ctx.ws = ws
         ctx.scale = scale
         return tuple(Y for Y, _ in outs)
 
     @staticmethod
+    @_first_order_only
     def backward(ctx, *dYs):
         n = len(ctx.ws)
         codes, xs, *rest = ctx.saved_tensors
@@ -841,15 +892,18 @@ class QLoRAGroupAct8Function(torch.autograd.Function):
 
 class SwiGLUFunction(torch.autograd.Function):
     """autograd wrapper of the gated activation: apply(gate, up) returns H
-    and keeps gate and up as 8-bit checkpoints for the backward."""
+    and keeps gate and up as 8-bit checkpoints for the backward. First order
+    only."""
 
     @staticmethod
     def forward(ctx, gate, up):
         H, g8, u8, _ = swiglu_fwd(gate.contiguous(), up.contiguous())
         ctx.save_for_backward(g8.codes, g8.scale, u8.codes, u8.scale)
+        ctx.tie = _tie(gate, up)
         return H
 
     @staticmethod
+    @_first_order_only
     def backward(ctx, dH):
         gc, gs, uc, us = ctx.saved_tensors
         rows, cols = gc.shape

@@ -61,3 +61,59 @@ def test_every_out_counts_as_modified(qn):
         qn.act8_quantize(X, out=i8)
     qn.act8_quantize(X, out=i8)
     assert torch.equal(i8.codes, x8.codes)
+
+
+def test_second_order_by_the_adapters_is_refused(qn):
+    w, X, dY, A, B = _layer(qn)
+    A, B, dY = (t.requires_grad_() for t in (A, B, dY))
+    for call in (lambda: qn.QLoRALinearFunction.apply(X, A, B, w, 1.0, None, 0.0, True),
+                 lambda: qn.QLoRAGroupAct8Function.apply(X, None, 1.0, [w], A, B)[0]):
+        gA, = torch.autograd.grad(call(), A, dY, create_graph=True)
+        for leaf in (B, dY):  # dA = (s dY B)^T X
+            with pytest.raises(RuntimeError, match="cannot be differentiated again"):
+                torch.autograd.grad(gA.float().sum(), leaf, retain_graph=True)
+
+
+def test_a_checkpoint_does_not_hold_the_input(qn):
+    """What the backward keeps of X is its checkpoint, not its memory."""
+    w, _, dY, A, B = _layer(qn, T=2048, N=64, K=2048)
+    A.requires_grad_()
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    X = torch.randn(2048, 2048, device="cuda").bfloat16().requires_grad_()
+    held = lambda t: torch.cuda.memory_allocated() - before
+    Z = X * 1  # not a leaf: only autograd would hold it
+    Y = qn.QLoRALinearFunction.apply(Z, A, B, w, 1.0, None, 0.0, True)
+    H = qn.SwiGLUFunction.apply(Z, Z)
+    del Z
+    # X, Y, H, three checkpoints, U; not Z (8 MiB)
+    mine = X.nbytes + Y.nbytes + H.nbytes + 3 * 2048 * 2048 * 33 // 32 + 2048 * 8 * 4
+    assert held(X) <= mine + (1 << 20)
+    (Y.float().sum() + H.float().sum()).backward()
+
+
+def test_second_order_is_refused(qn):
+    """Also where dY is a constant (a plain sum), which is no argument of the
+    backward that could require a gradient."""
+    w, X, dY, A, B = _layer(qn)
+    X, A, B = (t.requires_grad_() for t in (X, A, B))
+    calls = {
+        "linear": lambda: qn.QLoRALinearFunction.apply(X, A, B, w, 1.0, None, 0.0, True),
+        "group": lambda: sum(qn.QLoRAGroupAct8Function.apply(X, None, 1.0, [w, w], A, B, A, B)),
+        "swiglu": lambda: qn.SwiGLUFunction.apply(X, X),
+    }
+    for name, call in calls.items():
+        want = torch.autograd.grad(call().sum(), X)[0]
+        got, = torch.autograd.grad(call().sum(), X, create_graph=True)
+        assert torch.equal(got, want), name
+        assert got.requires_grad, name
+        refused = pytest.raises(RuntimeError, match="cannot be differentiated again")
+        with refused:
+            torch.autograd.grad(got.float().square().sum(), X, retain_graph=True)
+        with refused:  # beside a path that can be
+            torch.autograd.grad((got * X).float().sum(), X, retain_graph=True)
+        with refused:
+            got.float().square().sum().backward()
+        # the first order through create_graph stays usable, beside other paths
+        other, = torch.autograd.grad((call().float() * 0).sum() + X.float().square().sum(), X, create_graph=True)
+        assert torch.equal(other, (2 * X.float()).to(other.dtype)), name

@@ -571,11 +571,15 @@ def qlora_linear_bwd_act8(w, X8, dY, A=None, B=None, scale=1.0, U=None, need_dx=
 def qlora_linear_bwd_group_act8(ws, X8, dYs, As=None, Bs=None, scale=1.0, Us=None, need_dx=True, need_da=True,
                                 need_db=True, dAs=None, dBs=None, accumulate=False):
     """qlora_linear_bwd_group with the shared input kept as an Act8 ``X8``.
-    Returns (dX, list of dA or None, list of dB or None)."""
+    ``need_da`` and ``need_db`` may be lists, a layer each. Returns (dX, list
+    of dA or None, list of dB or None), None in a list for a layer's that is
+    not wanted."""
     nw = len(ws)
     if nw < 1 or len(dYs) != nw:
         _refuse(_lib.QL_ERR_SHAPE, "%d weights and %d dY" % (nw, len(dYs)))
-    for name, ts in (("As", As), ("Bs", Bs), ("Us", Us), ("dAs", dAs), ("dBs", dBs)):
+    need_da, need_db = (list(n) if isinstance(n, (list, tuple)) else [n] * nw for n in (need_da, need_db))
+    for name, ts in (("As", As), ("Bs", Bs), ("Us", Us), ("dAs", dAs), ("dBs", dBs), ("need_da", need_da),
+                     ("need_db", need_db)):
         if ts is not None and len(ts) != nw:
             _refuse(_lib.QL_ERR_SHAPE, "%d weights and %d %s" % (nw, len(ts), name))
     T = _matrix(dYs[0], "dY").shape[0]
@@ -592,28 +596,28 @@ def qlora_linear_bwd_group_act8(ws, X8, dYs, As=None, Bs=None, scale=1.0, Us=Non
             _refuse(_lib.QL_ERR_SHAPE, "layer %d has rank %d, layer 0 rank %d" % (i, ri, r))
         r = ri
     dX = torch.empty(T, cols, dtype=torch.bfloat16, device=dev) if need_dx else None
-    need_da, need_db = need_da and r > 0, need_db and r > 0
-    dAs = [_grads(need_da, pick(dAs, i), (r, cols), "dA", accumulate, dev) for i in range(nw)] if need_da else None
-    dBs = [_grads(need_db, pick(dBs, i), (w.rows, r), "dB", accumulate, dev) for i, w in enumerate(ws)] if need_db else None
-    if need_db:
-        for i in range(nw):
+    any_da, any_db = any(need_da) and r > 0, any(need_db) and r > 0
+    dAs = [_grads(need_da[i], pick(dAs, i), (r, cols), "dA", accumulate, dev) for i in range(nw)] if any_da else None
+    dBs = [_grads(need_db[i], pick(dBs, i), (w.rows, r), "dB", accumulate, dev) for i, w in enumerate(ws)] if any_db else None
+    for i in range(nw):
+        if any_db and need_db[i]:
             _tensor(pick(Us, i), "U", torch.float32, (T, r), dev)
     x8 = None
-    if need_da:
+    if any_da:
         x8 = X8.descriptor() if X8 is not None else _refuse(_lib.QL_ERR_NULL, "X8 is None (dA needs it)")
         _tensor(X8.codes, "X8", torch.uint8, (T, cols), dev)
     if T == 0:
         for g in (dAs or []) + (dBs or []):
-            if not accumulate:
+            if g is not None and not accumulate:
                 g.zero_()
         return dX, dAs, dBs
-    arr = lambda ts: (ctypes.c_void_p * nw)(*[t.data_ptr() for t in ts]) if ts is not None else None
+    arr = lambda ts: (ctypes.c_void_p * nw)(*[_addr(t) for t in ts]) if ts is not None else None
     descs = [w.descriptor() for w in ws]
     wp = (ctypes.c_void_p * nw)(*[ctypes.addressof(d) for d in descs])
     rows = (ctypes.c_int64 * nw)(*[w.rows for w in ws])
     ws_, wsb = _workspace(lib.qlora_linear_bwd_group_act8_workspace(rows, nw, cols, T, r), dev)
     _launch(dev, lib.qlora_linear_bwd_group_act8, wp, nw, x8, arr(dYs), T, arr(As) if r > 0 else None,
-            arr(Bs) if r > 0 else None, r, float(scale), arr(Us) if need_db else None, _ptr(dX), arr(dAs), arr(dBs),
+            arr(Bs) if r > 0 else None, r, float(scale), arr(Us) if any_db else None, _ptr(dX), arr(dAs), arr(dBs),
             1 if accumulate else 0, _ptr(ws_), wsb)
     return dX, dAs, dBs
 
@@ -792,10 +796,13 @@ class QLoRALinearFunction(torch.autograd.Function):
         ctx.act8 = act8 is not None and act8 is not False
         if ctx.act8:
             ctx.tie = _tie(X)
-            X8 = act8_quantize(X.contiguous()) if act8 is True else act8
-            if (X8.rows, X8.cols) != tuple(X.shape):
-                _refuse(_lib.QL_ERR_SHAPE, "act8 is %d x %d, X %s" % (X8.rows, X8.cols, tuple(X.shape)))
-            ctx.save_for_backward(X8.codes, X8.scale, A, B, U)
+            need_a, need_b = ctx.needs_input_grad[1:3]
+            if act8 is not True and (act8.rows, act8.cols) != tuple(X.shape):
+                _refuse(_lib.QL_ERR_SHAPE, "act8 is %d x %d, X %s" % (act8.rows, act8.cols, tuple(X.shape)))
+            X8 = None  # only dA reads it
+            if need_a:
+                X8 = act8_quantize(X.contiguous()) if act8 is True else act8
+            ctx.save_for_backward(X8.codes if need_a else None, X8.scale if need_a else None, A, B, U if need_b else None)
         else:
             ctx.save_for_backward(X, A, B, U)
         ctx.w = w
@@ -818,9 +825,10 @@ class QLoRALinearFunction(torch.autograd.Function):
     def _backward_act8(ctx, dY):
         codes, xs, A, B, U = ctx.saved_tensors
         need = ctx.needs_input_grad
-        dX, dA, dB = qlora_linear_bwd_act8(ctx.w, Act8(*codes.shape, codes, xs), dY.contiguous().to(torch.bfloat16),
-                                           A.contiguous(), B.contiguous(), ctx.scale, U=U, need_dx=need[0],
-                                           need_da=need[1], need_db=need[2], keep=ctx.keep, p=ctx.p)
+        X8 = Act8(*codes.shape, codes, xs) if need[1] else None
+        dX, dA, dB = qlora_linear_bwd_act8(ctx.w, X8, dY.contiguous().to(torch.bfloat16), A.contiguous(),
+                                           B.contiguous(), ctx.scale, U=U, need_dx=need[0], need_da=need[1],
+                                           need_db=need[2], keep=ctx.keep, p=ctx.p)
         return (dX, dA.to(A.dtype) if need[1] else None, dB.to(B.dtype) if need[2] else None,
                 None, None, None, None, None)
 
@@ -865,10 +873,14 @@ class QLoRAGroupAct8Function(torch.autograd.Function):
     def forward(ctx, X, act8, scale, ws, *adapters):
         As, Bs = [a.contiguous() for a in adapters[0::2]], [b.contiguous() for b in adapters[1::2]]
         outs = qlora_linear_fwd_group(ws, X.contiguous(), As, Bs, scale)
-        X8 = act8 if act8 is not None else act8_quantize(X.contiguous())
-        if (X8.rows, X8.cols) != tuple(X.shape):
-            _refuse(_lib.QL_ERR_SHAPE, "act8 is %d x %d, X %s" % (X8.rows, X8.cols, tuple(X.shape)))
-        ctx.save_for_backward(X8.codes, X8.scale, *As, *Bs, *[U for _, U in outs])
+        if act8 is not None and (act8.rows, act8.cols) != tuple(X.shape):
+            _refuse(_lib.QL_ERR_SHAPE, "act8 is %d x %d, X %s" % (act8.rows, act8.cols, tuple(X.shape)))
+        need_a, need_b = ctx.needs_input_grad[4::2], ctx.needs_input_grad[5::2]
+        X8 = None  # only the dA read it
+        if any(need_a):
+            X8 = act8 if act8 is not None else act8_quantize(X.contiguous())
+        ctx.save_for_backward(X8.codes if X8 is not None else None, X8.scale if X8 is not None else None, *As, *Bs,
+                              *[U if n else None for (_, U), n in zip(outs, need_b)])
         ctx.tie = _tie(X, *adapters)
         ctx.ws = ws
         ctx.scale = scale
@@ -880,34 +892,42 @@ class QLoRAGroupAct8Function(torch.autograd.Function):
         n = len(ctx.ws)
         codes, xs, *rest = ctx.saved_tensors
         As, Bs, Us = rest[:n], rest[n:2 * n], rest[2 * n:]
-        dYs = [(d if d is not None else torch.zeros(codes.shape[0], w.rows, device=codes.device)).contiguous()
-               .to(torch.bfloat16) for d, w in zip(dYs, ctx.ws)]
-        dX, dAs, dBs = qlora_linear_bwd_group_act8(ctx.ws, Act8(*codes.shape, codes, xs), dYs, As, Bs, ctx.scale,
-                                                   Us=Us, need_dx=ctx.needs_input_grad[0])
+        dYs = [d.contiguous().to(torch.bfloat16) for d in dYs]
+        need = ctx.needs_input_grad
+        X8 = Act8(*codes.shape, codes, xs) if codes is not None else None
+        dX, dAs, dBs = qlora_linear_bwd_group_act8(ctx.ws, X8, dYs, As, Bs, ctx.scale, Us=Us, need_dx=need[0],
+                                                   need_da=need[4::2], need_db=need[5::2])
         grads = []
         for i in range(n):
-            grads += [dAs[i].to(As[i].dtype), dBs[i].to(Bs[i].dtype)]
+            grads += [dAs[i].to(As[i].dtype) if need[4 + 2 * i] else None,
+                      dBs[i].to(Bs[i].dtype) if need[5 + 2 * i] else None]
         return (dX, None, None, None, *grads)
 
 
 class SwiGLUFunction(torch.autograd.Function):
     """autograd wrapper of the gated activation: apply(gate, up) returns H
-    and keeps gate and up as 8-bit checkpoints for the backward. First order
-    only."""
+    and keeps gate and up as 8-bit checkpoints for the backward, where one of
+    them needs a gradient. apply(gate, up, True) returns (H, h8) with H's own
+    checkpoint, an Act8 for QLoRALinearFunction's ``act8`` in the down
+    projection. First order only."""
 
     @staticmethod
-    def forward(ctx, gate, up):
-        H, g8, u8, _ = swiglu_fwd(gate.contiguous(), up.contiguous())
-        ctx.save_for_backward(g8.codes, g8.scale, u8.codes, u8.scale)
-        ctx.tie = _tie(gate, up)
-        return H
+    def forward(ctx, gate, up, h8=False):
+        keep = any(ctx.needs_input_grad[:2])
+        H, g8, u8, a8 = swiglu_fwd(gate.contiguous(), up.contiguous(), checkpoint=keep, h8=h8)
+        if keep:
+            ctx.save_for_backward(g8.codes, g8.scale, u8.codes, u8.scale)
+            ctx.tie = _tie(gate, up)
+        return (H, a8) if h8 else H
 
     @staticmethod
     @_first_order_only
-    def backward(ctx, dH):
+    def backward(ctx, dH, _h8=None):
         gc, gs, uc, us = ctx.saved_tensors
         rows, cols = gc.shape
-        return swiglu_bwd(Act8(rows, cols, gc, gs), Act8(rows, cols, uc, us), dH.contiguous().to(torch.bfloat16))
+        dg, du = swiglu_bwd(Act8(rows, cols, gc, gs), Act8(rows, cols, uc, us), dH.contiguous().to(torch.bfloat16))
+        need = ctx.needs_input_grad
+        return dg if need[0] else None, du if need[1] else None, None
 
 
 class KernelTimer:

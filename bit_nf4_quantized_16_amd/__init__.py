@@ -531,6 +531,11 @@ def _grads(want, given, shape, name, accumulate, device):
     return (torch.zeros if accumulate else torch.empty)(*shape, dtype=torch.float32, device=device)
 
 
+def _outputs(dX, dA, dB):
+    """The QL_OUT_* of the gradients that there are."""
+    return (dX is not None) * _lib.QL_OUT_DX | (dA is not None) * _lib.QL_OUT_DA | (dB is not None) * _lib.QL_OUT_DB
+
+
 def qlora_linear_bwd_act8(w, X8, dY, A=None, B=None, scale=1.0, U=None, need_dx=True, need_da=True, need_db=True,
                           dA=None, dB=None, accumulate=False, keep=None, p=0.0):
     """qlora_linear_bwd with the layer's input kept as an Act8 ``X8``. ``U``
@@ -556,7 +561,8 @@ def qlora_linear_bwd_act8(w, X8, dY, A=None, B=None, scale=1.0, U=None, need_dx=
         if not isinstance(keep, torch.Tensor) or keep.numel() != T * (w.cols // 8):
             _refuse(_lib.QL_ERR_SHAPE, "keep is no tensor of %d x %d bytes" % (T, w.cols // 8))
         _tensor(keep, "keep", torch.uint8, keep.shape, dev)
-    ws, wsb = _workspace(lib.qlora_linear_bwd_act8_workspace(w.rows, w.cols, max(T, 1), r, keep is not None), dev)
+    ws, wsb = _workspace(lib.qlora_linear_bwd_act8_workspace_for(w.rows, w.cols, max(T, 1), r, keep is not None,
+                                                                 _outputs(dX, dA, dB)), dev)
     if T == 0:  # no token: the sums are empty
         for g in (dA, dB):
             if g is not None and not accumulate:
@@ -615,7 +621,8 @@ def qlora_linear_bwd_group_act8(ws, X8, dYs, As=None, Bs=None, scale=1.0, Us=Non
     descs = [w.descriptor() for w in ws]
     wp = (ctypes.c_void_p * nw)(*[ctypes.addressof(d) for d in descs])
     rows = (ctypes.c_int64 * nw)(*[w.rows for w in ws])
-    ws_, wsb = _workspace(lib.qlora_linear_bwd_group_act8_workspace(rows, nw, cols, T, r), dev)
+    ws_, wsb = _workspace(lib.qlora_linear_bwd_group_act8_workspace_for(rows, nw, cols, T, r, _outputs(dX, dAs, dBs)),
+                          dev)
     _launch(dev, lib.qlora_linear_bwd_group_act8, wp, nw, x8, arr(dYs), T, arr(As) if r > 0 else None,
             arr(Bs) if r > 0 else None, r, float(scale), arr(Us) if any_db else None, _ptr(dX), arr(dAs), arr(dBs),
             1 if accumulate else 0, _ptr(ws_), wsb)

@@ -40,6 +40,9 @@ QL_KERNEL_Q4G_QUANTIZE = 16
 QL_KERNEL_Q4G_DEQUANTIZE = 17
 QL_KERNEL_Q4G_LINEAR = 18
 QL_ACT8_BLOCK = 32
+QL_OUT_DX = 1
+QL_OUT_DA = 2
+QL_OUT_DB = 4
 QL_NOALLOC_SCRATCH_BYTES = 96 << 20  # include/qlora_nf4.h
 QL_GRID_NF4 = 0
 QL_GRID_UNIFORM = 1
@@ -125,8 +128,10 @@ SIGNATURES = {
     "qlora_swiglu_fwd": (_I, [_P, _P, _I64, _I64, _P, _AP, _AP, _AP, _P]),
     "qlora_swiglu_bwd": (_I, [_AP, _AP, _P, _P, _P, _P]),
     "qlora_linear_bwd_act8_workspace": (_SZ, [_I64, _I64, _I64, _I32, _I]),
+    "qlora_linear_bwd_act8_workspace_for": (_SZ, [_I64, _I64, _I64, _I32, _I, _I]),
     "qlora_linear_bwd_act8": (_I, [_WP, _AP, _P, _I64, _P, _P, _I32, _F, _P, _F, _P, _P, _P, _P, _I, _P, _SZ, _P]),
     "qlora_linear_bwd_group_act8_workspace": (_SZ, [_P, _I32, _I64, _I64, _I32]),
+    "qlora_linear_bwd_group_act8_workspace_for": (_SZ, [_P, _I32, _I64, _I64, _I32, _I]),
     "qlora_linear_bwd_group_act8": (_I, [_P, _I32, _AP, _P, _I64, _P, _P, _I32, _F, _P, _P, _P, _P, _I, _P, _SZ, _P]),
     "q4g_packed_bytes": (_SZ, [_I64, _I64]),
     "q4g_num_groups": (_I64, [_I64, _I64, _I32]),

@@ -1186,8 +1186,15 @@ int qlora_swiglu_bwd(const ql_act8* gate8, const ql_act8* up8, const uint16_t* d
 }
 
 size_t qlora_linear_bwd_act8_workspace(int64_t rows, int64_t cols, int64_t T, int32_t r, int dropout) {
+    return qlora_linear_bwd_act8_workspace_for(rows, cols, T, r, dropout, QL_OUT_DX | QL_OUT_DA | QL_OUT_DB);
+}
+
+size_t qlora_linear_bwd_act8_workspace_for(int64_t rows, int64_t cols, int64_t T, int32_t r, int dropout,
+                                           int outputs) {
     if (rows <= 0 || cols <= 0 || T <= 0 || r < 0 || r > QL_MAX_RANK) return 0;
-    return carve_bwd8(nullptr, &rows, 1, cols, T, r, false, true, true, true, dropout != 0).bytes;
+    return carve_bwd8(nullptr, &rows, 1, cols, T, r, false, outputs & QL_OUT_DX, outputs & QL_OUT_DA,
+                      outputs & QL_OUT_DB, dropout != 0)
+        .bytes;
 }
 
 int qlora_linear_bwd_act8(const ql_nf4_weight* w, const ql_act8* X8, const uint16_t* dY, int64_t T, const uint16_t* A,
@@ -1199,10 +1206,17 @@ int qlora_linear_bwd_act8(const ql_nf4_weight* w, const ql_act8* X8, const uint1
 }
 
 size_t qlora_linear_bwd_group_act8_workspace(const int64_t* rows, int32_t nw, int64_t cols, int64_t T, int32_t r) {
+    return qlora_linear_bwd_group_act8_workspace_for(rows, nw, cols, T, r, QL_OUT_DX | QL_OUT_DA | QL_OUT_DB);
+}
+
+size_t qlora_linear_bwd_group_act8_workspace_for(const int64_t* rows, int32_t nw, int64_t cols, int64_t T, int32_t r,
+                                                 int outputs) {
     if (rows == nullptr || nw < 1 || nw > kGemmMaxGroup || cols <= 0 || T <= 0 || r < 0 || r > QL_MAX_RANK) return 0;
     for (int i = 0; i < nw; ++i)
         if (rows[i] <= 0) return 0;
-    return carve_bwd8(nullptr, rows, nw, cols, T, r, true, true, true, true, false).bytes;
+    return carve_bwd8(nullptr, rows, nw, cols, T, r, true, outputs & QL_OUT_DX, outputs & QL_OUT_DA,
+                      outputs & QL_OUT_DB, false)
+        .bytes;
 }
 
 int qlora_linear_bwd_group_act8(const ql_nf4_weight* const* w, int32_t nw, const ql_act8* X8, const uint16_t* const* dY,

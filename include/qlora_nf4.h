@@ -570,9 +570,17 @@ int qlora_swiglu_bwd(const ql_act8* gate8, const ql_act8* up8, const uint16_t* d
  * checkpoint of another shape and QL_ERR_UNSUPPORTED for p outside [0, 1) or
  * nonzero without a mask. The workspace is
  * qlora_linear_bwd_act8_workspace(...) bytes, dropout nonzero when keep is
- * given.
+ * given; a call that asks for fewer outputs needs only
+ * qlora_linear_bwd_act8_workspace_for(...) bytes, outputs the QL_OUT_* of those
+ * it asks for (without dX the product's split partials are left out, 64 MB at
+ * 4096 x 4096 and 1024 tokens).
  */
+#define QL_OUT_DX 1
+#define QL_OUT_DA 2
+#define QL_OUT_DB 4
 size_t qlora_linear_bwd_act8_workspace(int64_t rows, int64_t cols, int64_t T, int32_t r, int dropout);
+size_t qlora_linear_bwd_act8_workspace_for(int64_t rows, int64_t cols, int64_t T, int32_t r, int dropout,
+                                           int outputs);
 int qlora_linear_bwd_act8(const ql_nf4_weight* w, const ql_act8* X8, const uint16_t* dY, int64_t T,
                           const uint16_t* A, const uint16_t* B, int32_t r, float scale, const uint8_t* keep,
                           float p, const float* U_saved, uint16_t* dX, float* dA, float* dB, int accumulate,
@@ -584,10 +592,13 @@ int qlora_linear_bwd_act8(const ql_nf4_weight* w, const ql_act8* X8, const uint1
  * and dB[i] bitwise those of qlora_linear_bwd_act8 for layer i. U_saved[i] is
  * required where dB[i] is wanted, X8 where any dA[i] is. Other arguments and
  * errors as qlora_linear_bwd_group; the workspace is
- * qlora_linear_bwd_group_act8_workspace(...) bytes.
+ * qlora_linear_bwd_group_act8_workspace(...) bytes, or with outputs the
+ * QL_OUT_* that any layer asks for qlora_linear_bwd_group_act8_workspace_for(...).
  */
 size_t qlora_linear_bwd_group_act8_workspace(const int64_t* rows, int32_t nw, int64_t cols, int64_t T,
                                              int32_t r);
+size_t qlora_linear_bwd_group_act8_workspace_for(const int64_t* rows, int32_t nw, int64_t cols, int64_t T,
+                                                 int32_t r, int outputs);
 int qlora_linear_bwd_group_act8(const ql_nf4_weight* const* w, int32_t nw, const ql_act8* X8,
                                 const uint16_t* const* dY, int64_t T, const uint16_t* const* A,
                                 const uint16_t* const* B, int32_t r, float scale,

@@ -128,18 +128,28 @@ __global__ __launch_bounds__(kThreads) void q4g_quantize_kernel(const void* __re
         lo = umax_(l2[0], l2[1]) << 16;
     }
     group_range<G>(hi, lo);
-    const float top = __int_as_float(hi), bottom = static_cast<int>(lo) < 0 ? __uint_as_float(lo & 0x7FFFFFFFu) : 0.0f;
+    const float top = __int_as_float(hi);
+    float bottom = static_cast<int>(lo) < 0 ? __uint_as_float(lo & 0x7FFFFFFFu) : 0.0f;
     const bool sym = zero == nullptr;
     float s = sym ? quotient(fmaxf(top, bottom), 7.0f, 1.0f / 7.0f) : quotient(top + bottom, 15.0f, 1.0f / 15.0f);
     if constexpr (!SF32) s = __uint_as_float(pack_bf16x2(s, 0.0f) << 16);
     const bool live = s >= 0x1p-126f;  // below: the group is held as zeros
     if (!live) s = 0.0f;
     // the remainder of a quotient by a scale under about 2^-102 may have places under
-    // fp32's last: small scales and their values come up by 2^64 first, exactly
-    const float up = s < 0x1p-64f ? 0x1p64f : 1.0f, su = s * up, inv = 1.0f / su;
+    // fp32's last: small scales and their values come up by 2^64 first, exactly (by a
+    // branch of the wave: products for all took 11008 x 4096 from 23.6 to 25.2 us)
+    float su = s;
+    if (__builtin_expect(__any(s < 0x1p-64f), 0)) {
+        const float up = s < 0x1p-64f ? 0x1p64f : 1.0f;
+        su *= up;
+        bottom *= up;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * up);
+    }
+    const float inv = 1.0f / su;
     constexpr float kRound = 12582912.0f;  // 1.5 2^23
     constexpr int kRoundBits = 0x4B400000;
-    auto nearest = [&](float a) { return __float_as_int(quotient(a * up, su, inv) + kRound) - kRoundBits; };
+    auto nearest = [&](float a) { return __float_as_int(quotient(a, su, inv) + kRound) - kRoundBits; };
     const int z = (sym || !live) ? 8 : std::min(nearest(bottom), 15);
     uint32_t c = 0x88888888u;
     if (live) {

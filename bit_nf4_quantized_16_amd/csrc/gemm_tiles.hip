@@ -1058,7 +1058,10 @@ int launch_gemm_dx(const NF4Dev& w, const uint16_t* dY, const uint16_t* Gp, cons
     if (keep != nullptr && rp > 0) {
         a.keep = keep;
         a.c = c;
-        return launch_tiles<true, false, true>(a, split_ws, QL_KERNEL_DX_KEEP, "dequant GEMM dX with dropout", stream);
+        timer_begin(QL_KERNEL_DX_KEEP, stream);
+        const int s = launch_tiles<true, false, true>(a, split_ws, QL_KERNEL_GEMM_DX, "dequant GEMM dX with dropout", stream);
+        timer_end(QL_KERNEL_DX_KEEP, stream);
+        return s;
     }
     return launch_tiles<true>(a, split_ws, QL_KERNEL_GEMM_DX, "dequant GEMM dX", stream);
 }

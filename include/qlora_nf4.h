@@ -749,7 +749,7 @@ const char* qlora_last_error(void);
 #define QL_KERNEL_MERGE 8
 #define QL_KERNEL_QERROR 9
 #define QL_KERNEL_KEEP_APPLY 10
-#define QL_KERNEL_DX_KEEP 11 /* the dX GEMM with dropout's masked adapter term (without: QL_KERNEL_GEMM_DX) */
+#define QL_KERNEL_DX_KEEP 11 /* of QL_KERNEL_GEMM_DX, those with dropout's masked adapter term */
 #define QL_KERNEL_ADAMW 12
 #define QL_KERNEL_ACT8 13
 #define QL_KERNEL_SWIGLU 14

@@ -127,3 +127,16 @@ def test_repeated_and_captured(qn):
         for a, b in zip(out, step()):
             assert torch.equal(a, b)
     assert one[0].shape == (300, 320)
+
+
+def test_timers_count_the_masked_product(qn):
+    c = Case(qn, 100, 136, 128, 8, 0.2, seed=7)
+    timers = [qn.KernelTimer(k) for k in (qn._lib.QL_KERNEL_GEMM_DX, qn._lib.QL_KERNEL_DX_KEEP)]
+    for bits, p, want in ((c.bits, 0.2, [1, 1]), (None, 0.0, [1, 0])):
+        for t in timers:
+            t.arm()
+        qn.qlora_linear_bwd(c.w, c.X, c.dY, c.A, c.B, c.s, need_da=False, need_db=False, keep=bits, p=p)
+        torch.cuda.synchronize()
+        assert [t.read()[0] for t in timers] == want
+        for t in timers:
+            t.disarm()

@@ -31,8 +31,8 @@
 // What bounds it: the instructions that expand M and carry it through LDS to
 // the transposed operand, each wave's chunk after chunk. N = K = 4096, rank 16,
 // T = 1024: 9.7 us replayed (12.7 MB, 1.3 TB/s). N = 4096, K = 11008, rank 64,
-// T = 4096: 4.9 us for the terms, 51.8 here (79 MB, 1.5 TB/s; 24 GFLOP of term
-// products), 5.3 for the partials. Eight 16-column tiles a wave there: 122 us
+// T = 4096: 5.0 us for the terms, 53.1 here (79 MB, 1.5 TB/s; 24 GFLOP of term
+// products), 5.1 for the partials. Eight 16-column tiles a wave there: 122 us
 // for the whole (few workgroups), two waves' loads more in flight at 128
 // registers: 107.
 #include <algorithm>
@@ -505,7 +505,7 @@ int launch_act8_grads(Act8GradArgs a, float* part, hipStream_t stream) {
         hipLaunchKernelGGL(act8_terms_kernel, dim3(static_cast<uint32_t>(ceil_div(units, 4)), c1 > 0 ? 2 : 1), dim3(256), 0,
                            stream, a, rt, units);
     }
-    // Rank 16 and few columns: tiles half as wide, for workgroups on all CUs.
+    // Ranks to 64 and few columns: tiles half as wide, for workgroups on all CUs.
     const bool narrow = rt <= 4 && ceil_div(c0, kCols) + ceil_div(c1, kCols) <= 128;
     const int cols = narrow ? 32 : kCols;
     a.nblk0 = static_cast<int>(ceil_div(c0, cols));

@@ -870,7 +870,9 @@ int launch_wide_variant(const Q4GLinearArgs& a, hipStream_t stream) {
 //   T = 16  11008 x 4096 (64) 11.6 | 13.2, (32) 12.4 | 15.2, 22016 x 8192 (32) 44.6 | 42.6
 // At 16 tokens the wide kernel's rule gains with groups of 128 (10240 x 8192
 // 18.2 -> 16.2, 22016 x 8192 31.1 -> 29.2) and loses with groups of 32 (19.3 ->
-// 25.9, 41.8 -> 47.1).
+// 25.9, 41.8 -> 47.1); with groups of 64 it is even but for the largest (4096 x
+// 4096 6.4 | 6.5, 11008 x 4096 11.4 | 10.9, 10240 x 8192 19.0 | 19.1, 22016 x 8192
+// 29.0 | 32.6), so they go with those of 32.
 template <int GL, bool SF32>
 int launch_linear_variant(const Q4GLinearArgs& a, hipStream_t stream) {
     const bool two = ceil_div(a.N, 16) > 1024;

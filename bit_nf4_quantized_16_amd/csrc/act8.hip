@@ -49,7 +49,8 @@ __global__ __launch_bounds__(kThreads) void act8_dequantize_kernel(const uint8_t
 }
 
 // 1 / (1 + e^-g): v_exp_f32 and v_rcp_f32 (1 ulp each; the result is rounded
-// to bf16 by its users). e^-g = inf gives 0, e^-g = 0 gives 1.
+// to bf16 by its users; v_rcp_f32 gives zero for results under 2^-126, g under
+// -87.33, where h is under 1e-36 |u|). e^-g = 0 gives 1.
 __device__ __forceinline__ float sigmoid(float g) {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * g));
 }

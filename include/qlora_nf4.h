@@ -537,8 +537,10 @@ int act8_dequantize(const ql_act8* a, void* out, int out_dtype, void* stream);
  *   gate8, up8 (backward)  the forward's; g and u are their restored values
  *   dH     [rows, cols] bf16;  dgate, dup  out, [rows, cols] bf16
  *
- * sigmoid(g) = 1 / (1 + e^-g) in fp32, so g = -inf gives NaN. Outputs must not
- * alias inputs or one another. rows == 0 is a no-op.
+ * sigmoid(g) = 1 / (1 + e^-g) in fp32, zero where it is under 2^-126 (g under
+ * -87.33), so g = -inf gives NaN; a g that its checkpoint restores as infinity
+ * gives NaN in dgate (infinity times 1 - p = 0). Outputs must not alias inputs
+ * or one another. rows == 0 is a no-op.
  * Errors: as act8_quantize, QL_ERR_SHAPE also for checkpoints of other shapes.
  */
 int qlora_swiglu_fwd(const uint16_t* gate, const uint16_t* up, int64_t rows, int64_t cols, uint16_t* H,

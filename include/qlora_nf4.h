@@ -487,7 +487,8 @@ int qlora_linear_bwd_dropout(const ql_nf4_weight* w, const uint16_t* X, const ui
  *               QL_ACT8_BLOCK (32)
  *   codes  [rows, cols] u8, OCP FP8 E4M3FN codes
  *   scale  [rows, cols / 32] u8, one per block of 32 consecutive values of a
- *          row: the block's scale is 2^(scale - 127)
+ *          row: the block's scale is 2^(scale - 127) (act8_quantize writes 3 to
+ *          247; 0 to 2 restore rounded to bf16, 255 stands for NaN)
  *
  * With a the largest magnitude among the block's finite values, the scale is
  * 2^k with k the least integer such that a 2^-k <= 448, and at least -124. A

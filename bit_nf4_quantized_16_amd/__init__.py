@@ -809,7 +809,8 @@ class QLoRALinearFunction(torch.autograd.Function):
             X8 = None  # only dA reads it
             if need_a:
                 X8 = act8_quantize(X.contiguous()) if act8 is True else act8
-            ctx.save_for_backward(X8.codes if need_a else None, X8.scale if need_a else None, A, B, U if need_b else None)
+            ctx.save_for_backward(X8.codes if need_a else None, X8.scale if need_a else None, A, B,
+                                  U if need_b else None, keep)
         else:
             ctx.save_for_backward(X, A, B, U)
         ctx.w = w
@@ -830,12 +831,12 @@ class QLoRALinearFunction(torch.autograd.Function):
     @staticmethod
     @_first_order_only
     def _backward_act8(ctx, dY):
-        codes, xs, A, B, U = ctx.saved_tensors
+        codes, xs, A, B, U, keep = ctx.saved_tensors
         need = ctx.needs_input_grad
         X8 = Act8(*codes.shape, codes, xs) if need[1] else None
         dX, dA, dB = qlora_linear_bwd_act8(ctx.w, X8, dY.contiguous().to(torch.bfloat16), A.contiguous(),
                                            B.contiguous(), ctx.scale, U=U, need_dx=need[0], need_da=need[1],
-                                           need_db=need[2], keep=ctx.keep, p=ctx.p)
+                                           need_db=need[2], keep=keep, p=ctx.p)
         return (dX, dA.to(A.dtype) if need[1] else None, dB.to(B.dtype) if need[2] else None,
                 None, None, None, None, None)
 

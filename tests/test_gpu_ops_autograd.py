@@ -36,6 +36,18 @@ def test_a_checkpoint_written_again_is_refused_in_the_backward(qn):
         torch.autograd.grad(Y, A, dY)
 
 
+def test_a_keep_mask_written_again_is_refused_in_the_backward(qn):
+    """The next step's mask drawn into the same memory before the backward."""
+    w, X, dY, A, B = _layer(qn)
+    A.requires_grad_()
+    keep = workloads.pack_keep_bits(workloads.keep_mask(33, 128, 0.5, 8)).cuda()
+    Y = qn.QLoRALinearFunction.apply(X, A, B, w, 1.0, keep, 0.5, True)
+    torch.autograd.grad(Y, A, dY, retain_graph=True)
+    keep.copy_(workloads.pack_keep_bits(workloads.keep_mask(33, 128, 0.5, 9)).cuda())
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        torch.autograd.grad(Y, A, dY)
+
+
 def test_every_out_counts_as_modified(qn):
     w, X, dY, A, B = _layer(qn)
     x8 = qn.act8_quantize(X)
@@ -130,7 +142,7 @@ def test_linear_keeps_and_computes_what_is_needed(qn, need, own):
     want = torch.autograd.grad(qn.QLoRALinearFunction.apply(*full, w, 1.0, None, 0.0, True), full, dY)
     ins = [t.clone().requires_grad_(n) for t, n in zip((X, A, B), need)]
     Y = qn.QLoRALinearFunction.apply(*ins, w, 1.0, None, 0.0, qn.act8_quantize(X) if own else True)
-    codes, scale, _, _, U = Y.grad_fn.saved_tensors
+    codes, scale, _, _, U, _ = Y.grad_fn.saved_tensors
     assert (codes is not None) == need[1] and (scale is not None) == need[1] and (U is not None) == need[2]
     timer = qn.KernelTimer(qn._lib.QL_KERNEL_ACT8_GRAD)
     timer.arm()

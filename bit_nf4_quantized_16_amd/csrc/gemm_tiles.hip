@@ -36,7 +36,7 @@
 // steps first, multiply the accumulators by c or 0, and let the main loop add
 // dY W' to them. The adapter term costs no second accumulators and no pass of
 // its own over dX, and dX is rounded once. 11008 x 4096, T = 1024, r = 16, cold:
-// 134 us against 127 without dropout (a pass over the rounded dX took 12.6).
+// 130 us against 126 without dropout (a pass over the rounded dX took 12.6).
 #include <algorithm>
 #include <cstdlib>
 #include <cstring>
@@ -441,6 +441,151 @@ __global__ __launch_bounds__(64 * WA * WT, 512 / (64 * WA * WT)) void tile_gemm_
         }
     };
 
+    // Pipeline (two steps per iteration, stages named statically):
+    //   step s:   token loads for s+1 -> the other stage; codes for s+2 -> the
+    //             free register set; MFMAs on stage s; expand step s+1.
+    Codes<CC> cs0, cs1;
+
+    // With dropout: the main loop's first loads, and meanwhile the rank steps
+    // (of the first split) through the second stage and the mask on their sums
+    // (the loads after them: N = K = 4096, T = 300, r = 16 62 us, before them 60).
+    auto masked_term = [&]() {
+        dma(sb, sX0);
+        gcodes(sb, cs0);
+        gcodes(min(sb + 1, msteps - 1), cs1);
+        if (split == 0) {
+            uint32_t bits[SA][ST];  // a sub-tile's 32 columns of the lane's token: one word of the mask
+#pragma unroll
+            for (int a = 0; a < SA; ++a)
+#pragma unroll
+                for (int b = 0; b < ST; ++b) {
+                    const int64_t k = m0 + wa * MW + a * 32, t = t0 + wt * TW + b * 32 + (lane & 31);
+                    bits[a][b] = 0;
+                    if (k < p.K && t < p.T) bits[a][b] = *reinterpret_cast<const uint32_t*>(p.keep + t * (p.K / 8) + k / 8);
+                }
+            for (int j0 = 0; j0 < p.rp; j0 += kStep) {
+#pragma unroll
+                for (int i = 0; i < TT * 8 / NTHR; ++i) {
+                    const int c = tid + NTHR * i;
+                    const int row = c >> 3, lc = c & 7;
+                    const int64_t t = t0 + row;
+                    const uint4 v = (t < p.T) ? ld16(p.lt + t * p.rp + j0 + 8 * lc) : make_uint4(0, 0, 0, 0);
+                    st16(sX1 + row * kStep + 8 * (lc ^ swz(row)), v);
+                }
+#pragma unroll
+                for (int i = 0; i < TA * 8 / NTHR; ++i) {
+                    const int c = tid + NTHR * i;
+                    const int row = c / (TA / 8), col = 8 * (c % (TA / 8));
+                    const int64_t j = j0 + row;
+                    const int64_t k = m0 + col;
+                    const uint4 v = (j < p.r_la && k < p.K) ? ld16(p.la + j * p.ld_la + k) : make_uint4(0, 0, 0, 0);
+                    st16(sA1 + row * LDA + dx_col(row, col), v);
+                }
+                __syncthreads();
+                compute(sA1, sX1);
+                __syncthreads();
+            }
+            // acc element r of a sub-tile is its column 8 (r / 4) + 4 (lane / 32) + r % 4
+#pragma unroll
+            for (int a = 0; a < SA; ++a)
+#pragma unroll
+                for (int b = 0; b < ST; ++b) {
+                    const uint32_t m = bits[a][b] >> (4 * (lane >> 5));
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        acc[a][b][r] = (m >> (8 * (r / 4) + r % 4)) & 1u ? p.c * acc[a][b][r] : 0.0f;
+                }
+        }
+    };
+
+    if constexpr (GRP && DX) {
+        // A grouped dX: the same pipeline (dX form) over the part of [sb, se)
+        // each layer owns, layer by layer into the same accumulators; each
+        // part ends with every wave past a barrier after its last MFMA, so
+        // the stages are free for the next. (Kept apart from the one-layer
+        // text below, whose code it would otherwise change.)
+        for (int L = 0; L < p.ng; ++L) {
+            const int b = max(sb, p.gstep[L]), e = min(se, p.gstep[L + 1]);
+            if (b >= e) continue;
+            gw = p.gl[L].w;
+            gact = p.gl[L].act;
+            gN = p.gl[L].N;
+            gmu = DQ ? *p.gl[L].w.mean : 0.0f;
+            gbase = p.gstep[L];
+            dma(b, sX0);
+            gcodes(b, cs0);
+            gcodes(min(b + 1, e - 1), cs1);
+            expand(b, cs0, sA0);
+            __syncthreads();
+            for (int s = b; s < e; s += 2) {
+                dma(min(s + 1, e - 1), sX1);
+                __builtin_amdgcn_sched_barrier(0);
+                gcodes(min(s + 2, e - 1), cs0);
+                if (expand_first) {
+                    expand(s + 1, cs1, sA1);
+                    compute(sA0, sX0);
+                } else {
+                    compute(sA0, sX0);
+                    expand(s + 1, cs1, sA1);
+                }
+                stage_barrier<CC>();
+                if (s + 1 >= e) break;
+                dma(min(s + 2, e - 1), sX0);
+                __builtin_amdgcn_sched_barrier(0);
+                gcodes(min(s + 3, e - 1), cs1);
+                if (expand_first) {
+                    expand(s + 2, cs0, sA0);
+                    compute(sA1, sX1);
+                } else {
+                    compute(sA1, sX1);
+                    expand(s + 2, cs0, sA0);
+                }
+                stage_barrier<CC>();
+            }
+        }
+    } else if (sb < se) {
+    if constexpr (KEEP) {
+        masked_term();
+    } else {
+        dma(sb, sX0);
+        gcodes(sb, cs0);
+        gcodes(min(sb + 1, msteps - 1), cs1);
+    }
+    expand(sb, cs0, sA0);
+    __syncthreads();
+    for (int s = sb; s < msteps; s += 2) {
+        dma(min(s + 1, msteps - 1), sX1);
+        __builtin_amdgcn_sched_barrier(0);  // the token loads stay ahead of the code loads
+        gcodes(min(s + 2, msteps - 1), cs0);
+        interleave_step();
+        if constexpr (!DX) {
+            compute_expand(sA0, sX0, cs1, sA1);
+        } else if (expand_first) {
+            expand(s + 1, cs1, sA1);
+            compute(sA0, sX0);
+        } else {
+            compute(sA0, sX0);
+            expand(s + 1, cs1, sA1);
+        }
+        stage_barrier<CC>();
+        if (s + 1 >= msteps) break;
+        dma(min(s + 2, msteps - 1), sX0);
+        __builtin_amdgcn_sched_barrier(0);
+        gcodes(min(s + 3, msteps - 1), cs1);
+        interleave_step();
+        if constexpr (!DX) {
+            compute_expand(sA1, sX1, cs0, sA0);
+        } else if (expand_first) {
+            expand(s + 2, cs0, sA0);
+            compute(sA1, sX1);
+        } else {
+            compute(sA1, sX1);
+            expand(s + 2, cs0, sA0);
+        }
+        stage_barrier<CC>();
+    }
+    }  // sb < se
+
     // U (forward) or G (dX) inside the launch: the token operand of the rank
     // step from the words of this tile's tokens (TT x r_u, at most 8 a
     // thread), each converted as the separate projection converts it, bf16(s_u v), and
@@ -540,14 +685,13 @@ __global__ __launch_bounds__(64 * WA * WT, 512 / (64 * WA * WT)) void tile_gemm_
         }
     };
 
-    // LoRA term: rp/64 reduction steps over the rank, staged directly
+    // LoRA term: rp/64 more reduction steps over the rank, staged directly
     // (by the first split only; in a grouped dX, each layer's by split
     // L % splits: rank step ls of this split is step ls % nr of layer
     // split + (ls / nr) splits).
     const int nr = p.rp / kStep;
     constexpr bool kGdx = GRP && DX, kGfwd = GRP && !DX;
-    const int nls = kGdx ? (split < p.ng ? nr * ((p.ng - 1 - split) / p.splits + 1) : 0) : (split == 0 ? nr : 0);
-    auto rank_steps = [&]() {
+    const int nls = KEEP ? 0 : kGdx ? (split < p.ng ? nr * ((p.ng - 1 - split) / p.splits + 1) : 0) : (split == 0 ? nr : 0);
     for (int ls = 0; ls < nls; ++ls) {
         const int rl = kGdx ? split + (ls / nr) * p.splits : fl;  // the rank step's layer
         const uint16_t* const lt = GRP ? p.gl[rl].lt : p.lt;
@@ -591,117 +735,6 @@ __global__ __launch_bounds__(64 * WA * WT, 512 / (64 * WA * WT)) void tile_gemm_
         compute(sA0, sX0);
         __syncthreads();
     }
-    };
-
-    if constexpr (KEEP) {
-        rank_steps();
-        // acc element r of sub-tile (a, b) is column 32 a + 8 (r / 4) + 4 (lane / 32) + r % 4
-        // of token 32 b + lane % 32 (of the wave tile): 32 columns are one word of the mask
-        if (nls > 0) {
-#pragma unroll
-            for (int a = 0; a < SA; ++a)
-#pragma unroll
-                for (int b = 0; b < ST; ++b) {
-                    const int64_t k = m0 + wa * MW + a * 32, t = t0 + wt * TW + b * 32 + (lane & 31);
-                    uint32_t bits = 0;
-                    if (k < p.K && t < p.T) bits = *reinterpret_cast<const uint32_t*>(p.keep + t * (p.K / 8) + k / 8);
-                    bits >>= 4 * (lane >> 5);
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        acc[a][b][r] = (bits >> (8 * (r / 4) + r % 4)) & 1u ? p.c * acc[a][b][r] : 0.0f;
-                }
-        }
-    }
-
-    // Pipeline (two steps per iteration, stages named statically):
-    //   step s:   token loads for s+1 -> the other stage; codes for s+2 -> the
-    //             free register set; MFMAs on stage s; expand step s+1.
-    Codes<CC> cs0, cs1;
-    if constexpr (GRP && DX) {
-        // A grouped dX: the same pipeline (dX form) over the part of [sb, se)
-        // each layer owns, layer by layer into the same accumulators; each
-        // part ends with every wave past a barrier after its last MFMA, so
-        // the stages are free for the next. (Kept apart from the one-layer
-        // text below, whose code it would otherwise change.)
-        for (int L = 0; L < p.ng; ++L) {
-            const int b = max(sb, p.gstep[L]), e = min(se, p.gstep[L + 1]);
-            if (b >= e) continue;
-            gw = p.gl[L].w;
-            gact = p.gl[L].act;
-            gN = p.gl[L].N;
-            gmu = DQ ? *p.gl[L].w.mean : 0.0f;
-            gbase = p.gstep[L];
-            dma(b, sX0);
-            gcodes(b, cs0);
-            gcodes(min(b + 1, e - 1), cs1);
-            expand(b, cs0, sA0);
-            __syncthreads();
-            for (int s = b; s < e; s += 2) {
-                dma(min(s + 1, e - 1), sX1);
-                __builtin_amdgcn_sched_barrier(0);
-                gcodes(min(s + 2, e - 1), cs0);
-                if (expand_first) {
-                    expand(s + 1, cs1, sA1);
-                    compute(sA0, sX0);
-                } else {
-                    compute(sA0, sX0);
-                    expand(s + 1, cs1, sA1);
-                }
-                stage_barrier<CC>();
-                if (s + 1 >= e) break;
-                dma(min(s + 2, e - 1), sX0);
-                __builtin_amdgcn_sched_barrier(0);
-                gcodes(min(s + 3, e - 1), cs1);
-                if (expand_first) {
-                    expand(s + 2, cs0, sA0);
-                    compute(sA1, sX1);
-                } else {
-                    compute(sA1, sX1);
-                    expand(s + 2, cs0, sA0);
-                }
-                stage_barrier<CC>();
-            }
-        }
-    } else if (sb < se) {
-    dma(sb, sX0);
-    gcodes(sb, cs0);
-    gcodes(min(sb + 1, msteps - 1), cs1);
-    expand(sb, cs0, sA0);
-    __syncthreads();
-    for (int s = sb; s < msteps; s += 2) {
-        dma(min(s + 1, msteps - 1), sX1);
-        __builtin_amdgcn_sched_barrier(0);  // the token loads stay ahead of the code loads
-        gcodes(min(s + 2, msteps - 1), cs0);
-        interleave_step();
-        if constexpr (!DX) {
-            compute_expand(sA0, sX0, cs1, sA1);
-        } else if (expand_first) {
-            expand(s + 1, cs1, sA1);
-            compute(sA0, sX0);
-        } else {
-            compute(sA0, sX0);
-            expand(s + 1, cs1, sA1);
-        }
-        stage_barrier<CC>();
-        if (s + 1 >= msteps) break;
-        dma(min(s + 2, msteps - 1), sX0);
-        __builtin_amdgcn_sched_barrier(0);
-        gcodes(min(s + 3, msteps - 1), cs1);
-        interleave_step();
-        if constexpr (!DX) {
-            compute_expand(sA1, sX1, cs0, sA0);
-        } else if (expand_first) {
-            expand(s + 2, cs0, sA0);
-            compute(sA1, sX1);
-        } else {
-            compute(sA1, sX1);
-            expand(s + 2, cs0, sA0);
-        }
-        stage_barrier<CC>();
-    }
-    }  // sb < se
-
-    if constexpr (!KEEP) rank_steps();
 
     // Epilogue: D[m][t] -> out[t][m]; acc element r of sub-tile (a, b) sits at
     // m = 32a + 8(r/4) + 4(lane/32) + r%4, t = 32b + lane%32 of the wave tile.

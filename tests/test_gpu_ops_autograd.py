@@ -78,8 +78,12 @@ def test_every_out_counts_as_modified(qn):
 def test_second_order_by_the_adapters_is_refused(qn):
     w, X, dY, A, B = _layer(qn)
     A, B, dY = (t.requires_grad_() for t in (A, B, dY))
+    spread = torch.stack([B, B], dim=2)[:, :, 0]  # B's values, not contiguous
+    assert not spread.is_contiguous()
     for call in (lambda: qn.QLoRALinearFunction.apply(X, A, B, w, 1.0, None, 0.0, True),
-                 lambda: qn.QLoRAGroupAct8Function.apply(X, None, 1.0, [w], A, B)[0]):
+                 lambda: qn.QLoRALinearFunction.apply(X, A, spread, w, 1.0, None, 0.0, True),
+                 lambda: qn.QLoRAGroupAct8Function.apply(X, None, 1.0, [w], A, B)[0],
+                 lambda: qn.QLoRAGroupAct8Function.apply(X, None, 1.0, [w], A, spread)[0]):
         gA, = torch.autograd.grad(call(), A, dY, create_graph=True)
         for leaf in (B, dY):  # dA = (s dY B)^T X
             with pytest.raises(RuntimeError, match="cannot be differentiated again"):

@@ -42,6 +42,16 @@ __all__ = [
     "q4g_quantize",
     "q4g_dequantize",
     "q4g_linear_fwd",
+    "norm_fwd",
+    "norm_bwd",
+    "token_logp",
+    "PreferenceState",
+    "preference_loss_fwd",
+    "preference_loss_bwd",
+    "distill_loss",
+    "NormFunction",
+    "PreferenceLossFunction",
+    "DistillLossFunction",
     "QLoRALinearFunction",
     "QLoRAGroupFunction",
     "QLoRAGroupAct8Function",
@@ -722,6 +732,205 @@ def q4g_linear_fwd(w, X, out=None):
     return out
 
 
+# ---- norms -----------------------------------------------------------------
+def _typed(t, name, shape, device=None):
+    """t, checked like _tensor's, bf16 or fp32; and its QL_ dtype."""
+    if not isinstance(t, torch.Tensor):
+        _refuse(_lib.QL_ERR_NULL, "%s is no tensor" % name)
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        _refuse(_lib.QL_ERR_UNSUPPORTED, "%s is %s, expected bf16 or fp32" % (name, t.dtype))
+    _tensor(t, name, t.dtype, shape, device)
+    return code
+
+
+def norm_fwd(X, weight, bias=None, eps=1e-5, rms=False, stats=True):
+    """Layer norm (``rms``: root-mean-square norm) of the rows of X [rows,
+    cols], bf16 or fp32; weight and bias [cols] of one type, bf16 or fp32.
+    Returns (Y, mean, rstd): Y of X's type, the statistics fp32 [rows] for
+    norm_bwd (None without ``stats``; mean None with ``rms``)."""
+    if not isinstance(X, torch.Tensor) or X.dim() != 2:
+        _refuse(_lib.QL_ERR_SHAPE, "X is not 2-D")
+    rows, cols = X.shape
+    xd, dev = _typed(X, "X", X.shape), X.device
+    wd = _typed(weight, "weight", (cols,), dev)
+    if bias is not None:
+        _tensor(bias, "bias", weight.dtype, (cols,), dev)
+    Y = torch.empty_like(X)
+    mean = torch.empty(rows, dtype=torch.float32, device=dev) if stats and not rms else None
+    rstd = torch.empty(rows, dtype=torch.float32, device=dev) if stats else None
+    _launch(dev, lib.qlora_norm_fwd, X.data_ptr(), xd, rows, cols, weight.data_ptr(), _addr(bias), wd, float(eps),
+            1 if rms else 0, Y.data_ptr(), _addr(mean), _addr(rstd))
+    return Y, mean, rstd
+
+
+def norm_bwd(X, weight, dY, mean, rstd, need_dx=True, need_dw=True, need_db=True, dW=None, dB=None, accumulate=False):
+    """Backward of norm_fwd from its statistics (mean None: the
+    root-mean-square form). Returns (dX of X's type, dweight, dbias fp32
+    [cols]), None for those not wanted."""
+    if not isinstance(X, torch.Tensor) or X.dim() != 2:
+        _refuse(_lib.QL_ERR_SHAPE, "X is not 2-D")
+    rows, cols = X.shape
+    xd, dev = _typed(X, "X", X.shape), X.device
+    wd = _typed(weight, "weight", (cols,), dev)
+    _tensor(dY, "dY", X.dtype, X.shape, dev)
+    if mean is not None:
+        _tensor(mean, "mean", torch.float32, (rows,), dev)
+    _tensor(rstd, "rstd", torch.float32, (rows,), dev)
+    dX = torch.empty_like(X) if need_dx else None
+    dW = _grads(need_dw, dW, (cols,), "dW", accumulate, dev)
+    dB = _grads(need_db, dB, (cols,), "dB", accumulate, dev)
+    ws, wsb = _workspace(lib.qlora_norm_bwd_workspace(rows, cols) if need_dw or need_db else 0, dev)
+    _launch(dev, lib.qlora_norm_bwd, X.data_ptr(), xd, rows, cols, weight.data_ptr(), wd, dY.data_ptr(), _addr(mean),
+            rstd.data_ptr(), _addr(dX), _addr(dW), _addr(dB), 1 if accumulate else 0, _addr(ws), wsb)
+    return dX, dW, dB
+
+
+# ---- losses on logits --------------------------------------------------------
+def _logits(z):
+    """(QL_ dtype, T, V, row stride) of logits, checked: a 2-D device tensor
+    whose rows are runs of values, any number of values apart."""
+    if not isinstance(z, torch.Tensor) or z.dim() != 2:
+        _refuse(_lib.QL_ERR_SHAPE, "logits are not 2-D")
+    code = _DTYPES.get(z.dtype)
+    if code is None:
+        _refuse(_lib.QL_ERR_UNSUPPORTED, "logits are %s, expected bf16 or fp32" % z.dtype)
+    if not z.is_cuda:
+        _refuse(_lib.QL_ERR_UNSUPPORTED, "logits are on %s, expected a GPU" % z.device)
+    T, V = z.shape
+    ld, step = z.stride()
+    if T <= 1:
+        ld = V
+    if (step != 1 and V > 1) or ld < V:
+        _refuse(_lib.QL_ERR_UNSUPPORTED, "logits have strides %s" % (z.stride(),))
+    return code, T, V, ld
+
+
+def _dlogits(z, given, T, V, ld):
+    """A gradient laid out like z: the caller's, checked, or a new one."""
+    if given is not None:
+        if not isinstance(given, torch.Tensor):
+            _refuse(_lib.QL_ERR_NULL, "dlogits is no tensor")
+        if given.dtype != z.dtype or given.device != z.device:
+            _refuse(_lib.QL_ERR_UNSUPPORTED, "dlogits is %s on %s, logits %s on %s"
+                    % (given.dtype, given.device, z.dtype, z.device))
+        if given.shape != z.shape:
+            _refuse(_lib.QL_ERR_SHAPE, "dlogits is %s, logits %s" % (tuple(given.shape), tuple(z.shape)))
+        if (T > 1 and given.stride(0) != ld) or (V > 1 and given.stride(1) != 1):
+            _refuse(_lib.QL_ERR_UNSUPPORTED, "dlogits has strides %s, logits %s" % (given.stride(), z.stride()))
+        increment_version(given)  # written through its address
+        return given
+    off = z.data_ptr() % 16 // z.element_size()
+    if off == 0 and ld == V:
+        return torch.empty(T, V, dtype=z.dtype, device=z.device)
+    flat = torch.empty(off + max(T, 1) * ld, dtype=z.dtype, device=z.device)
+    return flat.as_strided((T, V), (ld, 1), off)
+
+
+def token_logp(logits, labels):
+    """Log probability of each row's label, fp32 [T]: logits [T, V] bf16 or
+    fp32, labels int64 [T]; 0 where the label is outside [0, V)."""
+    code, T, V, ld = _logits(logits)
+    dev = logits.device
+    _tensor(labels, "labels", torch.int64, (T,), dev)
+    out = torch.empty(T, dtype=torch.float32, device=dev)
+    ws, wsb = _workspace(lib.qlora_token_logp_workspace(T, V, code), dev)
+    _launch(dev, lib.qlora_token_logp, logits.data_ptr(), code, T, V, ld, labels.data_ptr(), out.data_ptr(), _addr(ws),
+            wsb)
+    return out
+
+
+_PREFERENCES = {"sigmoid": _lib.QL_PREF_SIGMOID, "hinge": _lib.QL_PREF_HINGE, "squared": _lib.QL_PREF_SQUARED}
+
+
+@dataclass
+class PreferenceState:
+    """What preference_loss_fwd leaves for preference_loss_bwd."""
+
+    pairs: int
+    rows: torch.Tensor  # fp32 [4, T]
+    logp: torch.Tensor  # fp32 [T], the labels' log probabilities
+
+
+def preference_loss_fwd(logits, labels, seq_start, ref_logp, beta=0.1, label_smoothing=0.0, kind="sigmoid",
+                        average=False):
+    """Loss on pairs of sequences packed in logits [T, V] (bf16 or fp32),
+    sequence s in rows seq_start[s] .. seq_start[s + 1] - 1, 2 i preferred over
+    2 i + 1. labels int64 [T] (outside [0, V): not counted), seq_start int64
+    [2 pairs + 1], ref_logp fp32 [2 pairs]: the sequences' log probabilities
+    (``average``: means over tokens) under the reference model. ``kind``
+    "sigmoid" (with ``label_smoothing``), "hinge" or "squared". Returns (loss
+    fp32 [pairs], the sequences' log probabilities fp32 [2 pairs], state)."""
+    code, T, V, ld = _logits(logits)
+    dev = logits.device
+    _tensor(labels, "labels", torch.int64, (T,), dev)
+    if not isinstance(ref_logp, torch.Tensor) or ref_logp.dim() != 1 or ref_logp.numel() % 2:
+        _refuse(_lib.QL_ERR_SHAPE, "ref_logp is no vector of an even length")
+    pairs = ref_logp.numel() // 2
+    _tensor(ref_logp, "ref_logp", torch.float32, (2 * pairs,), dev)
+    _tensor(seq_start, "seq_start", torch.int64, (2 * pairs + 1,), dev)
+    if kind not in _PREFERENCES:
+        _refuse(_lib.QL_ERR_UNSUPPORTED, "kind %r (%s)" % (kind, ", ".join(_PREFERENCES)))
+    loss = torch.empty(pairs, dtype=torch.float32, device=dev)
+    seq_logp = torch.empty(2 * pairs, dtype=torch.float32, device=dev)
+    state = PreferenceState(pairs, torch.empty(_lib.QL_PREF_STATE_ROWS, T, dtype=torch.float32, device=dev),
+                            torch.empty(T, dtype=torch.float32, device=dev))
+    ws, wsb = _workspace(lib.qlora_token_logp_workspace(T, V, code), dev)
+    _launch(dev, lib.qlora_preference_loss_fwd, logits.data_ptr(), code, T, V, ld, labels.data_ptr(),
+            seq_start.data_ptr(), pairs, ref_logp.data_ptr(), float(beta), float(label_smoothing), _PREFERENCES[kind],
+            1 if average else 0, loss.data_ptr(), seq_logp.data_ptr(), state.rows.data_ptr(), state.logp.data_ptr(),
+            _addr(ws), wsb)
+    return loss, seq_logp, state
+
+
+def preference_loss_bwd(logits, labels, state, dloss, dlogits=None):
+    """Gradient of preference_loss_fwd's loss with respect to the same logits,
+    dloss fp32 [pairs]. ``dlogits``: a tensor laid out like logits to write
+    into, logits itself among them."""
+    code, T, V, ld = _logits(logits)
+    dev = logits.device
+    _tensor(labels, "labels", torch.int64, (T,), dev)
+    _tensor(state.rows, "state", torch.float32, (_lib.QL_PREF_STATE_ROWS, T), dev)
+    _tensor(dloss, "dloss", torch.float32, (state.pairs,), dev)
+    dlogits = _dlogits(logits, dlogits, T, V, ld)
+    _launch(dev, lib.qlora_preference_loss_bwd, logits.data_ptr(), code, T, V, ld, labels.data_ptr(),
+            state.rows.data_ptr(), dloss.data_ptr(), state.pairs, dlogits.data_ptr())
+    return dlogits
+
+
+def distill_loss(logits, top_index, top_logits, labels=None, temperature=1.0, alpha=0.0, weight=None, need_loss=True,
+                 need_grad=False, dlogits=None):
+    """Distillation from a teacher's top logits: (1 - alpha) temperature^2
+    KL(teacher's top K || student) + alpha cross entropy of the labels, per row
+    of logits [T, V] (bf16 or fp32). top_index int64 [T, K], top_logits bf16 or
+    fp32 [T, K], K up to 256 (an index outside [0, V): absent); labels int64
+    [T] (outside [0, V): the row is not counted), needed with alpha. Returns
+    (loss fp32 [T], dlogits); with ``need_grad`` dlogits is the gradient of
+    sum_t weight[t] loss[t] (``weight`` fp32 [T], None: ones), formed in the
+    same pass; ``dlogits``: a tensor laid out like logits for it, logits itself
+    among them."""
+    code, T, V, ld = _logits(logits)
+    dev = logits.device
+    if not isinstance(top_index, torch.Tensor) or top_index.dim() != 2:
+        _refuse(_lib.QL_ERR_SHAPE, "top_index is not 2-D")
+    K = top_index.shape[1]
+    _tensor(top_index, "top_index", torch.int64, (T, K), dev)
+    top_code = _typed(top_logits, "top_logits", (T, K), dev)
+    if labels is not None:
+        _tensor(labels, "labels", torch.int64, (T,), dev)
+    elif alpha > 0:
+        _refuse(_lib.QL_ERR_NULL, "alpha %g without labels" % alpha)
+    if weight is not None:
+        _tensor(weight, "weight", torch.float32, (T,), dev)
+    loss = torch.empty(T, dtype=torch.float32, device=dev) if need_loss else None
+    grad = need_grad or dlogits is not None
+    dlogits = _dlogits(logits, dlogits, T, V, ld) if grad else None
+    _launch(dev, lib.qlora_distill_loss, logits.data_ptr(), code, T, V, ld, top_index.data_ptr(),
+            top_logits.data_ptr(), top_code, K, _addr(labels), float(temperature), float(alpha), _addr(weight),
+            _addr(loss), _addr(dlogits))
+    return loss, dlogits
+
+
 def paged_adamw_step(param, grad, exp_avg, exp_avg_sq, step, lr=2e-4, betas=(0.9, 0.999), eps=1e-8,
                      weight_decay=0.0, param_bf16=None, copy_stream=None):
     """One AdamW step (fp32 state) of a flat fp32 parameter tensor in place.
@@ -758,7 +967,8 @@ class _FirstOrderOnly(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, *_):
-        raise RuntimeError("the gradients from 8-bit checkpoints cannot be differentiated again")
+        raise RuntimeError("these gradients (from 8-bit checkpoints, of a norm, an epilogue or a loss on logits) "
+                           "cannot be differentiated again")
 
 
 @functools.lru_cache(None)
@@ -942,6 +1152,84 @@ class SwiGLUFunction(torch.autograd.Function):
         dg, du = swiglu_bwd(Act8(rows, cols, gc, gs), Act8(rows, cols, uc, us), dH.contiguous().to(torch.bfloat16))
         need = ctx.needs_input_grad
         return dg if need[0] else None, du if need[1] else None, None
+
+
+class NormFunction(torch.autograd.Function):
+    """autograd wrapper of the norms: apply(X, weight, bias, eps, rms); weight
+    and bias receive fp32 sums cast to their type. First order only."""
+
+    @staticmethod
+    def forward(ctx, X, weight, bias=None, eps=1e-5, rms=False):
+        Y, mean, rstd = norm_fwd(X.contiguous(), weight.contiguous(), bias.contiguous() if bias is not None else None,
+                                 eps, rms, stats=any(ctx.needs_input_grad[:3]))
+        ctx.save_for_backward(X, weight, mean, rstd)
+        ctx.tie = ()
+        return Y
+
+    @staticmethod
+    @_first_order_only
+    def backward(ctx, dY):
+        X, weight, mean, rstd = ctx.saved_tensors
+        need = (*ctx.needs_input_grad, False)[:3]  # without a bias argument
+        dX, dW, dB = norm_bwd(X.contiguous(), weight.contiguous(), dY.contiguous(), mean, rstd, *need)
+        return dX, dW.to(weight.dtype) if need[1] else None, dB.to(weight.dtype) if need[2] else None, None, None
+
+
+def _rows(z):
+    """z, or a copy of it, as the losses take logits."""
+    ok = z.dim() == 2 and (z.shape[1] <= 1 or z.stride(1) == 1) and (z.shape[0] <= 1 or z.stride(0) >= z.shape[1])
+    return z if ok else z.contiguous()
+
+
+class PreferenceLossFunction(torch.autograd.Function):
+    """autograd wrapper of the preference loss: apply(logits, labels,
+    seq_start, ref_logp, beta, label_smoothing, kind, average) returns (loss
+    [pairs], the sequences' log probabilities [2 pairs], which carry no
+    gradient). First order only; ref_logp is a constant."""
+
+    @staticmethod
+    def forward(ctx, logits, labels, seq_start, ref_logp, beta=0.1, label_smoothing=0.0, kind="sigmoid", average=False):
+        if ctx.needs_input_grad[3]:
+            _refuse(_lib.QL_ERR_UNSUPPORTED, "ref_logp requires a gradient")
+        loss, seq_logp, ctx.state = preference_loss_fwd(_rows(logits), labels, seq_start, ref_logp, beta,
+                                                        label_smoothing, kind, average)
+        ctx.save_for_backward(logits, labels)
+        ctx.tie = ()
+        ctx.mark_non_differentiable(seq_logp)
+        return loss, seq_logp
+
+    @staticmethod
+    @_first_order_only
+    def backward(ctx, dloss, _seq_logp=None):
+        logits, labels = ctx.saved_tensors
+        dz = preference_loss_bwd(_rows(logits), labels, ctx.state, dloss.contiguous().float())
+        return dz, None, None, None, None, None, None, None
+
+
+class DistillLossFunction(torch.autograd.Function):
+    """autograd wrapper of distillation: apply(logits, top_index, top_logits,
+    labels, temperature, alpha) returns the loss [T]. The backward reads the
+    logits once more (distill_loss with need_grad gives both in one pass where
+    the loss's gradient is known beforehand). First order only; the teacher is
+    a constant."""
+
+    @staticmethod
+    def forward(ctx, logits, top_index, top_logits, labels=None, temperature=1.0, alpha=0.0):
+        if ctx.needs_input_grad[2]:
+            _refuse(_lib.QL_ERR_UNSUPPORTED, "top_logits requires a gradient")
+        loss, _ = distill_loss(_rows(logits), top_index, top_logits, labels, temperature, alpha)
+        ctx.save_for_backward(logits, top_index, top_logits, labels)
+        ctx.tie = ()
+        ctx.how = (temperature, alpha)
+        return loss
+
+    @staticmethod
+    @_first_order_only
+    def backward(ctx, dloss):
+        logits, top_index, top_logits, labels = ctx.saved_tensors
+        _, dz = distill_loss(_rows(logits), top_index, top_logits, labels, *ctx.how, weight=dloss.contiguous().float(),
+                             need_loss=False, need_grad=True)
+        return dz, None, None, None, None, None
 
 
 class KernelTimer:

@@ -39,6 +39,18 @@ QL_KERNEL_ACT8_GRAD = 15
 QL_KERNEL_Q4G_QUANTIZE = 16
 QL_KERNEL_Q4G_DEQUANTIZE = 17
 QL_KERNEL_Q4G_LINEAR = 18
+QL_KERNEL_NORM = 19
+QL_KERNEL_LOGP = 20
+QL_KERNEL_PREFERENCE = 21
+QL_KERNEL_LOGP_GRAD = 22
+QL_KERNEL_DISTILL = 23
+QL_KERNEL_EPILOGUE = 24
+QL_NORM_MAX_COLS = 16384
+QL_PREF_SIGMOID = 0
+QL_PREF_HINGE = 1
+QL_PREF_SQUARED = 2
+QL_PREF_STATE_ROWS = 4
+QL_DISTILL_MAX_TOP = 256
 QL_ACT8_BLOCK = 32
 QL_OUT_DX = 1
 QL_OUT_DA = 2
@@ -138,6 +150,15 @@ SIGNATURES = {
     "q4g_quantize": (_I, [_P, _I, _I64, _I64, _I32, _P, _P, _I, _P, _P]),
     "q4g_dequantize": (_I, [_GP, _P, _I, _P]),
     "q4g_linear_fwd": (_I, [_GP, _P, _I64, _P, _P]),
+    "qlora_norm_fwd": (_I, [_P, _I, _I64, _I64, _P, _P, _I, _F, _I, _P, _P, _P, _P]),
+    "qlora_norm_bwd_workspace": (_SZ, [_I64, _I64]),
+    "qlora_norm_bwd": (_I, [_P, _I, _I64, _I64, _P, _I, _P, _P, _P, _P, _P, _P, _I, _P, _SZ, _P]),
+    "qlora_token_logp_workspace": (_SZ, [_I64, _I64, _I]),
+    "qlora_token_logp": (_I, [_P, _I, _I64, _I64, _I64, _P, _P, _P, _SZ, _P]),
+    "qlora_preference_loss_fwd": (_I, [_P, _I, _I64, _I64, _I64, _P, _P, _I64, _P, _F, _F, _I, _I, _P, _P, _P, _P, _P,
+                                       _SZ, _P]),
+    "qlora_preference_loss_bwd": (_I, [_P, _I, _I64, _I64, _I64, _P, _P, _P, _I64, _P, _P]),
+    "qlora_distill_loss": (_I, [_P, _I, _I64, _I64, _I64, _P, _P, _I, _I64, _P, _F, _F, _P, _P, _P, _P]),
     "qlora_paged_adamw_workspace": (_SZ, [_I64]),
     "qlora_paged_adamw": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _F, _F, _F, _F, _F, _P, _SZ, _P, _P]),
     "qlora_status_string": (ctypes.c_char_p, [_I]),

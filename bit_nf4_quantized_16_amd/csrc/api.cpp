@@ -36,6 +36,14 @@ int set_error(int code, const char* fmt, ...) {
     return code;
 }
 
+int check_ptr(const void* p, const char* name) {
+    if (p == nullptr) return set_error(QL_ERR_NULL, "%s is NULL", name);
+    if (!aligned16(p)) return set_error(QL_ERR_ALIGN, "%s is not 16-byte aligned", name);
+    return QL_OK;
+}
+
+void clear_error() { g_last_error[0] = '\0'; }
+
 int check_launch(const char* what) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return set_error(QL_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
@@ -88,12 +96,6 @@ struct Carver {
 };
 
 int rank_pad64(int r) { return r <= 0 ? 0 : (r + 63) / 64 * 64; }
-
-int check_ptr(const void* p, const char* name) {
-    if (p == nullptr) return set_error(QL_ERR_NULL, "%s is NULL", name);
-    if (!aligned16(p)) return set_error(QL_ERR_ALIGN, "%s is not 16-byte aligned", name);
-    return QL_OK;
-}
 
 int check_weight(const ql_nf4_weight* w) {
     if (w == nullptr) return set_error(QL_ERR_NULL, "weight descriptor is NULL");

@@ -9,6 +9,11 @@
 
 namespace qlnf4 {
 
+// The entry points' check of a device pointer: QL_OK, or the refusal with its
+// message set.
+int check_ptr(const void* p, const char* name);
+void clear_error();
+
 // Device view of a quantized weight (all pointers device memory).
 struct NF4Dev {
     const uint8_t* packed;
@@ -282,6 +287,99 @@ int launch_q4g_quantize(const void* W, bool w_f32, int64_t N, int64_t K, int gro
 int launch_q4g_dequantize(const Q4GDev& w, int64_t N, int64_t K, void* out, bool bf16_out, hipStream_t stream);
 int launch_q4g_linear(const Q4GDev& w, const uint16_t* X, int64_t T, int64_t N, int64_t K, uint16_t* Y,
                       hipStream_t stream);
+
+// Layer norm (rms 0) or root-mean-square norm over rows of C values.
+struct NormArgs {
+    const void* X;
+    int64_t T;
+    int C;  // a multiple of 8, at most QL_NORM_MAX_COLS
+    const void* w;
+    const void* b;  // null: none
+    int x_f32, w_f32, rms;
+    float eps;
+    void* Y;
+    float* mean;  // written by the forward (null: not kept), read by the backward
+    float* rstd;
+    const void* dY;
+    void* dX;   // null: not wanted
+    float* dW;  // null: not wanted
+    float* dB;
+    int accumulate;
+    float* part;  // norm_bwd_ws_bytes, for dW and dB
+};
+int launch_norm_fwd(const NormArgs& a, hipStream_t stream);
+size_t norm_bwd_ws_bytes(int64_t T, int64_t C);
+int launch_norm_bwd(const NormArgs& a, hipStream_t stream);
+
+// Log probabilities of labels: logp[t] = z[t][labels[t]] - lse(z[t]), 0 where
+// the label is outside [0, V). z [T, V] (row stride ld), bf16 or fp32.
+struct LogpArgs {
+    const void* z;
+    int f32;
+    int64_t T, ld;
+    int V;
+    const int64_t* labels;
+    float* logp;
+    // for the gradient, null without: softmax = 2^((z - ref) log2 e) inv; and
+    // dlogp, pair of rows in no sequence (zeros)
+    float* ref;
+    float* inv;
+    float* dlogp;
+    int* pair;
+    float* part;  // logp_ws_bytes
+    int slices;   // set by the launcher
+};
+size_t logp_ws_bytes(int64_t T, int64_t V, bool f32);
+int launch_logp(LogpArgs a, hipStream_t stream);
+
+struct PairArgs {
+    const int64_t* start;  // [2 pairs + 1]
+    const int64_t* labels;
+    const float* logp;
+    const float* ref;  // [2 pairs]
+    int64_t T;
+    int V;
+    float beta, smooth;
+    int kind, average;
+    float* loss;      // [pairs]
+    float* seq_logp;  // [2 pairs]
+    float* dlogp;     // [T]
+    int* pair;
+};
+int launch_pairs(const PairArgs& a, int pairs, hipStream_t stream);
+
+struct LogpGradArgs {
+    const void* z;
+    void* dz;  // rows as z's, the same offset from a 16-byte boundary; may be z
+    int f32;
+    int64_t T, ld;
+    int V;
+    const int64_t* labels;
+    const float* ref;
+    const float* inv;
+    const float* dlogp;
+    const int* pair;
+    const float* dloss;
+    int64_t pairs;
+    int slices;  // set by the launcher
+};
+int launch_logp_grad(LogpGradArgs a, hipStream_t stream);
+
+struct DistillArgs {
+    const void* z;
+    void* dz;  // null: the loss alone; else as LogpGradArgs'
+    int f32;
+    int64_t T, ld;
+    int V, K;
+    const int64_t* index;  // [T, K]
+    const void* top;       // [T, K]
+    int top_f32;
+    const int64_t* labels;  // null: every row counts (alpha = 0)
+    const float* weight;    // null: 1
+    float tau, alpha;
+    float* loss;  // null: not wanted
+};
+int launch_distill(const DistillArgs& a, hipStream_t stream);
 
 // AdamW step (fp32 state). paged: m and v are pinned host memory and pass
 // through ws (adamw_page_ws_bytes(n) bytes of device memory) in chunks,

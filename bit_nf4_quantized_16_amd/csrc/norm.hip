@@ -1,0 +1,293 @@
+// Layer norm and root-mean-square norm, forward and backward (gfx950).
+//
+//   mu = mean(x) (0 for the root-mean-square form), r = 1 / sqrt(mean((x - mu)^2) + eps)
+//   y = h w + b, h = (x - mu) r
+//   dx = r (g - mean(g) - h mean(g h)), g = dy w   (no mean(g) without a mean)
+//   dw = sum_t dy h, db = sum_t dy
+//
+// Both are bound by HBM: x is read once and kept in registers between the
+// statistics and the output, so the variance is summed from x - mu itself.
+#include "common.h"
+#include "internal.h"
+#include "reduce.h"
+
+namespace qlnf4 {
+
+namespace {
+
+// VEC values of type bf16 (F32 false) or fp32 from p.
+template <bool F32, int VEC>
+__device__ __forceinline__ void load_vec(const void* p, int64_t at, float (&v)[VEC]) {
+    if constexpr (F32) {
+#pragma unroll
+        for (int q = 0; q < VEC / 4; ++q) {
+            const float4 f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at)[q];
+            v[4 * q] = f.x, v[4 * q + 1] = f.y, v[4 * q + 2] = f.z, v[4 * q + 3] = f.w;
+        }
+    } else {
+        uint32_t w[VEC / 2];
+        if constexpr (VEC == 8) {
+            const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
+            w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+        } else {
+            const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at);
+            w[0] = u.x, w[1] = u.y;
+        }
+#pragma unroll
+        for (int q = 0; q < VEC / 2; ++q) {
+            v[2 * q] = __uint_as_float(w[q] << 16);
+            v[2 * q + 1] = __uint_as_float(w[q] & 0xFFFF0000u);
+        }
+    }
+}
+
+template <bool F32, int VEC>
+__device__ __forceinline__ void store_vec(void* p, int64_t at, const float (&v)[VEC]) {
+    if constexpr (F32) {
+        static_assert(VEC == 4, "16 bytes");
+        *reinterpret_cast<float4*>(static_cast<float*>(p) + at) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+        static_assert(VEC == 8, "16 bytes");
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) =
+            make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    }
+}
+
+// A row by `waves` waves (the workgroup's, or one of its four), a lane NV
+// pieces of 16 bytes of x.
+template <bool XF32, bool WF32, int NV>
+__global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs p, int waves) {
+    constexpr int VEC = XF32 ? 4 : 8;
+    __shared__ float red[2][16];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t row = waves == 1 ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 6) + wave : blockIdx.x;
+    if (row >= p.T) return;  // a whole wave, and only where no barrier follows
+    const int first = waves == 1 ? lane : threadIdx.x, step = 64 * waves;
+    const int C = p.C;
+    const int64_t base = row * C;
+
+    float x[NV][VEC];
+    float s[1] = {0.0f};
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int c = (first + j * step) * VEC;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) x[j][i] = 0.0f;
+        if (c < C) load_vec<XF32, VEC>(p.X, base + c, x[j]);
+    }
+    float mu = 0.0f;
+    const float inv = 1.0f / static_cast<float>(C);
+    if (!p.rms) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) s[0] += x[j][i];
+        block_reduce(s, red[0], wave, waves, AddOp{});
+        mu = s[0] * inv;
+    }
+    s[0] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const bool in = (first + j * step) * VEC < C;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            x[j][i] = in ? x[j][i] - mu : 0.0f;
+            s[0] = __builtin_fmaf(x[j][i], x[j][i], s[0]);
+        }
+    }
+    block_reduce(s, red[1], wave, waves, AddOp{});
+    const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(s[0], inv, p.eps));
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int c = (first + j * step) * VEC;
+        if (c >= C) continue;
+        float w[VEC], b[VEC], y[VEC];
+        load_vec<WF32, VEC>(p.w, c, w);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) b[i] = 0.0f;
+        if (p.b != nullptr) load_vec<WF32, VEC>(p.b, c, b);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) y[i] = __builtin_fmaf(x[j][i] * r, w[i], b[i]);
+        store_vec<XF32, VEC>(p.Y, base + c, y);
+    }
+    if (first == 0) {
+        if (p.mean != nullptr) p.mean[row] = mu;
+        if (p.rstd != nullptr) p.rstd[row] = r;
+    }
+}
+
+// A workgroup takes rows blockIdx, blockIdx + gridDim, ...; a thread keeps its
+// columns' sums of dy h and dy over them and leaves them in part.
+template <bool XF32, bool WF32, int NV, bool GRADS>
+__global__ __launch_bounds__(1024) void norm_bwd_kernel(NormArgs p) {
+    constexpr int VEC = XF32 ? 4 : 8;
+    __shared__ float red[2][32];
+    const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const int C = p.C, step = blockDim.x;
+    const float inv = 1.0f / static_cast<float>(C);
+    const bool rms = p.rms;
+    float sw[NV][VEC], sb[NV][VEC];
+    if constexpr (GRADS) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) sw[j][i] = sb[j][i] = 0.0f;
+    }
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x, turn ^= 1) {
+        const int64_t base = row * C;
+        const float r = p.rstd[row], mu = rms ? 0.0f : p.mean[row];
+        float h[NV][VEC], g[NV][VEC];
+        float s[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (threadIdx.x + j * step) * VEC;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) h[j][i] = g[j][i] = 0.0f;
+            if (c < C) {
+                load_vec<XF32, VEC>(p.X, base + c, h[j]);
+                load_vec<XF32, VEC>(p.dY, base + c, g[j]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (threadIdx.x + j * step) * VEC;
+            float w[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) w[i] = 0.0f;
+            if (c < C && p.dX != nullptr) load_vec<WF32, VEC>(p.w, c, w);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                h[j][i] = c < C ? (h[j][i] - mu) * r : 0.0f;
+                if constexpr (GRADS) {
+                    sw[j][i] = __builtin_fmaf(g[j][i], h[j][i], sw[j][i]);
+                    sb[j][i] += g[j][i];
+                }
+                g[j][i] *= w[i];
+                s[0] = __builtin_fmaf(g[j][i], h[j][i], s[0]);
+                s[1] += g[j][i];
+            }
+        }
+        if (p.dX == nullptr) continue;
+        block_reduce(s, red[turn], wave, waves, AddOp{}, AddOp{});
+        const float gh = s[0] * inv, gm = rms ? 0.0f : s[1] * inv;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (threadIdx.x + j * step) * VEC;
+            if (c >= C) continue;
+            float d[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) d[i] = r * (__builtin_fmaf(-gh, h[j][i], g[j][i]) - gm);
+            store_vec<XF32, VEC>(p.dX, base + c, d);
+        }
+    }
+    if constexpr (GRADS) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (threadIdx.x + j * step) * VEC;
+            if (c >= C) continue;
+            float* const o = p.part + static_cast<int64_t>(blockIdx.x) * C + c;
+            float* const ob = o + static_cast<int64_t>(gridDim.x) * C;
+#pragma unroll
+            for (int i = 0; i < VEC; i += 4) {
+                if (p.dW != nullptr)
+                    *reinterpret_cast<float4*>(o + i) = make_float4(sw[j][i], sw[j][i + 1], sw[j][i + 2], sw[j][i + 3]);
+                if (p.dB != nullptr)
+                    *reinterpret_cast<float4*>(ob + i) = make_float4(sb[j][i], sb[j][i + 1], sb[j][i + 2], sb[j][i + 3]);
+            }
+        }
+    }
+}
+
+// The workgroups' sums added in order: 16 columns a workgroup by 16 threads
+// each, y the array (dw, db).
+__global__ __launch_bounds__(256) void norm_grads_kernel(NormArgs p, int parts) {
+    __shared__ float red[16][17];
+    const int col = threadIdx.x & 15, k = threadIdx.x >> 4;
+    const int c = blockIdx.x * 16 + col;
+    float* const out = blockIdx.y == 0 ? p.dW : p.dB;
+    if (out == nullptr) return;
+    const float* const src = p.part + static_cast<int64_t>(blockIdx.y) * parts * p.C;
+    float s = 0.0f;
+    if (c < p.C) {
+#pragma unroll 8
+        for (int g = k; g < parts; g += 16) s += src[static_cast<int64_t>(g) * p.C + c];
+    }
+    red[k][col] = s;
+    __syncthreads();
+    if (threadIdx.x < 16 && c < p.C) {
+        float t = red[0][col];
+        for (int i = 1; i < 16; ++i) t += red[i][col];
+        out[c] = p.accumulate ? out[c] + t : t;
+    }
+}
+
+template <typename F>
+void norm_dispatch(const NormArgs& a, int nv, F f) {
+    auto by_nv = [&](auto xf, auto wf) {
+        switch (nv) {
+            case 1: f(xf, wf, std::integral_constant<int, 1>{}); break;
+            case 2: f(xf, wf, std::integral_constant<int, 2>{}); break;
+            default: f(xf, wf, std::integral_constant<int, 4>{}); break;
+        }
+    };
+    if (a.x_f32)
+        a.w_f32 ? by_nv(std::true_type{}, std::true_type{}) : by_nv(std::true_type{}, std::false_type{});
+    else
+        a.w_f32 ? by_nv(std::false_type{}, std::true_type{}) : by_nv(std::false_type{}, std::false_type{});
+}
+
+// Pieces of 16 bytes in a row; waves that take them, at most four pieces a lane.
+struct RowPlan {
+    int nv, waves;
+};
+RowPlan row_plan(int64_t C, bool f32, int want) {
+    const int pieces = static_cast<int>(ceil_div(C, f32 ? 4 : 8));
+    RowPlan r{1, 1};
+    for (r.nv = 1; r.nv < want && 64 * r.nv < pieces; r.nv *= 2) {}
+    while (r.waves < 16 && 64 * r.nv * r.waves < pieces) r.waves *= 2;
+    while (64 * r.nv * r.waves < pieces) r.nv *= 2;
+    return r;
+}
+
+int64_t norm_bwd_groups(int64_t T) { return std::min<int64_t>(T, 512); }
+
+}  // namespace
+
+int launch_norm_fwd(const NormArgs& a, hipStream_t stream) {
+    const RowPlan r = row_plan(a.C, a.x_f32, 2);
+    const int rows = r.waves == 1 ? 4 : 1;
+    timer_begin(QL_KERNEL_NORM, stream);
+    norm_dispatch(a, r.nv, [&](auto xf, auto wf, auto nv) {
+        hipLaunchKernelGGL((norm_fwd_kernel<decltype(xf)::value, decltype(wf)::value, decltype(nv)::value>),
+                           dim3(static_cast<uint32_t>(ceil_div(a.T, rows))), dim3(64 * r.waves * rows), 0, stream, a,
+                           r.waves);
+    });
+    timer_end(QL_KERNEL_NORM, stream);
+    return check_launch("norm forward");
+}
+
+size_t norm_bwd_ws_bytes(int64_t T, int64_t C) { return static_cast<size_t>(norm_bwd_groups(T)) * C * 2 * sizeof(float); }
+
+int launch_norm_bwd(const NormArgs& a, hipStream_t stream) {
+    const RowPlan r = row_plan(a.C, a.x_f32, 2);
+    const int64_t groups = norm_bwd_groups(a.T);
+    const bool grads = a.dW != nullptr || a.dB != nullptr;
+    timer_begin(QL_KERNEL_NORM, stream);
+    if (groups > 0) norm_dispatch(a, r.nv, [&](auto xf, auto wf, auto nv) {
+        const dim3 grid(static_cast<uint32_t>(groups)), block(64 * r.waves);
+        if (grads)
+            hipLaunchKernelGGL((norm_bwd_kernel<decltype(xf)::value, decltype(wf)::value, decltype(nv)::value, true>), grid,
+                               block, 0, stream, a);
+        else
+            hipLaunchKernelGGL((norm_bwd_kernel<decltype(xf)::value, decltype(wf)::value, decltype(nv)::value, false>),
+                               grid, block, 0, stream, a);
+    });
+    if (grads)
+        hipLaunchKernelGGL(norm_grads_kernel, dim3(static_cast<uint32_t>(ceil_div(a.C, 16)), 2), dim3(256), 0, stream, a,
+                           static_cast<int>(groups));
+    timer_end(QL_KERNEL_NORM, stream);
+    return check_launch("norm backward");
+}
+
+}  // namespace qlnf4

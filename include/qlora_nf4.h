@@ -679,6 +679,114 @@ int q4g_dequantize(const ql_q4g_weight* w, void* out, int out_dtype, void* strea
 int q4g_linear_fwd(const ql_q4g_weight* w, const uint16_t* X, int64_t T, uint16_t* Y, void* stream);
 
 /*
+ * qlora_norm_fwd / qlora_norm_bwd — layer norm and root-mean-square norm over
+ * the rows of an activation, and their backward:
+ *
+ *   mu = mean(x) (0 with rms), r = 1 / sqrt(mean((x - mu)^2) + eps)
+ *   h = (x - mu) r,  Y = h weight + bias
+ *   g = dY weight,   dX = r (g - mean(g) - h mean(g h))   (no mean(g) with rms)
+ *   dweight = sum over rows of dY h,  dbias = sum over rows of dY
+ *
+ *   X, Y, dY, dX  [rows, cols], x_dtype QL_BF16 or QL_F32; cols a multiple of
+ *          8, at most QL_NORM_MAX_COLS
+ *   weight, bias  [cols], w_dtype QL_BF16 or QL_F32; bias may be NULL
+ *   mean, rstd    [rows] fp32, out of the forward (each may be NULL) and in of
+ *          the backward; mean is 0 with rms. In the backward mean NULL is the
+ *          root-mean-square form
+ *   dX, dweight, dbias  out, each NULL to skip it; dweight, dbias [cols] fp32,
+ *          added to with accumulate 1
+ *   ws     qlora_norm_bwd_workspace(rows, cols) bytes where dweight or dbias is
+ *          wanted (else unused, may be NULL)
+ *
+ * Sums and statistics are fp32 (the variance from x - mu), outputs rounded
+ * once; the order of every sum is fixed. Y may be X and dX may be dY; nothing
+ * else may overlap. rows == 0: the forward is a no-op, the backward's sums are
+ * empty (zeros without accumulate).
+ * Errors: QL_ERR_NULL, QL_ERR_SHAPE (rows < 0 or 2^22 and more, cols), QL_ERR_UNSUPPORTED
+ * (dtypes, eps negative or not finite, rms or accumulate not 0 or 1), QL_ERR_ALIGN,
+ * QL_ERR_WORKSPACE, QL_ERR_HIP.
+ */
+#define QL_NORM_MAX_COLS 16384
+int qlora_norm_fwd(const void* X, int x_dtype, int64_t rows, int64_t cols, const void* weight, const void* bias,
+                   int w_dtype, float eps, int rms, void* Y, float* mean, float* rstd, void* stream);
+size_t qlora_norm_bwd_workspace(int64_t rows, int64_t cols);
+int qlora_norm_bwd(const void* X, int x_dtype, int64_t rows, int64_t cols, const void* weight, int w_dtype,
+                   const void* dY, const float* mean, const float* rstd, void* dX, float* dweight, float* dbias,
+                   int accumulate, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Losses on logits. z [T, V] is bf16 or fp32 (dtype), row t at logits + t ld
+ * values, ld >= V; a row starts at any value (no alignment but the type's), so
+ * slices of a padded vocabulary need no copy. labels [T] are int64 on the
+ * device; a row whose label is outside [0, V) (-100, say) is not counted: it is
+ * not read and its gradient is zero. Gradients have the logits' type, row
+ * stride and offset from a 16-byte boundary (QL_ERR_ALIGN otherwise) and may
+ * take the logits' place (dlogits == logits); what lies between the rows is
+ * left as it is. Sums are fp32, over the tokens of a sequence fp64; orders are
+ * fixed. Limits: T <= 2^22, V < 2^30, T V <= 2^35.
+ *
+ * qlora_token_logp — log probability of each row's label,
+ *   logp[t] = z[t][labels[t]] - log sum_j e^z[t][j]      (0 where not counted)
+ * ws: qlora_token_logp_workspace(T, V, dtype) bytes.
+ *
+ * qlora_preference_loss_fwd / _bwd — a loss on pairs of sequences. The rows of
+ * sequence s are seq_start[s] .. seq_start[s + 1] - 1 (int64 on the device,
+ * 2 pairs + 1 of them, not decreasing; values outside [0, T] are taken as the
+ * nearer end); sequence 2 i is pair i's preferred answer, 2 i + 1 the other.
+ * With L_s the sum of the sequence's counted logp (their mean with average 1;
+ * 0 without any) and ref_logp [2 pairs] the same under the reference model:
+ *
+ *   d = (L_2i - ref_2i) - (L_2i+1 - ref_2i+1),  x = beta d
+ *   QL_PREF_SIGMOID  loss = -(1 - e) log sigmoid(x) - e log sigmoid(-x), e = label_smoothing
+ *   QL_PREF_HINGE    loss = max(0, 1 - x)
+ *   QL_PREF_SQUARED  loss = (d - 1 / (2 beta))^2
+ *   dlogits[t][j] = dloss[i] (dloss_i / dlogp_t) (1[j = labels[t]] - softmax(z[t])_j)
+ *
+ *   loss, dloss  [pairs] fp32;  seq_logp  out [2 pairs] fp32, the L_s
+ *   state  out of the forward, QL_PREF_STATE_ROWS x T fp32, for the backward
+ *          on the same logits and labels; rows in no sequence get no gradient
+ *   ws     qlora_token_logp_workspace(T, V, dtype) bytes
+ * pairs = 0 or T = 0 are allowed.
+ *
+ * qlora_distill_loss — distillation from a teacher's top K logits (1 to
+ * QL_DISTILL_MAX_TOP of them a row), its loss and, with dlogits, its gradient in
+ * the one pass over the logits. top_index [T, K] int64 on the device, top_logits
+ * [T, K] bf16 or fp32 (top_dtype); entries whose index is outside [0, V) are
+ * absent. With p the softmax of the present top_logits / tau (over them) and
+ * q that of the row / tau:
+ *
+ *   loss[t] = (1 - a) tau^2 sum_k p_k (log p_k - log q_k) + a (lse(z[t]) - z[t][labels[t]])
+ *   dlogits[t][j] = weight[t] ((1 - a) tau (q_j - p_j) + a (softmax(z[t])_j - 1[j = labels[t]]))
+ *
+ * p_j the sum over the entries of index j; entries with p_k = 0 add nothing. A
+ * row without entries has no first term. labels may be NULL with a = 0 (every
+ * row counts). weight [T] fp32 (NULL: 1) scales the gradient alone. loss and
+ * dlogits may each be NULL.
+ *
+ * Errors: QL_ERR_NULL, QL_ERR_SHAPE, QL_ERR_UNSUPPORTED (dtypes; beta not
+ * positive and finite, label_smoothing outside [0, 1], kind, average; tau not
+ * positive and finite, a outside [0, 1]), QL_ERR_ALIGN, QL_ERR_WORKSPACE,
+ * QL_ERR_HIP.
+ */
+#define QL_PREF_SIGMOID 0
+#define QL_PREF_HINGE 1
+#define QL_PREF_SQUARED 2
+#define QL_PREF_STATE_ROWS 4
+#define QL_DISTILL_MAX_TOP 256
+size_t qlora_token_logp_workspace(int64_t T, int64_t V, int dtype);
+int qlora_token_logp(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld, const int64_t* labels,
+                     float* logp, void* ws, size_t ws_bytes, void* stream);
+int qlora_preference_loss_fwd(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld, const int64_t* labels,
+                              const int64_t* seq_start, int64_t pairs, const float* ref_logp, float beta,
+                              float label_smoothing, int kind, int average, float* loss, float* seq_logp, float* state,
+                              float* logp, void* ws, size_t ws_bytes, void* stream);
+int qlora_preference_loss_bwd(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld, const int64_t* labels,
+                              const float* state, const float* dloss, int64_t pairs, void* dlogits, void* stream);
+int qlora_distill_loss(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld, const int64_t* top_index,
+                       const void* top_logits, int top_dtype, int64_t K, const int64_t* labels, float tau, float a,
+                       const float* weight, float* loss, void* dlogits, void* stream);
+
+/*
  * qlora_paged_adamw — one AdamW step of the trained adapter parameters with
  * 32-bit optimizer state that lives in device memory or, paged out, in host
  * memory ([apxml], the paged-optimizer paragraph: optimizer state moves
@@ -760,7 +868,13 @@ const char* qlora_last_error(void);
 #define QL_KERNEL_Q4G_QUANTIZE 16
 #define QL_KERNEL_Q4G_DEQUANTIZE 17
 #define QL_KERNEL_Q4G_LINEAR 18
-#define QL_KERNEL_COUNT 19
+#define QL_KERNEL_NORM 19
+#define QL_KERNEL_LOGP 20
+#define QL_KERNEL_PREFERENCE 21
+#define QL_KERNEL_LOGP_GRAD 22
+#define QL_KERNEL_DISTILL 23
+#define QL_KERNEL_EPILOGUE 24
+#define QL_KERNEL_COUNT 25
 int qlora_timer_arm(int kernel_id);
 int qlora_timer_read(int kernel_id, int64_t* launches, double* total_ms);
 int qlora_timer_disarm(int kernel_id);

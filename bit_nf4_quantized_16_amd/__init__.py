@@ -42,6 +42,10 @@ __all__ = [
     "q4g_quantize",
     "q4g_dequantize",
     "q4g_linear_fwd",
+    "qlora_linear_fwd_epilogue",
+    "epilogue_bwd",
+    "q4g_linear_fwd_epilogue",
+    "QLoRALinearEpilogueFunction",
     "norm_fwd",
     "norm_bwd",
     "token_logp",
@@ -732,6 +736,100 @@ def q4g_linear_fwd(w, X, out=None):
     return out
 
 
+# ---- the linear layer with bias, activation and residual --------------------
+_ACTS = {"none": _lib.QL_ACT_NONE, "silu": _lib.QL_ACT_SILU, "gelu": _lib.QL_ACT_GELU,
+         "gelu_tanh": _lib.QL_ACT_GELU_TANH}
+
+
+def _act(act):
+    code = _ACTS.get(act)
+    if code is None:
+        _refuse(_lib.QL_ERR_UNSUPPORTED, "act %r (%s)" % (act, ", ".join(_ACTS)))
+    return code
+
+
+def _epilogue(bias, act, residual, Z, T, rows, device):
+    code = _act(act)
+    if bias is not None:
+        _tensor(bias, "bias", torch.bfloat16, (rows,), device)
+    if residual is not None:
+        _tensor(residual, "residual", torch.bfloat16, (T, rows), device)
+    return _lib.QlEpilogue(_addr(bias), code, _addr(residual), _addr(Z))
+
+
+def qlora_linear_fwd_epilogue(w, X, A=None, B=None, scale=1.0, bias=None, act="none", residual=None, save_u=True,
+                              save_z=False, keep=None, p=0.0, out=None):
+    """Y = act(z) + residual with z = X W'^T + scale (X A^T) B^T + bias: the
+    linear forward with its epilogue in the same launch. bias [N] and residual
+    [T, N] bf16, each optional; ``act`` "none", "silu", "gelu" or "gelu_tanh";
+    ``keep`` / ``p`` as qlora_linear_fwd. Returns (Y, U or None, Z or None): U
+    fp32 [T, r] and Z = z in bf16 [T, N] for the backward. ``out``: Y's tensor,
+    which may be the residual."""
+    T = _matrix(X, "X").shape[0]
+    dev = w.packed.device
+    _tensor(X, "X", torch.bfloat16, (T, w.cols), dev)
+    r = _adapters(A, B, w.rows, w.cols, dev)
+    new = out is None
+    Y = torch.empty(T, w.rows, dtype=torch.bfloat16, device=dev) if new else _tensor(out, "out", torch.bfloat16,
+                                                                                      (T, w.rows), dev)
+    U = torch.empty(T, r, dtype=torch.float32, device=dev) if save_u and r > 0 else None
+    Z = torch.empty(T, w.rows, dtype=torch.bfloat16, device=dev) if save_z else None
+    e = _epilogue(bias, act, residual, Z, T, w.rows, dev)
+    if keep is None:
+        need = lib.qlora_linear_fwd_workspace(w.rows, w.cols, max(T, 1), r)
+    else:
+        if not isinstance(keep, torch.Tensor) or keep.numel() != T * (w.cols // 8):
+            _refuse(_lib.QL_ERR_SHAPE, "keep is no tensor of %d x %d bytes" % (T, w.cols // 8))
+        _tensor(keep, "keep", torch.uint8, keep.shape, dev)
+        need = lib.qlora_linear_fwd_dropout_workspace(w.rows, w.cols, max(T, 1), r)
+    ws, wsb = _workspace(need, dev)
+    _launch(dev, lib.qlora_linear_fwd_epilogue, w.descriptor(), X.data_ptr(), T, _addr(A), _addr(B), r, float(scale),
+            _addr(keep), float(p), e, Y.data_ptr(), _addr(U), _addr(ws), wsb)
+    if not new:
+        increment_version(out)
+    return Y, U, Z
+
+
+def q4g_linear_fwd_epilogue(w, X, bias=None, act="none", residual=None, out=None):
+    """q4g_linear_fwd with an epilogue: act(X W'^T + bias) + residual (bf16
+    [T, rows]), arguments as qlora_linear_fwd_epilogue."""
+    if not isinstance(X, torch.Tensor) or X.dim() != 2:
+        _refuse(_lib.QL_ERR_SHAPE, "X is not 2-D")
+    d = w.descriptor()
+    T, dev = X.shape[0], w.packed.device
+    _tensor(X, "X", torch.bfloat16, (T, w.cols), dev)
+    e = _epilogue(bias, act, residual, None, T, w.rows, dev)
+    new = out is None
+    if new:
+        out = torch.empty(T, w.rows, dtype=torch.bfloat16, device=dev)
+    else:
+        _tensor(out, "out", torch.bfloat16, (T, w.rows), dev)
+    _launch(dev, lib.q4g_linear_fwd_epilogue, d, X.data_ptr(), T, e, out.data_ptr())
+    if not new:
+        increment_version(out)
+    return out
+
+
+def epilogue_bwd(dY, Z=None, act="none", need_dz=True, need_dbias=True, dbias=None, accumulate=False):
+    """Back through the epilogue: (dZ, dbias), dZ = dY act'(Z) bf16 for
+    qlora_linear_bwd and dbias fp32 [N] its sum over rows (None where not
+    wanted). Without an activation dZ is dY itself. The residual's gradient is
+    dY."""
+    rows, cols = _matrix(dY, "dY").shape
+    dev = dY.device
+    code = _act(act)
+    if code != _lib.QL_ACT_NONE:
+        _tensor(Z, "Z", torch.bfloat16, (rows, cols), dev)
+    dZ = None
+    if need_dz:
+        dZ = torch.empty_like(dY) if code != _lib.QL_ACT_NONE else dY
+    dbias = _grads(need_dbias, dbias, (cols,), "dbias", accumulate, dev)
+    ws, wsb = _workspace(lib.qlora_epilogue_bwd_workspace(rows, cols) if need_dbias else 0, dev)
+    _launch(dev, lib.qlora_epilogue_bwd, dY.data_ptr(), _addr(Z), rows, cols, code,
+            _addr(dZ) if code != _lib.QL_ACT_NONE else None, _addr(dbias), 1 if accumulate else 0, _addr(ws), wsb)
+    return dZ, dbias
+
+
 # ---- norms -----------------------------------------------------------------
 def _typed(t, name, shape, device=None):
     """t, checked like _tensor's, bf16 or fp32; and its QL_ dtype."""
@@ -1152,6 +1250,42 @@ class SwiGLUFunction(torch.autograd.Function):
         dg, du = swiglu_bwd(Act8(rows, cols, gc, gs), Act8(rows, cols, uc, us), dH.contiguous().to(torch.bfloat16))
         need = ctx.needs_input_grad
         return dg if need[0] else None, du if need[1] else None, None
+
+
+class QLoRALinearEpilogueFunction(torch.autograd.Function):
+    """autograd wrapper of the linear layer with an epilogue: apply(X, A, B, w,
+    scale, bias, act, residual, keep, p). X, A, B, bias and residual receive
+    gradients, those of A, B and bias fp32 sums cast to their type; w is
+    frozen. First order only."""
+
+    @staticmethod
+    def forward(ctx, X, A, B, w, scale, bias=None, act="none", residual=None, keep=None, p=0.0):
+        need = (*ctx.needs_input_grad, False, False, False)
+        c = lambda t: t.contiguous() if t is not None else None
+        Y, U, Z = qlora_linear_fwd_epilogue(w, X.contiguous(), c(A), c(B), scale, c(bias), act, c(residual),
+                                            save_u=need[2], save_z=act != "none" and (any(need[:3]) or need[5]),
+                                            keep=keep, p=p)
+        ctx.save_for_backward(X if need[1] else None, A, B, U, Z, keep)
+        ctx.tie = _tie(*[t for t in (X, bias, residual) if t is not None])
+        ctx.how = (w, scale, act, p, bias.dtype if bias is not None else None)
+        return Y
+
+    @staticmethod
+    @_first_order_only
+    def backward(ctx, dY):
+        X, A, B, U, Z, keep = ctx.saved_tensors
+        w, scale, act, p, bias_dtype = ctx.how
+        need = (*ctx.needs_input_grad, False, False, False)
+        dY = dY.contiguous().to(torch.bfloat16)
+        linear = any(need[:3])
+        dZ, db = (epilogue_bwd(dY, Z, act, need_dz=linear, need_dbias=need[5]) if linear or need[5] else (None, None))
+        dX = dA = dB = None
+        if linear:
+            c = lambda t: t.contiguous() if t is not None else None
+            dX, dA, dB = qlora_linear_bwd(w, c(X), dZ, c(A), c(B), scale, U=U, need_dx=need[0], need_da=need[1],
+                                          need_db=need[2], keep=keep, p=p)
+        return (dX, dA.to(A.dtype) if need[1] else None, dB.to(B.dtype) if need[2] else None, None, None,
+                db.to(bias_dtype) if need[5] else None, None, dY if need[7] else None, None, None)
 
 
 class NormFunction(torch.autograd.Function):

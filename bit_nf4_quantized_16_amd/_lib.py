@@ -45,6 +45,10 @@ QL_KERNEL_PREFERENCE = 21
 QL_KERNEL_LOGP_GRAD = 22
 QL_KERNEL_DISTILL = 23
 QL_KERNEL_EPILOGUE = 24
+QL_ACT_NONE = 0
+QL_ACT_SILU = 1
+QL_ACT_GELU = 2
+QL_ACT_GELU_TANH = 3
 QL_NORM_MAX_COLS = 16384
 QL_PREF_SIGMOID = 0
 QL_PREF_HINGE = 1
@@ -95,6 +99,15 @@ class QlQ4GWeight(ctypes.Structure):
     ]
 
 
+class QlEpilogue(ctypes.Structure):
+    _fields_ = [
+        ("bias", ctypes.c_void_p),
+        ("act", ctypes.c_int32),
+        ("residual", ctypes.c_void_p),
+        ("Z", ctypes.c_void_p),
+    ]
+
+
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
@@ -104,6 +117,7 @@ _F = ctypes.c_float
 _WP = ctypes.POINTER(QlNf4Weight)
 _AP = ctypes.POINTER(QlAct8)
 _GP = ctypes.POINTER(QlQ4GWeight)
+_EP = ctypes.POINTER(QlEpilogue)
 
 # name -> (restype, argtypes); the exported surface of include/qlora_nf4.h
 SIGNATURES = {
@@ -150,6 +164,10 @@ SIGNATURES = {
     "q4g_quantize": (_I, [_P, _I, _I64, _I64, _I32, _P, _P, _I, _P, _P]),
     "q4g_dequantize": (_I, [_GP, _P, _I, _P]),
     "q4g_linear_fwd": (_I, [_GP, _P, _I64, _P, _P]),
+    "qlora_linear_fwd_epilogue": (_I, [_WP, _P, _I64, _P, _P, _I32, _F, _P, _F, _EP, _P, _P, _P, _SZ, _P]),
+    "q4g_linear_fwd_epilogue": (_I, [_GP, _P, _I64, _EP, _P, _P]),
+    "qlora_epilogue_bwd_workspace": (_SZ, [_I64, _I64]),
+    "qlora_epilogue_bwd": (_I, [_P, _P, _I64, _I64, _I, _P, _P, _I, _P, _SZ, _P]),
     "qlora_norm_fwd": (_I, [_P, _I, _I64, _I64, _P, _P, _I, _F, _I, _P, _P, _P, _P]),
     "qlora_norm_bwd_workspace": (_SZ, [_I64, _I64]),
     "qlora_norm_bwd": (_I, [_P, _I, _I64, _I64, _P, _I, _P, _P, _P, _P, _P, _P, _I, _P, _SZ, _P]),

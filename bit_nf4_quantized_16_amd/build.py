@@ -23,7 +23,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libqlora_nf4.so")
 
-SOURCES = ["quantize.hip", "dequant.hip", "gemv.hip", "lora.hip", "gemm_tiles.hip", "merge.hip", "qerror.hip", "dropout.hip", "optim.hip", "act8.hip", "act8_grad.hip", "q4g.hip", "norm.hip", "loss.hip", "api.cpp", "api_train.cpp"]
+SOURCES = ["quantize.hip", "dequant.hip", "gemv.hip", "lora.hip", "gemm_tiles.hip", "merge.hip", "qerror.hip", "dropout.hip", "optim.hip", "act8.hip", "act8_grad.hip", "q4g.hip", "norm.hip", "epilogue.hip", "loss.hip", "api.cpp", "api_train.cpp"]
 ARCH = "gfx950"
 
 

@@ -429,15 +429,33 @@ int check_dropout(const uint8_t* keep, float p) {
     return QL_OK;
 }
 
+int check_epilogue(const ql_epilogue* e, int64_t T, Epilogue* out) {
+    if (e->act < QL_ACT_NONE || e->act > QL_ACT_GELU_TANH) return set_error(QL_ERR_UNSUPPORTED, "activation %d", e->act);
+    int s;
+    if (T > 0) {
+        if (e->bias != nullptr && (s = check_ptr(e->bias, "bias")) != QL_OK) return s;
+        if (e->residual != nullptr && (s = check_ptr(e->residual, "residual")) != QL_OK) return s;
+        if (e->Z != nullptr && (s = check_ptr(e->Z, "Z")) != QL_OK) return s;
+    }
+    *out = Epilogue{e->bias, e->residual, e->Z, e->act};
+    return QL_OK;
+}
+
 int linear_fwd(const ql_nf4_weight* w, const uint16_t* X, int64_t T, const uint16_t* A, const uint16_t* B, int32_t r,
                float scale, const uint8_t* keep, float p, uint16_t* Y, float* U_out, void* ws, size_t ws_bytes,
-               void* stream) {
+               void* stream, const ql_epilogue* epilogue = nullptr) {
     g_last_error[0] = '\0';
     int s;
     if ((s = check_weight(w)) != QL_OK) return s;
     if ((s = check_linear_shape(w, T, r)) != QL_OK) return s;
     const bool drop = keep != nullptr;
     if (drop && (s = check_dropout(keep, p)) != QL_OK) return s;
+    Epilogue epd{};
+    const Epilogue* ep = nullptr;
+    if (epilogue != nullptr) {
+        if ((s = check_epilogue(epilogue, T, &epd)) != QL_OK) return s;
+        ep = &epd;
+    }
     if (T == 0) return QL_OK;
     const int64_t N = w->rows, K = w->cols;
     if ((s = check_ptr(X, "X")) != QL_OK) return s;
@@ -457,8 +475,8 @@ int linear_fwd(const ql_nf4_weight* w, const uint16_t* X, int64_t T, const uint1
     hipStream_t st = static_cast<hipStream_t>(stream);
     const FwdWs f = carve_fwd(ws, N, K, T, r, drop);
     const NF4Dev wd = to_dev(w);
-    if (T <= kGemvMaxT && !drop) return launch_gemv(wd, X, T, N, K, A, B, r, scale, Y, U_out, f.gemv, st);
-    if (f.uword != nullptr) return launch_gemm_fwd_u(wd, X, A, B, r, scale, Y, U_out, T, N, K, f.uword, st);
+    if (T <= kGemvMaxT && !drop) return launch_gemv(wd, X, T, N, K, A, B, r, scale, Y, U_out, f.gemv, st, ep);
+    if (f.uword != nullptr) return launch_gemm_fwd_u(wd, X, A, B, r, scale, Y, U_out, T, N, K, f.uword, st, ep);
     const int rp = rank_pad64(r);
     const uint16_t* Bsrc = B;
     int64_t ld_b = r;
@@ -491,7 +509,7 @@ int linear_fwd(const ql_nf4_weight* w, const uint16_t* X, int64_t T, const uint1
             r_b = rp;
         }
     }
-    return launch_gemm_fwd(wd, X, f.Us, Bsrc, ld_b, r_b, rp, Y, T, N, K, f.split, st);
+    return launch_gemm_fwd(wd, X, f.Us, Bsrc, ld_b, r_b, rp, Y, T, N, K, f.split, st, ep);
 }
 
 // A grouped forward at T > 16 takes one GEMM launch over all layers' row
@@ -896,6 +914,20 @@ int qlora_linear_fwd_group(const ql_nf4_weight* const* w, int32_t nw, const uint
     return linear_fwd_group(w, nw, X, T, A, B, r, scale, Y, U_out, ws, ws_bytes, stream);
 }
 
+int qlora_linear_fwd_epilogue(const ql_nf4_weight* w, const uint16_t* X, int64_t T, const uint16_t* A, const uint16_t* B,
+                              int32_t r, float scale, const uint8_t* keep, float p, const ql_epilogue* e, uint16_t* Y,
+                              float* U_out, void* ws, size_t ws_bytes, void* stream) {
+    if (e == nullptr) {
+        g_last_error[0] = '\0';
+        return set_error(QL_ERR_NULL, "epilogue is NULL");
+    }
+    if (keep == nullptr && p != 0.0f) {
+        g_last_error[0] = '\0';
+        return set_error(QL_ERR_UNSUPPORTED, "dropout p = %g without a mask", (double)p);
+    }
+    return linear_fwd(w, X, T, A, B, r, scale, keep, p, Y, U_out, ws, ws_bytes, stream, e);
+}
+
 int qlora_linear_fwd_dropout(const ql_nf4_weight* w, const uint16_t* X, int64_t T, const uint16_t* A,
                              const uint16_t* B, int32_t r, float scale, const uint8_t* keep, float p, uint16_t* Y,
                              float* U_out, void* ws, size_t ws_bytes, void* stream) {
@@ -1298,15 +1330,34 @@ int q4g_dequantize(const ql_q4g_weight* w, void* out, int out_dtype, void* strea
                                  static_cast<hipStream_t>(stream));
 }
 
-int q4g_linear_fwd(const ql_q4g_weight* w, const uint16_t* X, int64_t T, uint16_t* Y, void* stream) {
+static int q4g_linear(const ql_q4g_weight* w, const uint16_t* X, int64_t T, const ql_epilogue* e, uint16_t* Y, void* stream) {
     g_last_error[0] = '\0';
     int s;
     if ((s = check_q4g(w)) != QL_OK) return s;
     if (T < 0 || T > (int64_t{1} << 21)) return set_error(QL_ERR_SHAPE, "T = %lld", (long long)T);
+    Epilogue ep{};
+    if (e != nullptr) {
+        if (e->Z != nullptr) return set_error(QL_ERR_UNSUPPORTED, "Z is not kept by a 4-bit group linear");
+        if ((s = check_epilogue(e, T, &ep)) != QL_OK) return s;
+    }
     if (T == 0) return QL_OK;
     if ((s = check_ptr(X, "X")) != QL_OK) return s;
     if ((s = check_ptr(Y, "Y")) != QL_OK) return s;
-    return launch_q4g_linear(q4g_dev(w), X, T, w->rows, w->cols, Y, static_cast<hipStream_t>(stream));
+    return launch_q4g_linear(q4g_dev(w), X, T, w->rows, w->cols, Y, static_cast<hipStream_t>(stream),
+                             e != nullptr ? &ep : nullptr);
+}
+
+int q4g_linear_fwd(const ql_q4g_weight* w, const uint16_t* X, int64_t T, uint16_t* Y, void* stream) {
+    return q4g_linear(w, X, T, nullptr, Y, stream);
+}
+
+int q4g_linear_fwd_epilogue(const ql_q4g_weight* w, const uint16_t* X, int64_t T, const ql_epilogue* e, uint16_t* Y,
+                            void* stream) {
+    if (e == nullptr) {
+        g_last_error[0] = '\0';
+        return set_error(QL_ERR_NULL, "epilogue is NULL");
+    }
+    return q4g_linear(w, X, T, e, Y, stream);
 }
 
 }  // extern "C"

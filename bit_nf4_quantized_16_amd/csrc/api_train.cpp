@@ -1,5 +1,5 @@
-// C ABI of the operators around the linear layer in a training step: norms and
-// the losses on logits. Validation before any launch, as in api.cpp. No C++
+// C ABI of the operators around the linear layer in a training step: norms, the
+// backward of its epilogue, and the losses on logits. Validation before any launch, as in api.cpp. No C++
 // exception crosses this file's extern "C" functions.
 #include <hip/hip_runtime.h>
 
@@ -45,6 +45,15 @@ int check_norm(int64_t rows, int64_t cols, int x_dtype, int w_dtype) {
     int s;
     if ((s = check_dtype(x_dtype, "activation")) != QL_OK) return s;
     return check_dtype(w_dtype, "weight");
+}
+
+int check_epilogue_shape(int64_t rows, int64_t cols) {
+    if (rows < 0 || rows > (int64_t{1} << 31)) return set_error(QL_ERR_SHAPE, "rows = %lld", (long long)rows);
+    if (cols <= 0 || cols % 8 != 0 || cols > (int64_t{1} << 31))
+        return set_error(QL_ERR_SHAPE, "cols = %lld (a multiple of 8)", (long long)cols);
+    if (rows > 0 && cols > (int64_t{1} << 40) / rows)
+        return set_error(QL_ERR_SHAPE, "%lld x %lld", (long long)rows, (long long)cols);
+    return QL_OK;
 }
 
 int check_logits_shape(int64_t T, int64_t V, int64_t ld, int dtype) {
@@ -147,6 +156,39 @@ int qlora_norm_bwd(const void* X, int x_dtype, int64_t rows, int64_t cols, const
     a.accumulate = accumulate;
     a.part = static_cast<float*>(ws);
     return launch_norm_bwd(a, static_cast<hipStream_t>(stream));
+}
+
+size_t qlora_epilogue_bwd_workspace(int64_t rows, int64_t cols) {
+    if (check_epilogue_shape(rows, cols) != QL_OK) return 0;
+    return epilogue_bwd_ws_bytes(rows, cols);
+}
+
+int qlora_epilogue_bwd(const uint16_t* dY, const uint16_t* Z, int64_t rows, int64_t cols, int act, uint16_t* dZ,
+                       float* dbias, int accumulate, void* ws, size_t ws_bytes, void* stream) {
+    clear_error();
+    int s;
+    if ((s = check_epilogue_shape(rows, cols)) != QL_OK) return s;
+    if (act < QL_ACT_NONE || act > QL_ACT_GELU_TANH) return set_error(QL_ERR_UNSUPPORTED, "activation %d", act);
+    if ((s = check_flag(accumulate, "accumulate")) != QL_OK) return s;
+    if (dbias == nullptr && (dZ == nullptr || rows == 0)) return QL_OK;
+    if (dbias != nullptr && (s = check_ptr(dbias, "dbias")) != QL_OK) return s;
+    if (rows > 0) {
+        if ((s = check_ptr(dY, "dY")) != QL_OK) return s;
+        if (act != QL_ACT_NONE && (s = check_ptr(Z, "Z")) != QL_OK) return s;
+        if (dZ != nullptr && (s = check_ptr(dZ, "dZ")) != QL_OK) return s;
+        if (dbias != nullptr && (s = check_ws(ws, ws_bytes, epilogue_bwd_ws_bytes(rows, cols))) != QL_OK) return s;
+    }
+    EpilogueBwdArgs a{};
+    a.dY = dY;
+    a.Z = Z;
+    a.T = rows;
+    a.N = cols;
+    a.act = act;
+    a.dZ = dZ;
+    a.dB = dbias;
+    a.accumulate = accumulate;
+    a.part = static_cast<float*>(ws);
+    return launch_epilogue_bwd(a, static_cast<hipStream_t>(stream));
 }
 
 size_t qlora_token_logp_workspace(int64_t T, int64_t V, int dtype) {

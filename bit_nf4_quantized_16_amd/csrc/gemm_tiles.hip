@@ -94,6 +94,7 @@ struct TileArgs {
     // keep bits [T, K / 8] and c = 1 / (1 - p).
     const uint8_t* keep;
     float c;
+    Epilogue ep;  // the EPI kernels (one forward)
 };
 
 typedef short v4i16 __attribute__((ext_vector_type(4)));
@@ -164,9 +165,10 @@ struct Codes {
     BlockConst bc;
 };
 
-template <int TA, int TT, int WA, int WT, bool DX, bool DQ, bool GRP, bool KEEP = false>
+template <int TA, int TT, int WA, int WT, bool DX, bool DQ, bool GRP, bool KEEP = false, bool EPI = false>
 __global__ __launch_bounds__(64 * WA * WT, 512 / (64 * WA * WT)) void tile_gemm_kernel(TileArgs p) {
     static_assert(!KEEP || (DX && !GRP), "a keep mask is the one-layer dX's");
+    static_assert(!EPI || (!DX && !GRP), "bias, activation and residual are the one-layer forward's");
     using S = TileShape<TA, TT, WA, WT, DX>;
     constexpr int SA = S::SA, ST = S::ST, CPT = S::CPT, CC = S::CC, LDA = S::LDA, TPR = S::TPR;
     constexpr int MW = S::MW, TW = S::TW, NW = S::NW, NTHR = S::NTHR;
@@ -772,31 +774,93 @@ __global__ __launch_bounds__(64 * WA * WT, 512 / (64 * WA * WT)) void tile_gemm_
         uint16_t* const base = g == 0 ? sA0 : g == 1 ? sA1 : g == 2 ? sX0 : sX1;
         return reinterpret_cast<char*>(base) + (t % RPA) * (TA * 2);
     };
+    // the tile's pieces c of rows t, 16 bytes of a global row a thread and turn
+    auto pieces = [&](auto f) {
+#pragma unroll
+        for (int i = 0; i < TT * CPR / NTHR; ++i) {
+            const int q = i * NTHR + tid;
+            const int t = q / CPR, c = q % CPR;
+            const int64_t gt = t0 + t, gm = m0 + 8 * c;
+            if (gt >= p.T || gm >= MA) continue;  // MA is a multiple of 8: a chunk is whole or outside
+            f(reinterpret_cast<uint4*>(out_row(t) + (c ^ (t % RPA % CPR)) * 16), gt * MA + gm);
+        }
+    };
+    // f(a, b, qq, where these four values of the tile are staged)
+    auto quads = [&](auto f) {
+#pragma unroll
+        for (int a = 0; a < SA; ++a)
+#pragma unroll
+            for (int b = 0; b < ST; ++b)
+#pragma unroll
+                for (int qq = 0; qq < 4; ++qq) {
+                    const int m = wa * MW + a * 32 + 8 * qq + 4 * (lane >> 5);
+                    const int t = wt * TW + b * 32 + (lane & 31);
+                    const int c = (m / 8) ^ (t % RPA % CPR);
+                    f(a, b, qq, reinterpret_cast<uint2*>(out_row(t) + c * 16 + (m % 8) * 2));
+                }
+    };
     __syncthreads();  // every wave is done reading the stages
+    if constexpr (EPI) {
+        // Bias in the accumulators; z through the stages where it is kept; the
+        // residual into the stages as it comes (whole pieces), from where each
+        // lane takes its values and puts the sums in their place: everything
+        // is fp32 until the one rounding.
+        if (p.ep.bias != nullptr) {
 #pragma unroll
-    for (int a = 0; a < SA; ++a)
+            for (int a = 0; a < SA; ++a)
 #pragma unroll
-        for (int b = 0; b < ST; ++b)
+                for (int qq = 0; qq < 4; ++qq) {
+                    const int64_t m = std::min<int64_t>(m0 + wa * MW + a * 32 + 8 * qq + 4 * (lane >> 5), MA - 4);
+                    const uint2 bv = *reinterpret_cast<const uint2*>(p.ep.bias + m);
+                    const float bf[4] = {__uint_as_float(bv.x << 16), __uint_as_float(bv.x & 0xFFFF0000u),
+                                         __uint_as_float(bv.y << 16), __uint_as_float(bv.y & 0xFFFF0000u)};
 #pragma unroll
-            for (int qq = 0; qq < 4; ++qq) {
-                const int m = wa * MW + a * 32 + 8 * qq + 4 * (lane >> 5);
-                const int t = wt * TW + b * 32 + (lane & 31);
-                uint2 v;
-                v.x = pack_bf16x2(acc[a][b][4 * qq], acc[a][b][4 * qq + 1]);
-                v.y = pack_bf16x2(acc[a][b][4 * qq + 2], acc[a][b][4 * qq + 3]);
-                const int c = (m / 8) ^ (t % RPA % CPR);
-                *reinterpret_cast<uint2*>(out_row(t) + c * 16 + (m % 8) * 2) = v;
-            }
-    __syncthreads();
+                    for (int b = 0; b < ST; ++b)
 #pragma unroll
-    for (int i = 0; i < TT * CPR / NTHR; ++i) {
-        const int q = i * NTHR + tid;
-        const int t = q / CPR, c = q % CPR;
-        const int64_t gt = t0 + t, gm = m0 + 8 * c;
-        if (gt >= p.T || gm >= MA) continue;  // MA is a multiple of 8: a chunk is whole or outside
-        const uint4 v = *reinterpret_cast<const uint4*>(out_row(t) + (c ^ (t % RPA % CPR)) * 16);
-        *reinterpret_cast<uint4*>((kGfwd ? p.gl[fl].out : p.out) + gt * MA + gm) = v;
+                        for (int i = 0; i < 4; ++i) acc[a][b][4 * qq + i] += bf[i];
+                }
+        }
+        if (p.ep.z != nullptr) {
+            quads([&](int a, int b, int qq, uint2* at) {
+                *at = make_uint2(pack_bf16x2(acc[a][b][4 * qq], acc[a][b][4 * qq + 1]),
+                                 pack_bf16x2(acc[a][b][4 * qq + 2], acc[a][b][4 * qq + 3]));
+            });
+            __syncthreads();
+            pieces([&](const uint4* at, int64_t g) { *reinterpret_cast<uint4*>(p.ep.z + g) = *at; });
+            __syncthreads();
+        }
+        const bool res = p.ep.res != nullptr;
+        if (res) {
+            pieces([&](uint4* at, int64_t g) { *at = *reinterpret_cast<const uint4*>(p.ep.res + g); });
+            __syncthreads();
+        }
+        with_act(p.ep.act, [&](auto act) {
+            quads([&](int a, int b, int qq, uint2* at) {
+                float y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[i] = act_value<decltype(act)::value>(acc[a][b][4 * qq + i]);
+                if (res) {
+                    const uint2 v = *at;
+                    y[0] += __uint_as_float(v.x << 16);
+                    y[1] += __uint_as_float(v.x & 0xFFFF0000u);
+                    y[2] += __uint_as_float(v.y << 16);
+                    y[3] += __uint_as_float(v.y & 0xFFFF0000u);
+                }
+                *at = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+            });
+        });
+    } else {
+        quads([&](int a, int b, int qq, uint2* at) {
+            uint2 v;
+            v.x = pack_bf16x2(acc[a][b][4 * qq], acc[a][b][4 * qq + 1]);
+            v.y = pack_bf16x2(acc[a][b][4 * qq + 2], acc[a][b][4 * qq + 3]);
+            *at = v;
+        });
     }
+    __syncthreads();
+    pieces([&](const uint4* at, int64_t g) {
+        *reinterpret_cast<uint4*>((kGfwd ? p.gl[fl].out : p.out) + g) = *at;
+    });
 }
 
 namespace {
@@ -829,6 +893,43 @@ __global__ void split_reduce_kernel(const float* __restrict__ part, int splits, 
     o.x = pack_bf16x2(s.x, s.y);
     o.y = pack_bf16x2(s.z, s.w);
     reinterpret_cast<uint2*>(out)[i] = o;
+}
+
+// The same with an epilogue: rows of a quarter of MA values, `blocks`
+// workgroups each.
+__global__ void split_reduce_epilogue_kernel(const float* __restrict__ part, int splits, int64_t T, int64_t MA,
+                                             uint32_t blocks, Epilogue ep, uint16_t* out) {
+    const uint32_t t = blockIdx.x / blocks;
+    const int64_t m = 4 * (static_cast<int64_t>(blockIdx.x - t * blocks) * 256 + threadIdx.x);
+    if (m >= MA) return;
+    const int64_t at = t * MA + m, n = T * MA;
+    float4 s = *reinterpret_cast<const float4*>(part + at);
+    for (int k = 1; k < splits; ++k) {
+        const float4 v = *reinterpret_cast<const float4*>(part + k * n + at);
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
+    }
+    float y[4] = {s.x, s.y, s.z, s.w};
+    auto add = [&](const uint16_t* p) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        y[0] += __uint_as_float(v.x << 16);
+        y[1] += __uint_as_float(v.x & 0xFFFF0000u);
+        y[2] += __uint_as_float(v.y << 16);
+        y[3] += __uint_as_float(v.y & 0xFFFF0000u);
+    };
+    auto put = [&](uint16_t* p) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+    };
+    if (ep.bias != nullptr) add(ep.bias + m);
+    if (ep.z != nullptr) put(ep.z + at);
+    with_act(ep.act, [&](auto act) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = act_value<decltype(act)::value>(y[i]);
+    });
+    if (ep.res != nullptr) add(ep.res + at);
+    put(out + at);
 }
 
 // A grouped forward's reduce pass: the summed partials of column chunk m of
@@ -865,7 +966,7 @@ __global__ void split_reduce_group_kernel(const float* __restrict__ part, int sp
 // GRP: a grouped dX (a.ng layers, a.gstep set) or forward (a.gtile, a.gcol
 // set, a.N the row tiles' total rows, the 256 tile only); a.w only gives
 // the format.
-template <bool DX, bool GRP = false, bool KEEP = false>
+template <bool DX, bool GRP = false, bool KEEP = false, bool EPI = false>
 int launch_tiles(TileArgs& a, float* split_ws, int kid, const char* what, hipStream_t stream, int nu = 0) {
     const int64_t MA = DX ? a.K : a.N;
     const GemmPlan pl = plan_gemm(MA, a.T, (GRP && DX) ? int64_t{kStep} * a.gstep[a.ng] : (DX ? a.N : a.K));
@@ -884,14 +985,14 @@ int launch_tiles(TileArgs& a, float* split_ws, int kid, const char* what, hipStr
     timer_begin(kid, stream);
     if (tile == 256) {
         if (a.w.dq)
-            hipLaunchKernelGGL((tile_gemm_kernel<256, 256, 4, 2, DX, true, GRP, KEEP>), grid, dim3(512), 0, stream, a);
+            hipLaunchKernelGGL((tile_gemm_kernel<256, 256, 4, 2, DX, true, GRP, KEEP, EPI>), grid, dim3(512), 0, stream, a);
         else
-            hipLaunchKernelGGL((tile_gemm_kernel<256, 256, 4, 2, DX, false, GRP, KEEP>), grid, dim3(512), 0, stream, a);
+            hipLaunchKernelGGL((tile_gemm_kernel<256, 256, 4, 2, DX, false, GRP, KEEP, EPI>), grid, dim3(512), 0, stream, a);
     } else {
         if (a.w.dq)
-            hipLaunchKernelGGL((tile_gemm_kernel<128, 128, 2, 2, DX, true, GRP, KEEP>), grid, dim3(256), 0, stream, a);
+            hipLaunchKernelGGL((tile_gemm_kernel<128, 128, 2, 2, DX, true, GRP, KEEP, EPI>), grid, dim3(256), 0, stream, a);
         else
-            hipLaunchKernelGGL((tile_gemm_kernel<128, 128, 2, 2, DX, false, GRP, KEEP>), grid, dim3(256), 0, stream, a);
+            hipLaunchKernelGGL((tile_gemm_kernel<128, 128, 2, 2, DX, false, GRP, KEEP, EPI>), grid, dim3(256), 0, stream, a);
     }
     if (a.splits > 1 && GRP && !DX) {
         GroupOut g{};
@@ -901,6 +1002,10 @@ int launch_tiles(TileArgs& a, float* split_ws, int kid, const char* what, hipStr
         const int64_t n4 = a.T * a.gcol[a.ng] / 4;
         hipLaunchKernelGGL(split_reduce_group_kernel, dim3(static_cast<uint32_t>(ceil_div(n4, 256))), dim3(256), 0,
                            stream, split_ws, a.splits, a.T, g);
+    } else if (a.splits > 1 && EPI) {
+        const int64_t blocks = ceil_div(MA / 4, 256);
+        hipLaunchKernelGGL(split_reduce_epilogue_kernel, dim3(static_cast<uint32_t>(a.T * blocks)), dim3(256), 0, stream,
+                           split_ws, a.splits, a.T, MA, static_cast<uint32_t>(blocks), a.ep, a.out);
     } else if (a.splits > 1) {
         const int64_t n4 = a.T * MA / 4;
         hipLaunchKernelGGL(split_reduce_kernel, dim3(static_cast<uint32_t>(ceil_div(n4, 256))), dim3(256), 0, stream,
@@ -949,7 +1054,8 @@ size_t gemm_split_bytes(int64_t MA, int64_t T, int64_t RED) {
 }
 
 int launch_gemm_fwd(const NF4Dev& w, const uint16_t* X, const uint16_t* Us, const uint16_t* Bsrc, int64_t ld_b,
-                    int r_b, int rp, uint16_t* Y, int64_t T, int64_t N, int64_t K, float* split_ws, hipStream_t stream) {
+                    int r_b, int rp, uint16_t* Y, int64_t T, int64_t N, int64_t K, float* split_ws, hipStream_t stream,
+                    const Epilogue* ep) {
     TileArgs a{};
     a.w = w;
     a.act = X;
@@ -963,7 +1069,10 @@ int launch_gemm_fwd(const NF4Dev& w, const uint16_t* X, const uint16_t* Us, cons
     a.T = T;
     a.N = N;
     a.K = K;
-    return launch_tiles<false>(a, split_ws, QL_KERNEL_GEMM_FWD, "dequant GEMM forward", stream);
+    if (ep == nullptr) return launch_tiles<false>(a, split_ws, QL_KERNEL_GEMM_FWD, "dequant GEMM forward", stream);
+    a.ep = *ep;
+    return launch_tiles<false, false, false, true>(a, split_ws, QL_KERNEL_GEMM_FWD, "dequant GEMM forward with an epilogue",
+                                                   stream);
 }
 
 bool gemm_fwd_u_in_launch(int64_t N, int64_t K, int64_t T, int r) {
@@ -1020,7 +1129,8 @@ int launch_gemm_dx_g(const NF4Dev& w, const uint16_t* dY, const uint16_t* A, int
 size_t gemm_fwd_u_words(int64_t T, int r) { return static_cast<size_t>(T) * r + 1; }  // + the epoch word
 
 int launch_gemm_fwd_u(const NF4Dev& w, const uint16_t* X, const uint16_t* A, const uint16_t* B, int r, float scale,
-                      uint16_t* Y, float* U_out, int64_t T, int64_t N, int64_t K, uint64_t* words, hipStream_t stream) {
+                      uint16_t* Y, float* U_out, int64_t T, int64_t N, int64_t K, uint64_t* words, hipStream_t stream,
+                      const Epilogue* ep) {
     TileArgs a{};
     a.w = w;
     a.act = X;
@@ -1068,8 +1178,12 @@ int launch_gemm_fwd_u(const NF4Dev& w, const uint16_t* X, const uint16_t* A, con
     // itself (a negative n: at once, without reading the words)
     const char* e = std::getenv("QLORA_NF4_GEMM_SPIN");
     a.spin = e ? std::atoi(e) : (1 << 14);
-    return launch_tiles<false>(a, nullptr, QL_KERNEL_GEMM_FWD, "dequant GEMM forward", stream,
-                               static_cast<int>(ceil_div(T, 16)));
+    const int nu = static_cast<int>(ceil_div(T, 16));
+    if (ep == nullptr)
+        return launch_tiles<false>(a, nullptr, QL_KERNEL_GEMM_FWD, "dequant GEMM forward", stream, nu);
+    a.ep = *ep;
+    return launch_tiles<false, false, false, true>(a, nullptr, QL_KERNEL_GEMM_FWD, "dequant GEMM forward with an epilogue",
+                                                   stream, nu);
 }
 
 int launch_gemm_dx(const NF4Dev& w, const uint16_t* dY, const uint16_t* Gp, const uint16_t* A, int r, int rp,

@@ -107,6 +107,7 @@ struct GemvArgs {
     int ngroup;       // weights in this launch
     int nu_all;       // U workgroups of all weights (they come first in the grid)
     GemvWeight g[kGemvGroup];
+    Epilogue ep;      // the EPI kernels, one weight
 };
 
 // Steps whose loads one wave keeps in flight, by TX = 16-byte x loads per
@@ -144,7 +145,8 @@ constexpr int gemv_min_waves() {
 
 // NS > 0: every wave has NS steps, or NS - 1 (all issued up front);
 // NS == 0: a ring of gemv_ring_depth<TX>() steps, refilled as they are used.
-template <int TX, int NS>
+// EPI: act(sum + bias) + residual in place of the sum.
+template <int TX, int NS, bool EPI>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(gemv_min_waves<TX, NS>()))) void gemv_kernel(
     GemvArgs p) {
     constexpr int D = NS > 0 ? NS : gemv_ring_depth<TX>();
@@ -273,6 +275,13 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(gemv_min_wa
         const int64_t last = N * r - 1;
 #pragma unroll
         for (int q = 0; q < kBQ; ++q) bpre[q] = gw.B[std::min<int64_t>(n0 * r + std::min(tid + 512 * q, nb - 1), last)];
+    }
+    // this thread's output's bias and residual, on their way meanwhile
+    uint32_t ebias = 0, eres = 0;
+    if constexpr (EPI) {
+        const int64_t n = std::min<int64_t>(n0 + ((tid >> 4) & 15), N - 1);
+        if (p.ep.bias != nullptr) ebias = p.ep.bias[n];
+        if (p.ep.res != nullptr) eres = p.ep.res[std::min(tid & 15, T - 1) * N + n];
     }
 
     auto issue = [&](GemvStage<TX>& st, int k) {
@@ -434,6 +443,12 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(gemv_min_wa
                 for (int j = 0; j < r; ++j) lora = __builtin_fmaf(sU[ot * r + j], bf16_to_f32(sB[ol * r + j]), lora);
                 sum += p.scale * lora;
             }
+            if constexpr (EPI) {
+                sum += bf16_to_f32(ebias);
+                if (p.ep.z != nullptr) p.ep.z[ot * N + n] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(sum));
+                with_act(p.ep.act, [&](auto act) { sum = act_value<decltype(act)::value>(sum); });
+                if (p.ep.res != nullptr) sum += bf16_to_f32(eres);
+            }
             gw.Y[ot * N + n] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(sum));
         }
     }
@@ -465,33 +480,33 @@ size_t gemv_ws_bytes(int64_t T, int64_t K, int r) {
 
 namespace {
 
-template <int TX>
+template <int TX, bool EPI>
 void launch_gemv_tx(int ns, dim3 grid, const GemvArgs& g, hipStream_t stream) {
     const dim3 block(64 * kGemvWaves);
     constexpr int M = gemv_max_steps<TX>();
     switch (ns > M ? 0 : ns) {
-        case 1: hipLaunchKernelGGL((gemv_kernel<TX, 1>), grid, block, 0, stream, g); break;
-        case 2: hipLaunchKernelGGL((gemv_kernel<TX, 2>), grid, block, 0, stream, g); break;
+        case 1: hipLaunchKernelGGL((gemv_kernel<TX, 1, EPI>), grid, block, 0, stream, g); break;
+        case 2: hipLaunchKernelGGL((gemv_kernel<TX, 2, EPI>), grid, block, 0, stream, g); break;
         case 3:
-            if constexpr (M >= 3) hipLaunchKernelGGL((gemv_kernel<TX, 3>), grid, block, 0, stream, g);
+            if constexpr (M >= 3) hipLaunchKernelGGL((gemv_kernel<TX, 3, EPI>), grid, block, 0, stream, g);
             break;
         case 4:
-            if constexpr (M >= 4) hipLaunchKernelGGL((gemv_kernel<TX, 4>), grid, block, 0, stream, g);
+            if constexpr (M >= 4) hipLaunchKernelGGL((gemv_kernel<TX, 4, EPI>), grid, block, 0, stream, g);
             break;
         case 5:
-            if constexpr (M >= 5) hipLaunchKernelGGL((gemv_kernel<TX, 5>), grid, block, 0, stream, g);
+            if constexpr (M >= 5) hipLaunchKernelGGL((gemv_kernel<TX, 5, EPI>), grid, block, 0, stream, g);
             break;
         case 6:
-            if constexpr (M >= 6) hipLaunchKernelGGL((gemv_kernel<TX, 6>), grid, block, 0, stream, g);
+            if constexpr (M >= 6) hipLaunchKernelGGL((gemv_kernel<TX, 6, EPI>), grid, block, 0, stream, g);
             break;
-        default: hipLaunchKernelGGL((gemv_kernel<TX, 0>), grid, block, 0, stream, g); break;
+        default: hipLaunchKernelGGL((gemv_kernel<TX, 0, EPI>), grid, block, 0, stream, g); break;
     }
 }
 
 }  // namespace
 
 int launch_gemv_group(const GemvCall* calls, int nw, const uint16_t* X, int64_t T, int64_t K, int r, float scale,
-                      void* ws, hipStream_t stream) {
+                      void* ws, hipStream_t stream, const Epilogue* ep) {
     if (nw < 1 || nw > kGemvGroup) return set_error(QL_ERR_SHAPE, "dequant GEMV: %d weights in one launch", nw);
     GemvArgs g{};
     g.X = X;
@@ -549,20 +564,30 @@ int launch_gemv_group(const GemvCall* calls, int nw, const uint16_t* X, int64_t 
     const int64_t nbs = ceil_div(K / 64, 4);
     const int ns = static_cast<int>(std::min<int64_t>(ceil_div(nbs, kGemvWaves), 1 << 20));
     const int tx = T <= 2 ? 1 : (T <= 4 ? 2 : (T <= 8 ? 4 : 8));
-    switch (tx) {
-        case 1: launch_gemv_tx<1>(ns, grid, g, stream); break;
-        case 2: launch_gemv_tx<2>(ns, grid, g, stream); break;
-        case 4: launch_gemv_tx<4>(ns, grid, g, stream); break;
-        default: launch_gemv_tx<8>(ns, grid, g, stream); break;
+    auto by_tx = [&](auto epi) {
+        constexpr bool EPI = decltype(epi)::value;
+        switch (tx) {
+            case 1: launch_gemv_tx<1, EPI>(ns, grid, g, stream); break;
+            case 2: launch_gemv_tx<2, EPI>(ns, grid, g, stream); break;
+            case 4: launch_gemv_tx<4, EPI>(ns, grid, g, stream); break;
+            default: launch_gemv_tx<8, EPI>(ns, grid, g, stream); break;
+        }
+    };
+    if (ep != nullptr) {
+        g.ep = *ep;
+        by_tx(std::true_type{});
+    } else {
+        by_tx(std::false_type{});
     }
     timer_end(QL_KERNEL_GEMV, stream);
     return check_launch("dequant GEMV");
 }
 
 int launch_gemv(const NF4Dev& w, const uint16_t* X, int64_t T, int64_t N, int64_t K, const uint16_t* A,
-                const uint16_t* B, int r, float scale, uint16_t* Y, float* U_out, void* ws, hipStream_t stream) {
+                const uint16_t* B, int r, float scale, uint16_t* Y, float* U_out, void* ws, hipStream_t stream,
+                const Epilogue* ep) {
     const GemvCall c{w, N, A, B, Y, U_out};
-    return launch_gemv_group(&c, 1, X, T, K, r, scale, ws, stream);
+    return launch_gemv_group(&c, 1, X, T, K, r, scale, ws, stream, ep);
 }
 
 }  // namespace qlnf4

@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "act.h"
 #include "qlora_nf4.h"
 
 namespace qlnf4 {
@@ -111,7 +112,8 @@ int launch_pad_copy(const uint16_t* src, int64_t rows, int64_t cols, uint16_t* d
 // ws holds gemv_ws_bytes(T, K, r) bytes, 16-B aligned.
 size_t gemv_ws_bytes(int64_t T, int64_t K, int r);
 int launch_gemv(const NF4Dev& w, const uint16_t* X, int64_t T, int64_t N, int64_t K, const uint16_t* A,
-                const uint16_t* B, int r, float scale, uint16_t* Y, float* U_out, void* ws, hipStream_t stream);
+                const uint16_t* B, int r, float scale, uint16_t* Y, float* U_out, void* ws, hipStream_t stream,
+                const Epilogue* ep = nullptr);
 // Up to four such weights that share X (the same K, T, rank and scale) in
 // one launch; weight i uses gemv_ws_bytes(T, K, r) bytes of ws from i times
 // that size on (a multiple of 256).
@@ -125,7 +127,7 @@ struct GemvCall {
 };
 constexpr int kGemvMaxGroup = 4;
 int launch_gemv_group(const GemvCall* calls, int nw, const uint16_t* X, int64_t T, int64_t K, int r, float scale,
-                      void* ws, hipStream_t stream);
+                      void* ws, hipStream_t stream, const Epilogue* ep = nullptr);  // ep: one weight's
 
 // Tile / split-K plan of the dequant GEMMs for an MA x T output with a
 // reduction of RED, and the fp32 workspace its split partials need.
@@ -141,7 +143,7 @@ size_t gemm_split_bytes(int64_t MA, int64_t T, int64_t RED);
 // bf16(s U), zero beyond r; Bsrc [N, r_b] with row stride ld_b, 16-B rows).
 int launch_gemm_fwd(const NF4Dev& w, const uint16_t* X, const uint16_t* Us, const uint16_t* Bsrc, int64_t ld_b,
                     int r_b, int rp, uint16_t* Y, int64_t T, int64_t N, int64_t K, float* split_ws,
-                    hipStream_t stream);
+                    hipStream_t stream, const Epilogue* ep = nullptr);
 // dX = dY W' + Gp A over the padded rank rp (Gp [T, rp] bf16, A [r, K]).
 // The forward with U = X A^T computed inside the GEMM launch (its first
 // workgroups; no separate projection launch): whether it applies to a
@@ -162,7 +164,8 @@ int launch_gemm_dx_g(const NF4Dev& w, const uint16_t* dY, const uint16_t* A, int
                      int64_t N, int64_t K, const ProjArgs& g, uint64_t* words, hipStream_t stream);
 // Y = X W'^T + s (X A^T) B^T with U_out = X A^T (optional), one launch.
 int launch_gemm_fwd_u(const NF4Dev& w, const uint16_t* X, const uint16_t* A, const uint16_t* B, int r, float scale,
-                      uint16_t* Y, float* U_out, int64_t T, int64_t N, int64_t K, uint64_t* words, hipStream_t stream);
+                      uint16_t* Y, float* U_out, int64_t T, int64_t N, int64_t K, uint64_t* words, hipStream_t stream,
+                      const Epilogue* ep = nullptr);
 // dX = dY W' + G A (G bf16 [T, rp]); with a keep mask dY W' + c (G A) * keep.
 int launch_gemm_dx(const NF4Dev& w, const uint16_t* dY, const uint16_t* Gp, const uint16_t* A, int r, int rp,
                    const uint8_t* keep, float c, uint16_t* dX, int64_t T, int64_t N, int64_t K, float* split_ws,
@@ -286,7 +289,23 @@ int launch_q4g_quantize(const void* W, bool w_f32, int64_t N, int64_t K, int gro
                         bool scale_f32, uint8_t* zero, hipStream_t stream);
 int launch_q4g_dequantize(const Q4GDev& w, int64_t N, int64_t K, void* out, bool bf16_out, hipStream_t stream);
 int launch_q4g_linear(const Q4GDev& w, const uint16_t* X, int64_t T, int64_t N, int64_t K, uint16_t* Y,
-                      hipStream_t stream);
+                      hipStream_t stream, const Epilogue* ep = nullptr);
+
+// dZ = dY act'(Z) (dZ null: not wanted; Z may be null without an activation)
+// and dB = sum over rows of it, N a multiple of 8.
+struct EpilogueBwdArgs {
+    const uint16_t* dY;
+    const uint16_t* Z;
+    int64_t T, N;
+    int act;
+    uint16_t* dZ;
+    float* dB;  // null: not wanted
+    int accumulate;
+    float* part;       // epilogue_bwd_ws_bytes, for dB
+    int64_t rows_per;  // set by the launcher
+};
+size_t epilogue_bwd_ws_bytes(int64_t T, int64_t N);
+int launch_epilogue_bwd(EpilogueBwdArgs a, hipStream_t stream);
 
 // Layer norm (rms 0) or root-mean-square norm over rows of C values.
 struct NormArgs {
@@ -310,6 +329,11 @@ struct NormArgs {
 int launch_norm_fwd(const NormArgs& a, hipStream_t stream);
 size_t norm_bwd_ws_bytes(int64_t T, int64_t C);
 int launch_norm_bwd(const NormArgs& a, hipStream_t stream);
+
+// out0[c] = (accumulate ? out0[c] : 0) + sum over g of part[g][c], g < parts, and
+// out1 from the array after it; each null: not wanted.
+void launch_column_sums(const float* part, int64_t parts, int64_t C, float* out0, float* out1, int accumulate,
+                        hipStream_t stream);
 
 // Log probabilities of labels: logp[t] = z[t][labels[t]] - lse(z[t]), 0 where
 // the label is outside [0, V). z [T, V] (row stride ld), bf16 or fp32.

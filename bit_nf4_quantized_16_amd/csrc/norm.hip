@@ -199,26 +199,27 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormArgs p) {
     }
 }
 
-// The workgroups' sums added in order: 16 columns a workgroup by 16 threads
-// each, y the array (dw, db).
-__global__ __launch_bounds__(256) void norm_grads_kernel(NormArgs p, int parts) {
+// Column sums of part [arrays][parts][C], in order: 16 columns a workgroup by
+// 16 threads each.
+__global__ __launch_bounds__(256) void column_sums_kernel(const float* part, int64_t parts, int64_t C, float* out0,
+                                                          float* out1, int accumulate) {
     __shared__ float red[16][17];
     const int col = threadIdx.x & 15, k = threadIdx.x >> 4;
-    const int c = blockIdx.x * 16 + col;
-    float* const out = blockIdx.y == 0 ? p.dW : p.dB;
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 16 + col;
+    float* const out = blockIdx.y == 0 ? out0 : out1;
     if (out == nullptr) return;
-    const float* const src = p.part + static_cast<int64_t>(blockIdx.y) * parts * p.C;
+    const float* const src = part + blockIdx.y * parts * C;
     float s = 0.0f;
-    if (c < p.C) {
+    if (c < C) {
 #pragma unroll 8
-        for (int g = k; g < parts; g += 16) s += src[static_cast<int64_t>(g) * p.C + c];
+        for (int64_t g = k; g < parts; g += 16) s += src[g * C + c];
     }
     red[k][col] = s;
     __syncthreads();
-    if (threadIdx.x < 16 && c < p.C) {
+    if (threadIdx.x < 16 && c < C) {
         float t = red[0][col];
         for (int i = 1; i < 16; ++i) t += red[i][col];
-        out[c] = p.accumulate ? out[c] + t : t;
+        out[c] = accumulate ? out[c] + t : t;
     }
 }
 
@@ -254,6 +255,12 @@ int64_t norm_bwd_groups(int64_t T) { return std::min<int64_t>(T, 512); }
 
 }  // namespace
 
+void launch_column_sums(const float* part, int64_t parts, int64_t C, float* out0, float* out1, int accumulate,
+                        hipStream_t stream) {
+    hipLaunchKernelGGL(column_sums_kernel, dim3(static_cast<uint32_t>(ceil_div(C, 16)), out1 != nullptr ? 2 : 1), dim3(256),
+                       0, stream, part, parts, C, out0, out1, accumulate);
+}
+
 int launch_norm_fwd(const NormArgs& a, hipStream_t stream) {
     const RowPlan r = row_plan(a.C, a.x_f32, 2);
     const int rows = r.waves == 1 ? 4 : 1;
@@ -283,9 +290,7 @@ int launch_norm_bwd(const NormArgs& a, hipStream_t stream) {
             hipLaunchKernelGGL((norm_bwd_kernel<decltype(xf)::value, decltype(wf)::value, decltype(nv)::value, false>),
                                grid, block, 0, stream, a);
     });
-    if (grads)
-        hipLaunchKernelGGL(norm_grads_kernel, dim3(static_cast<uint32_t>(ceil_div(a.C, 16)), 2), dim3(256), 0, stream, a,
-                           static_cast<int>(groups));
+    if (grads) launch_column_sums(a.part, groups, a.C, a.dW, a.dB, a.accumulate, stream);
     timer_end(QL_KERNEL_NORM, stream);
     return check_launch("norm backward");
 }

@@ -320,7 +320,17 @@ struct Q4GLinearArgs {
     uint16_t* Y;
     int64_t slice;     // set by the launcher: values of a row whose constants are in LDS at a time
     int slice_groups;  // their groups
+    Epilogue ep;       // where epilogue is set
+    int epilogue;
 };
+
+// act(y + bias) + residual for output n of a row, at i of Y.
+__device__ __forceinline__ float q4g_epilogue(const Epilogue& ep, float y, int64_t n, int64_t i) {
+    if (ep.bias != nullptr) y += bf16_to_f32(ep.bias[n]);
+    with_act(ep.act, [&](auto act) { y = act_value<decltype(act)::value>(y); });
+    if (ep.res != nullptr) y += bf16_to_f32(ep.res[i]);
+    return y;
+}
 
 // One chunk's operands of a lane, as loaded.
 template <int RT, int TX>
@@ -534,7 +544,11 @@ __global__ __launch_bounds__(512) void q4g_linear_kernel(Q4GLinearArgs p) {
 #pragma unroll
             for (int ww = 0; ww < NW; ++ww) y += reinterpret_cast<const float*>(lds + ww * kSlot)[e];
             y = q4g_finite<SF32>(y, live, p.w, p.X, tl, n0, nl, K, lane);
-            if (live) p.Y[tl * N + n0 + nl] = to_bf16_bits(y);
+            if (live) {
+                const int64_t i = tl * N + n0 + nl;
+                if (p.epilogue) y = q4g_epilogue(p.ep, y, n0 + nl, i);
+                p.Y[i] = to_bf16_bits(y);
+            }
         }
     }
 }
@@ -791,7 +805,11 @@ __global__ __launch_bounds__(64 * NW) void q4g_linear_wide_kernel(Q4GLinearArgs 
 #pragma unroll
             for (int ww = 0; ww < NW; ++ww) y += reinterpret_cast<const float*>(lds + ww * kSlot)[e];
             y = q4g_finite<SF32>(y, live, p.w, p.X + t0 * K, tl, n0, nl, K, lane);
-            if (live) p.Y[(t0 + tl) * N + n0 + nl] = to_bf16_bits(y);
+            if (live) {
+                const int64_t i = (t0 + tl) * N + n0 + nl;
+                if (p.epilogue) y = q4g_epilogue(p.ep, y, n0 + nl, i);
+                p.Y[i] = to_bf16_bits(y);
+            }
         }
     }
 }
@@ -936,8 +954,8 @@ int launch_q4g_dequantize(const Q4GDev& w, int64_t N, int64_t K, void* out, bool
 }
 
 int launch_q4g_linear(const Q4GDev& w, const uint16_t* X, int64_t T, int64_t N, int64_t K, uint16_t* Y,
-                      hipStream_t stream) {
-    const Q4GLinearArgs a{w, X, T, N, K, Y, 0, 0};
+                      hipStream_t stream, const Epilogue* ep) {
+    const Q4GLinearArgs a{w, X, T, N, K, Y, 0, 0, ep != nullptr ? *ep : Epilogue{}, ep != nullptr};
     timer_begin(QL_KERNEL_Q4G_LINEAR, stream);
     int s;
     switch (w.group) {

@@ -679,6 +679,67 @@ int q4g_dequantize(const ql_q4g_weight* w, void* out, int out_dtype, void* strea
 int q4g_linear_fwd(const ql_q4g_weight* w, const uint16_t* X, int64_t T, uint16_t* Y, void* stream);
 
 /*
+ * The linear forward with an epilogue: Y = act(z) + residual with z = X W'^T +
+ * s (X A^T) B^T + bias, in fp32 and rounded to bf16 once.
+ *
+ *   bias      [N] bf16, or NULL
+ *   act       QL_ACT_NONE, QL_ACT_SILU (z sigmoid(z)), QL_ACT_GELU (z times the
+ *             normal distribution function, to 1.1e-5 of it) or
+ *             QL_ACT_GELU_TANH (z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2)
+ *   residual  [T, N] bf16, or NULL; may be Y itself
+ *   Z         out [T, N] bf16, z rounded, which qlora_epilogue_bwd takes; or NULL
+ *
+ * The struct is host memory; its pointers are device pointers, 16-byte aligned.
+ *
+ * qlora_linear_fwd_epilogue — qlora_linear_fwd (keep NULL, p 0) or
+ * qlora_linear_fwd_dropout (keep and p as there) with an epilogue: the same
+ * products, workspace (that call's query), limits and errors; U_out is bitwise
+ * that call's, and without bias, activation and residual so is Y. QL_ERR_UNSUPPORTED
+ * also for an unknown activation and for p without keep.
+ *
+ * q4g_linear_fwd_epilogue — q4g_linear_fwd with an epilogue (Z must be NULL).
+ * Where the sum is not finite it is formed as there, then the epilogue follows.
+ *
+ * An infinite z gives act's limit where that is infinite and NaN where it is
+ * zero (z = -inf under an activation).
+ */
+#define QL_ACT_NONE 0
+#define QL_ACT_SILU 1
+#define QL_ACT_GELU 2
+#define QL_ACT_GELU_TANH 3
+typedef struct ql_epilogue {
+    const uint16_t* bias;
+    int32_t act;
+    const uint16_t* residual;
+    uint16_t* Z;
+} ql_epilogue;
+int qlora_linear_fwd_epilogue(const ql_nf4_weight* w, const uint16_t* X, int64_t T, const uint16_t* A,
+                              const uint16_t* B, int32_t r, float scale, const uint8_t* keep, float p,
+                              const ql_epilogue* e, uint16_t* Y, float* U_out, void* ws, size_t ws_bytes, void* stream);
+int q4g_linear_fwd_epilogue(const ql_q4g_weight* w, const uint16_t* X, int64_t T, const ql_epilogue* e, uint16_t* Y,
+                            void* stream);
+
+/*
+ * qlora_epilogue_bwd — back through the epilogue:
+ *
+ *   dZ = dY act'(Z)      (the dY of qlora_linear_bwd; the residual's gradient is dY)
+ *   dbias = sum over rows of dZ, before its rounding
+ *
+ *   dY, Z  [rows, cols] bf16, cols a multiple of 8; Z may be NULL with QL_ACT_NONE
+ *   dZ     out [rows, cols] bf16, or NULL; may be dY or Z
+ *   dbias  out [cols] fp32, or NULL; added to with accumulate 1
+ *   ws     qlora_epilogue_bwd_workspace(rows, cols) bytes where dbias is wanted
+ *
+ * rows == 0: dbias is an empty sum. Sums are fp32 in a fixed order.
+ * Errors: QL_ERR_NULL, QL_ERR_SHAPE (rows < 0 or over 2^31, cols, more than 2^40
+ * values), QL_ERR_UNSUPPORTED (act, accumulate), QL_ERR_ALIGN, QL_ERR_WORKSPACE,
+ * QL_ERR_HIP.
+ */
+size_t qlora_epilogue_bwd_workspace(int64_t rows, int64_t cols);
+int qlora_epilogue_bwd(const uint16_t* dY, const uint16_t* Z, int64_t rows, int64_t cols, int act, uint16_t* dZ,
+                       float* dbias, int accumulate, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * qlora_norm_fwd / qlora_norm_bwd — layer norm and root-mean-square norm over
  * the rows of an activation, and their backward:
  *

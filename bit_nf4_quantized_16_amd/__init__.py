@@ -754,7 +754,7 @@ def _epilogue(bias, act, residual, Z, T, rows, device):
         _tensor(bias, "bias", torch.bfloat16, (rows,), device)
     if residual is not None:
         _tensor(residual, "residual", torch.bfloat16, (T, rows), device)
-    return _lib.QlEpilogue(_addr(bias), code, _addr(residual), _addr(Z))
+    return _lib.QlEpilogue(_addr(bias), code, _addr(residual), _addr(Z), _DTYPES[Z.dtype] if Z is not None else 0)
 
 
 def qlora_linear_fwd_epilogue(w, X, A=None, B=None, scale=1.0, bias=None, act="none", residual=None, save_u=True,
@@ -763,8 +763,9 @@ def qlora_linear_fwd_epilogue(w, X, A=None, B=None, scale=1.0, bias=None, act="n
     linear forward with its epilogue in the same launch. bias [N] and residual
     [T, N] bf16, each optional; ``act`` "none", "silu", "gelu" or "gelu_tanh";
     ``keep`` / ``p`` as qlora_linear_fwd. Returns (Y, U or None, Z or None): U
-    fp32 [T, r] and Z = z in bf16 [T, N] for the backward. ``out``: Y's tensor,
-    which may be the residual."""
+    fp32 [T, r] and Z = z [T, N] for the backward, fp32 or, with ``save_z``
+    torch.bfloat16, rounded (half the memory). ``out``: Y's tensor, which may be
+    the residual."""
     T = _matrix(X, "X").shape[0]
     dev = w.packed.device
     _tensor(X, "X", torch.bfloat16, (T, w.cols), dev)
@@ -773,16 +774,15 @@ def qlora_linear_fwd_epilogue(w, X, A=None, B=None, scale=1.0, bias=None, act="n
     Y = torch.empty(T, w.rows, dtype=torch.bfloat16, device=dev) if new else _tensor(out, "out", torch.bfloat16,
                                                                                       (T, w.rows), dev)
     U = torch.empty(T, r, dtype=torch.float32, device=dev) if save_u and r > 0 else None
-    Z = torch.empty(T, w.rows, dtype=torch.bfloat16, device=dev) if save_z else None
+    if save_z not in (False, True, torch.float32, torch.bfloat16):
+        _refuse(_lib.QL_ERR_UNSUPPORTED, "save_z %r (False, True, torch.float32 or torch.bfloat16)" % (save_z,))
+    Z = torch.empty(T, w.rows, dtype=torch.float32 if save_z is True else save_z, device=dev) if save_z else None
     e = _epilogue(bias, act, residual, Z, T, w.rows, dev)
-    if keep is None:
-        need = lib.qlora_linear_fwd_workspace(w.rows, w.cols, max(T, 1), r)
-    else:
+    if keep is not None:
         if not isinstance(keep, torch.Tensor) or keep.numel() != T * (w.cols // 8):
             _refuse(_lib.QL_ERR_SHAPE, "keep is no tensor of %d x %d bytes" % (T, w.cols // 8))
         _tensor(keep, "keep", torch.uint8, keep.shape, dev)
-        need = lib.qlora_linear_fwd_dropout_workspace(w.rows, w.cols, max(T, 1), r)
-    ws, wsb = _workspace(need, dev)
+    ws, wsb = _workspace(lib.qlora_linear_fwd_epilogue_workspace(w.rows, w.cols, max(T, 1), r, keep is not None), dev)
     _launch(dev, lib.qlora_linear_fwd_epilogue, w.descriptor(), X.data_ptr(), T, _addr(A), _addr(B), r, float(scale),
             _addr(keep), float(p), e, Y.data_ptr(), _addr(U), _addr(ws), wsb)
     if not new:
@@ -811,21 +811,20 @@ def q4g_linear_fwd_epilogue(w, X, bias=None, act="none", residual=None, out=None
 
 
 def epilogue_bwd(dY, Z=None, act="none", need_dz=True, need_dbias=True, dbias=None, accumulate=False):
-    """Back through the epilogue: (dZ, dbias), dZ = dY act'(Z) bf16 for
+    """Back through the epilogue (Z as kept): (dZ, dbias), dZ = dY act'(Z) bf16 for
     qlora_linear_bwd and dbias fp32 [N] its sum over rows (None where not
     wanted). Without an activation dZ is dY itself. The residual's gradient is
     dY."""
     rows, cols = _matrix(dY, "dY").shape
     dev = dY.device
     code = _act(act)
-    if code != _lib.QL_ACT_NONE:
-        _tensor(Z, "Z", torch.bfloat16, (rows, cols), dev)
+    zd = _typed(Z, "Z", (rows, cols), dev) if code != _lib.QL_ACT_NONE else _lib.QL_F32
     dZ = None
     if need_dz:
         dZ = torch.empty_like(dY) if code != _lib.QL_ACT_NONE else dY
     dbias = _grads(need_dbias, dbias, (cols,), "dbias", accumulate, dev)
     ws, wsb = _workspace(lib.qlora_epilogue_bwd_workspace(rows, cols) if need_dbias else 0, dev)
-    _launch(dev, lib.qlora_epilogue_bwd, dY.data_ptr(), _addr(Z), rows, cols, code,
+    _launch(dev, lib.qlora_epilogue_bwd, dY.data_ptr(), _addr(Z), zd, rows, cols, code,
             _addr(dZ) if code != _lib.QL_ACT_NONE else None, _addr(dbias), 1 if accumulate else 0, _addr(ws), wsb)
     return dZ, dbias
 

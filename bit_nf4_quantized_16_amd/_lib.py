@@ -105,6 +105,7 @@ class QlEpilogue(ctypes.Structure):
         ("act", ctypes.c_int32),
         ("residual", ctypes.c_void_p),
         ("Z", ctypes.c_void_p),
+        ("z_dtype", ctypes.c_int32),
     ]
 
 
@@ -164,10 +165,11 @@ SIGNATURES = {
     "q4g_quantize": (_I, [_P, _I, _I64, _I64, _I32, _P, _P, _I, _P, _P]),
     "q4g_dequantize": (_I, [_GP, _P, _I, _P]),
     "q4g_linear_fwd": (_I, [_GP, _P, _I64, _P, _P]),
+    "qlora_linear_fwd_epilogue_workspace": (_SZ, [_I64, _I64, _I64, _I32, _I]),
     "qlora_linear_fwd_epilogue": (_I, [_WP, _P, _I64, _P, _P, _I32, _F, _P, _F, _EP, _P, _P, _P, _SZ, _P]),
     "q4g_linear_fwd_epilogue": (_I, [_GP, _P, _I64, _EP, _P, _P]),
     "qlora_epilogue_bwd_workspace": (_SZ, [_I64, _I64]),
-    "qlora_epilogue_bwd": (_I, [_P, _P, _I64, _I64, _I, _P, _P, _I, _P, _SZ, _P]),
+    "qlora_epilogue_bwd": (_I, [_P, _P, _I, _I64, _I64, _I, _P, _P, _I, _P, _SZ, _P]),
     "qlora_norm_fwd": (_I, [_P, _I, _I64, _I64, _P, _P, _I, _F, _I, _P, _P, _P, _P]),
     "qlora_norm_bwd_workspace": (_SZ, [_I64, _I64]),
     "qlora_norm_bwd": (_I, [_P, _I, _I64, _I64, _P, _I, _P, _P, _P, _P, _P, _P, _I, _P, _SZ, _P]),

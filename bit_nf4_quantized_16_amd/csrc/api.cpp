@@ -146,6 +146,7 @@ struct FwdWs {
     float* split = nullptr;  // fp32 split-K partials of the GEMM path
     void* gemv = nullptr;    // GEMV path: fp32 U and its projection's partials
     uint64_t* uword = nullptr;  // GEMM path with U inside the launch: U words and counters
+    float* Uf = nullptr;     // fp32 [T, r] = U in place of Us, GEMM path with an epilogue
     size_t bytes = 0;
 };
 
@@ -153,7 +154,7 @@ constexpr int64_t kGemvMaxT = 16;
 
 // Dropout (a keep mask) always takes the GEMM path: the GEMV feeds the base
 // and the adapter the same x operands.
-FwdWs carve_fwd(void* ws, int64_t N, int64_t K, int64_t T, int32_t r, bool drop = false) {
+FwdWs carve_fwd(void* ws, int64_t N, int64_t K, int64_t T, int32_t r, bool drop = false, bool epilogue = false) {
     Carver c(ws);
     FwdWs f;
     const int rp = rank_pad64(r);
@@ -165,7 +166,10 @@ FwdWs carve_fwd(void* ws, int64_t N, int64_t K, int64_t T, int32_t r, bool drop 
             f.uword = c.take<uint64_t>(gemm_fwd_u_words(T, r));  // U inside the GEMM launch
         } else if (r > 0) {
             if (drop) f.Xd = c.take<uint16_t>(static_cast<size_t>(T) * K);
-            f.Us = c.take<uint16_t>(static_cast<size_t>(T) * rp);
+            if (epilogue)
+                f.Uf = c.take<float>(static_cast<size_t>(T) * r);
+            else
+                f.Us = c.take<uint16_t>(static_cast<size_t>(T) * rp);
             if (r % 8 != 0) f.Bp = c.take<uint16_t>(static_cast<size_t>(N) * rp);
             const size_t pb = lora_proj_ws_bytes(T, r, K, false);
             if (pb) f.proj = c.take<char>(pb);
@@ -437,7 +441,8 @@ int check_epilogue(const ql_epilogue* e, int64_t T, Epilogue* out) {
         if (e->residual != nullptr && (s = check_ptr(e->residual, "residual")) != QL_OK) return s;
         if (e->Z != nullptr && (s = check_ptr(e->Z, "Z")) != QL_OK) return s;
     }
-    *out = Epilogue{e->bias, e->residual, e->Z, e->act};
+    if (e->z_dtype != QL_F32 && e->z_dtype != QL_BF16) return set_error(QL_ERR_UNSUPPORTED, "Z dtype %d", e->z_dtype);
+    *out = Epilogue{e->bias, e->residual, e->Z, e->z_dtype == QL_F32, e->act};
     return QL_OK;
 }
 
@@ -465,7 +470,7 @@ int linear_fwd(const ql_nf4_weight* w, const uint16_t* X, int64_t T, const uint1
         if ((s = check_ptr(B, "B")) != QL_OK) return s;
         if (U_out != nullptr && (s = check_ptr(U_out, "U_out")) != QL_OK) return s;
     }
-    const FwdWs need = carve_fwd(nullptr, N, K, T, r, drop);
+    const FwdWs need = carve_fwd(nullptr, N, K, T, r, drop, ep != nullptr);
     if (need.bytes > 0) {
         if (ws == nullptr || ws_bytes < need.bytes)
             return set_error(QL_ERR_WORKSPACE, "workspace %zu bytes, need %zu", ws == nullptr ? 0 : ws_bytes,
@@ -473,7 +478,7 @@ int linear_fwd(const ql_nf4_weight* w, const uint16_t* X, int64_t T, const uint1
         if (!aligned16(ws)) return set_error(QL_ERR_ALIGN, "workspace is not 16-byte aligned");
     }
     hipStream_t st = static_cast<hipStream_t>(stream);
-    const FwdWs f = carve_fwd(ws, N, K, T, r, drop);
+    const FwdWs f = carve_fwd(ws, N, K, T, r, drop, ep != nullptr);
     const NF4Dev wd = to_dev(w);
     if (T <= kGemvMaxT && !drop) return launch_gemv(wd, X, T, N, K, A, B, r, scale, Y, U_out, f.gemv, st, ep);
     if (f.uword != nullptr) return launch_gemm_fwd_u(wd, X, A, B, r, scale, Y, U_out, T, N, K, f.uword, st, ep);
@@ -498,9 +503,13 @@ int linear_fwd(const ql_nf4_weight* w, const uint16_t* X, int64_t T, const uint1
         a.alpha_f = c;
         a.out_f = U_out;
         a.ld_f = r;
-        a.alpha_b = scale * c;
-        a.out_b = f.Us;
-        a.ld_b = rp;
+        if (ep != nullptr) {  // the epilogue's GEMM takes U in fp32
+            if (U_out == nullptr) a.out_f = f.Uf;
+        } else {
+            a.alpha_b = scale * c;
+            a.out_b = f.Us;
+            a.ld_b = rp;
+        }
         if ((s = launch_lora_proj(a, false, f.proj, st)) != QL_OK) return s;
         if (r % 8 != 0) {  // rows of B are not 16-byte aligned: pad them
             if ((s = launch_pad_copy(B, N, r, f.Bp, rp, st)) != QL_OK) return s;
@@ -509,7 +518,10 @@ int linear_fwd(const ql_nf4_weight* w, const uint16_t* X, int64_t T, const uint1
             r_b = rp;
         }
     }
-    return launch_gemm_fwd(wd, X, f.Us, Bsrc, ld_b, r_b, rp, Y, T, N, K, f.split, st, ep);
+    if (ep != nullptr)
+        return launch_gemm_fwd_epilogue(wd, X, U_out != nullptr ? U_out : f.Uf, scale, r, Bsrc, ld_b, r_b, Y, T, N, K, f.split,
+                                        *ep, st);
+    return launch_gemm_fwd(wd, X, f.Us, Bsrc, ld_b, r_b, rp, Y, T, N, K, f.split, st);
 }
 
 // A grouped forward at T > 16 takes one GEMM launch over all layers' row
@@ -912,6 +924,11 @@ int qlora_linear_fwd_group(const ql_nf4_weight* const* w, int32_t nw, const uint
                            const uint16_t* const* A, const uint16_t* const* B, int32_t r, float scale,
                            uint16_t* const* Y, float* const* U_out, void* ws, size_t ws_bytes, void* stream) {
     return linear_fwd_group(w, nw, X, T, A, B, r, scale, Y, U_out, ws, ws_bytes, stream);
+}
+
+size_t qlora_linear_fwd_epilogue_workspace(int64_t rows, int64_t cols, int64_t T, int32_t r, int dropout) {
+    if (rows <= 0 || cols <= 0 || T <= 0 || r < 0 || r > QL_MAX_RANK) return 0;
+    return carve_fwd(nullptr, rows, cols, T, r, dropout != 0, true).bytes;
 }
 
 int qlora_linear_fwd_epilogue(const ql_nf4_weight* w, const uint16_t* X, int64_t T, const uint16_t* A, const uint16_t* B,

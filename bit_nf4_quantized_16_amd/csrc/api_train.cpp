@@ -163,12 +163,13 @@ size_t qlora_epilogue_bwd_workspace(int64_t rows, int64_t cols) {
     return epilogue_bwd_ws_bytes(rows, cols);
 }
 
-int qlora_epilogue_bwd(const uint16_t* dY, const uint16_t* Z, int64_t rows, int64_t cols, int act, uint16_t* dZ,
+int qlora_epilogue_bwd(const uint16_t* dY, const void* Z, int z_dtype, int64_t rows, int64_t cols, int act, uint16_t* dZ,
                        float* dbias, int accumulate, void* ws, size_t ws_bytes, void* stream) {
     clear_error();
     int s;
     if ((s = check_epilogue_shape(rows, cols)) != QL_OK) return s;
     if (act < QL_ACT_NONE || act > QL_ACT_GELU_TANH) return set_error(QL_ERR_UNSUPPORTED, "activation %d", act);
+    if ((s = check_dtype(z_dtype, "Z")) != QL_OK) return s;
     if ((s = check_flag(accumulate, "accumulate")) != QL_OK) return s;
     if (dbias == nullptr && (dZ == nullptr || rows == 0)) return QL_OK;
     if (dbias != nullptr && (s = check_ptr(dbias, "dbias")) != QL_OK) return s;
@@ -181,6 +182,7 @@ int qlora_epilogue_bwd(const uint16_t* dY, const uint16_t* Z, int64_t rows, int6
     EpilogueBwdArgs a{};
     a.dY = dY;
     a.Z = Z;
+    a.z_f32 = z_dtype == QL_F32;
     a.T = rows;
     a.N = cols;
     a.act = act;

@@ -16,7 +16,7 @@ namespace {
 
 constexpr int kThreads = 256, kUnroll = 4;
 
-template <int ACT, bool SUM>
+template <int ACT, bool SUM, bool ZF32>
 __global__ __launch_bounds__(kThreads) void epilogue_bwd_kernel(EpilogueBwdArgs p, int lanes, uint32_t blocks) {
     __shared__ float red[SUM ? kThreads * 8 : 1];
     const int slot = threadIdx.x / lanes, slots = kThreads / lanes, lane = threadIdx.x - slot * lanes;
@@ -26,24 +26,36 @@ __global__ __launch_bounds__(kThreads) void epilogue_bwd_kernel(EpilogueBwdArgs 
     const bool in = col < p.N;
     float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     for (int64_t r = r0 + slot; r < r1 && in; r += slots * kUnroll) {
-        uint4 d[kUnroll], z[kUnroll];
+        uint4 d[kUnroll], z[kUnroll], z2[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const int64_t row = r + u * slots < r1 ? r + u * slots : r1 - 1;  // read again, not used
             d[u] = *reinterpret_cast<const uint4*>(p.dY + row * p.N + col);
-            if constexpr (ACT != QL_ACT_NONE) z[u] = *reinterpret_cast<const uint4*>(p.Z + row * p.N + col);
+            if constexpr (ACT != QL_ACT_NONE && ZF32) {
+                const uint4* const zp = reinterpret_cast<const uint4*>(static_cast<const float*>(p.Z) + row * p.N + col);
+                z[u] = zp[0];
+                z2[u] = zp[1];
+            } else if constexpr (ACT != QL_ACT_NONE) {
+                z[u] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.Z) + row * p.N + col);
+            }
         }
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const int64_t row = r + u * slots;
             if (row >= r1) continue;
             const uint32_t dw[4] = {d[u].x, d[u].y, d[u].z, d[u].w};
-            uint32_t zw[4] = {0, 0, 0, 0}, o[4];
-            if constexpr (ACT != QL_ACT_NONE) zw[0] = z[u].x, zw[1] = z[u].y, zw[2] = z[u].z, zw[3] = z[u].w;
+            float zv[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            uint32_t o[4];
+            if constexpr (ACT != QL_ACT_NONE) {
+                const uint32_t zw[8] = {z[u].x, z[u].y, z[u].z, z[u].w, z2[u].x, z2[u].y, z2[u].z, z2[u].w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    zv[i] = __uint_as_float(ZF32 ? zw[i] : i % 2 ? zw[i / 2] & 0xFFFF0000u : zw[i / 2] << 16);
+            }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const float g0 = __uint_as_float(dw[q] << 16) * act_slope<ACT>(__uint_as_float(zw[q] << 16));
-                const float g1 = __uint_as_float(dw[q] & 0xFFFF0000u) * act_slope<ACT>(__uint_as_float(zw[q] & 0xFFFF0000u));
+                const float g0 = __uint_as_float(dw[q] << 16) * act_slope<ACT>(zv[2 * q]);
+                const float g1 = __uint_as_float(dw[q] & 0xFFFF0000u) * act_slope<ACT>(zv[2 * q + 1]);
                 o[q] = pack_bf16x2(g0, g1);
                 if constexpr (SUM) {
                     s[2 * q] += g0;
@@ -100,12 +112,20 @@ int launch_epilogue_bwd(EpilogueBwdArgs a, hipStream_t stream) {
         runs = pl.runs;
         with_act(a.act, [&](auto act) {
             const dim3 grid(static_cast<uint32_t>(pl.blocks * pl.runs));
+            auto launch = [&](auto sum, auto zf32) {
+                hipLaunchKernelGGL((epilogue_bwd_kernel<decltype(act)::value, decltype(sum)::value, decltype(zf32)::value>),
+                                   grid, dim3(kThreads), 0, stream, a, pl.lanes, static_cast<uint32_t>(pl.blocks));
+            };
+            auto by_z = [&](auto sum) {
+                if (decltype(act)::value != QL_ACT_NONE && a.z_f32)
+                    launch(sum, std::true_type{});
+                else
+                    launch(sum, std::false_type{});
+            };
             if (a.dB != nullptr)
-                hipLaunchKernelGGL((epilogue_bwd_kernel<decltype(act)::value, true>), grid, dim3(kThreads), 0, stream, a,
-                                   pl.lanes, static_cast<uint32_t>(pl.blocks));
+                by_z(std::true_type{});
             else
-                hipLaunchKernelGGL((epilogue_bwd_kernel<decltype(act)::value, false>), grid, dim3(kThreads), 0, stream, a,
-                                   pl.lanes, static_cast<uint32_t>(pl.blocks));
+                by_z(std::false_type{});
         });
     }
     if (a.dB != nullptr) launch_column_sums(a.part, runs, a.N, a.dB, nullptr, a.accumulate, stream);

@@ -94,7 +94,11 @@ struct TileArgs {
     // keep bits [T, K / 8] and c = 1 / (1 - p).
     const uint8_t* keep;
     float c;
-    Epilogue ep;  // the EPI kernels (one forward)
+    // The EPI kernels (one forward with an epilogue): the rank steps take s U
+    // as two bf16 terms, from the fp32 U or the words.
+    Epilogue ep;
+    const float* uf;  // [T, r_f]
+    int r_f;
 };
 
 typedef short v4i16 __attribute__((ext_vector_type(4)));
@@ -598,6 +602,14 @@ __global__ __launch_bounds__(64 * WA * WT, 512 / (64 * WA * WT)) void tile_gemm_
     // tile forms its values itself, each an fp32 sum of the products in k
     // order (plain fused multiply-adds, a few registers; the same values up
     // to rounding, not bit for bit). Ranks r_u .. 63 are zero.
+    // (EPI: s U in two bf16 terms, value and rest, ranks j and 32 + j of the
+    // step.)
+    auto put_u = [&](int row, int j, float v) {
+        const uint16_t hi = to_bf16_bits(v);
+        sX0[row * kStep + 8 * ((j >> 3) ^ swz(row)) + (j & 7)] = hi;
+        if constexpr (EPI)
+            sX0[row * kStep + 8 * ((4 + (j >> 3)) ^ swz(row)) + (j & 7)] = to_bf16_bits(v - bf16_to_f32(hi));
+    };
     auto stage_u_words = [&]() {
         if constexpr (kUin) {
         constexpr int WPT = TT * 16 / NTHR;  // words a thread, at most
@@ -618,8 +630,7 @@ __global__ __launch_bounds__(64 * WA * WT, 512 / (64 * WA * WT)) void tile_gemm_
                                                __HIP_MEMORY_SCOPE_AGENT);
                         ok = ok && static_cast<uint32_t>(wd >> 32) == tag;
                     }
-                    sX0[row * kStep + 8 * ((j >> 3) ^ swz(row)) + (j & 7)] =
-                        to_bf16_bits(p.s_u * __uint_as_float(static_cast<uint32_t>(wd)));
+                    put_u(row, j, p.s_u * __uint_as_float(static_cast<uint32_t>(wd)));
                 }
             }
             return ok;
@@ -674,16 +685,40 @@ __global__ __launch_bounds__(64 * WA * WT, 512 / (64 * WA * WT)) void tile_gemm_
                         }
                     }
                 }
-                sX0[row * kStep + 8 * ((j >> 3) ^ swz(row)) + (j & 7)] = to_bf16_bits(p.s_u * u);
+                put_u(row, j, p.s_u * u);
             }
         }
-        // ranks r_u .. 63 are zero
+        // ranks r_u .. 63 are zero (with two terms r_u .. 31 and 32 + r_u .. 63)
 #pragma unroll
         for (int i = 0; i < TT * 8 / NTHR; ++i) {
             const int c = tid + NTHR * i;
             const int row = c >> 3, lc = c & 7;
-            if (8 * lc >= p.r_u) st16(sX0 + row * kStep + 8 * (lc ^ swz(row)), make_uint4(0, 0, 0, 0));
+            if (8 * (EPI ? lc & 3 : lc) >= p.r_u) st16(sX0 + row * kStep + 8 * (lc ^ swz(row)), make_uint4(0, 0, 0, 0));
         }
+        }
+    };
+
+    // The same operand from U in memory, eight ranks a thread and turn.
+    auto stage_u_terms = [&](int j0, bool both, bool rest_term) {
+        if constexpr (EPI) {
+#pragma unroll
+            for (int i = 0; i < TT * 8 / NTHR; ++i) {
+                const int c = tid + NTHR * i;
+                const int row = c >> 3, lc = c & 7;
+                const int64_t t = t0 + row;
+                const int j = j0 + 8 * (both ? lc & 3 : lc);
+                const bool low = both ? lc >= 4 : rest_term;
+                float v[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) v[q] = t < p.T && j + q < p.r_f ? p.s_u * p.uf[t * p.r_f + j + q] : 0.0f;
+                if (low) {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) v[q] -= bf16_to_f32(to_bf16_bits(v[q]));
+                }
+                st16(sX0 + row * kStep + 8 * (lc ^ swz(row)),
+                     make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                pack_bf16x2(v[6], v[7])));
+            }
         }
     };
 
@@ -691,15 +726,24 @@ __global__ __launch_bounds__(64 * WA * WT, 512 / (64 * WA * WT)) void tile_gemm_
     // (by the first split only; in a grouped dX, each layer's by split
     // L % splits: rank step ls of this split is step ls % nr of layer
     // split + (ls / nr) splits).
-    const int nr = p.rp / kStep;
+    // EPI: both terms of s U in one step up to rank 32, else the values' steps
+    // and then the rests'.
+    const bool packed = EPI && p.r_f <= 32;
+    const int nr = EPI && !packed ? 2 * (p.rp / kStep) : p.rp / kStep;
     constexpr bool kGdx = GRP && DX, kGfwd = GRP && !DX;
     const int nls = KEEP ? 0 : kGdx ? (split < p.ng ? nr * ((p.ng - 1 - split) / p.splits + 1) : 0) : (split == 0 ? nr : 0);
     for (int ls = 0; ls < nls; ++ls) {
         const int rl = kGdx ? split + (ls / nr) * p.splits : fl;  // the rank step's layer
         const uint16_t* const lt = GRP ? p.gl[rl].lt : p.lt;
         const uint16_t* const la = GRP ? p.gl[rl].la : p.la;
-        const int64_t j0 = static_cast<int64_t>(kGdx ? ls % nr : ls) * kStep;
-        if (kUin && p.nu > 0) {
+        const bool rest = EPI && !packed && ls >= nr / 2;
+        const int64_t j0 = static_cast<int64_t>(kGdx ? ls % nr : rest ? ls - nr / 2 : ls) * kStep;
+        if constexpr (EPI) {
+            if (kUin && p.nu > 0)
+                stage_u_words();
+            else
+                stage_u_terms(static_cast<int>(j0), packed, rest);
+        } else if (kUin && p.nu > 0) {
             stage_u_words();  // rp == 64: the one rank step
         } else {
 #pragma unroll
@@ -717,7 +761,7 @@ __global__ __launch_bounds__(64 * WA * WT, 512 / (64 * WA * WT)) void tile_gemm_
             for (int i = 0; i < TA * 8 / NTHR; ++i) {
                 const int c = tid + NTHR * i;
                 const int64_t n = m0 + (c >> 3);
-                const int64_t j = j0 + 8 * (c & 7);
+                const int64_t j = j0 + 8 * (packed ? c & 3 : c & 7);
                 const uint4 v = (n < MA && j < p.r_la) ? ld16(la + n * p.ld_la + j) : make_uint4(0, 0, 0, 0);
                 st16(sA0 + (c >> 3) * LDA + 8 * (c & 7), v);
             }
@@ -820,13 +864,29 @@ __global__ __launch_bounds__(64 * WA * WT, 512 / (64 * WA * WT)) void tile_gemm_
                         for (int i = 0; i < 4; ++i) acc[a][b][4 * qq + i] += bf[i];
                 }
         }
-        if (p.ep.z != nullptr) {
+        if (p.ep.z != nullptr && p.ep.z_f32) {
+            // as the split partials, straight from the registers
+#pragma unroll
+            for (int a = 0; a < SA; ++a)
+#pragma unroll
+                for (int b = 0; b < ST; ++b)
+#pragma unroll
+                    for (int qq = 0; qq < 4; ++qq) {
+                        const int64_t m = m0 + wa * MW + a * 32 + 8 * qq + 4 * (lane >> 5);
+                        const int64_t t = t0 + wt * TW + b * 32 + (lane & 31);
+                        if (t < p.T && m < MA)
+                            p.ep.keep4(t * MA + m, acc[a][b][4 * qq], acc[a][b][4 * qq + 1], acc[a][b][4 * qq + 2],
+                                       acc[a][b][4 * qq + 3]);
+                    }
+        } else if (p.ep.z != nullptr) {
             quads([&](int a, int b, int qq, uint2* at) {
                 *at = make_uint2(pack_bf16x2(acc[a][b][4 * qq], acc[a][b][4 * qq + 1]),
                                  pack_bf16x2(acc[a][b][4 * qq + 2], acc[a][b][4 * qq + 3]));
             });
             __syncthreads();
-            pieces([&](const uint4* at, int64_t g) { *reinterpret_cast<uint4*>(p.ep.z + g) = *at; });
+            pieces([&](const uint4* at, int64_t g) {
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.ep.z) + g) = *at;
+            });
             __syncthreads();
         }
         const bool res = p.ep.res != nullptr;
@@ -923,7 +983,7 @@ __global__ void split_reduce_epilogue_kernel(const float* __restrict__ part, int
         *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
     };
     if (ep.bias != nullptr) add(ep.bias + m);
-    if (ep.z != nullptr) put(ep.z + at);
+    ep.keep4(at, y[0], y[1], y[2], y[3]);
     with_act(ep.act, [&](auto act) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[i] = act_value<decltype(act)::value>(y[i]);
@@ -1054,8 +1114,7 @@ size_t gemm_split_bytes(int64_t MA, int64_t T, int64_t RED) {
 }
 
 int launch_gemm_fwd(const NF4Dev& w, const uint16_t* X, const uint16_t* Us, const uint16_t* Bsrc, int64_t ld_b,
-                    int r_b, int rp, uint16_t* Y, int64_t T, int64_t N, int64_t K, float* split_ws, hipStream_t stream,
-                    const Epilogue* ep) {
+                    int r_b, int rp, uint16_t* Y, int64_t T, int64_t N, int64_t K, float* split_ws, hipStream_t stream) {
     TileArgs a{};
     a.w = w;
     a.act = X;
@@ -1069,8 +1128,28 @@ int launch_gemm_fwd(const NF4Dev& w, const uint16_t* X, const uint16_t* Us, cons
     a.T = T;
     a.N = N;
     a.K = K;
-    if (ep == nullptr) return launch_tiles<false>(a, split_ws, QL_KERNEL_GEMM_FWD, "dequant GEMM forward", stream);
-    a.ep = *ep;
+    return launch_tiles<false>(a, split_ws, QL_KERNEL_GEMM_FWD, "dequant GEMM forward", stream);
+}
+
+int launch_gemm_fwd_epilogue(const NF4Dev& w, const uint16_t* X, const float* U, float scale, int r, const uint16_t* Bsrc,
+                             int64_t ld_b, int r_b, uint16_t* Y, int64_t T, int64_t N, int64_t K, float* split_ws,
+                             const Epilogue& ep, hipStream_t stream) {
+    TileArgs a{};
+    a.w = w;
+    a.act = X;
+    a.ld_act = K;
+    a.la = Bsrc;
+    a.ld_la = ld_b;
+    a.r_la = r_b;
+    a.rp = static_cast<int>(ceil_div(r, kStep)) * kStep;
+    a.out = Y;
+    a.T = T;
+    a.N = N;
+    a.K = K;
+    a.ep = ep;
+    a.uf = U;
+    a.r_f = r;
+    a.s_u = scale;
     return launch_tiles<false, false, false, true>(a, split_ws, QL_KERNEL_GEMM_FWD, "dequant GEMM forward with an epilogue",
                                                    stream);
 }
@@ -1182,6 +1261,7 @@ int launch_gemm_fwd_u(const NF4Dev& w, const uint16_t* X, const uint16_t* A, con
     if (ep == nullptr)
         return launch_tiles<false>(a, nullptr, QL_KERNEL_GEMM_FWD, "dequant GEMM forward", stream, nu);
     a.ep = *ep;
+    a.r_f = r;
     return launch_tiles<false, false, false, true>(a, nullptr, QL_KERNEL_GEMM_FWD, "dequant GEMM forward with an epilogue",
                                                    stream, nu);
 }

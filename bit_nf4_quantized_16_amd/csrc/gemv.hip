@@ -445,7 +445,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(gemv_min_wa
             }
             if constexpr (EPI) {
                 sum += bf16_to_f32(ebias);
-                if (p.ep.z != nullptr) p.ep.z[ot * N + n] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(sum));
+                p.ep.keep(ot * N + n, sum);
                 with_act(p.ep.act, [&](auto act) { sum = act_value<decltype(act)::value>(sum); });
                 if (p.ep.res != nullptr) sum += bf16_to_f32(eres);
             }

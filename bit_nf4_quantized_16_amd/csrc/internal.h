@@ -143,7 +143,12 @@ size_t gemm_split_bytes(int64_t MA, int64_t T, int64_t RED);
 // bf16(s U), zero beyond r; Bsrc [N, r_b] with row stride ld_b, 16-B rows).
 int launch_gemm_fwd(const NF4Dev& w, const uint16_t* X, const uint16_t* Us, const uint16_t* Bsrc, int64_t ld_b,
                     int r_b, int rp, uint16_t* Y, int64_t T, int64_t N, int64_t K, float* split_ws,
-                    hipStream_t stream, const Epilogue* ep = nullptr);
+                    hipStream_t stream);
+// The same with an epilogue, from U in fp32 [T, r]: s U enters as two bf16
+// terms (16 bits), so z is as good as fp32 sums make it.
+int launch_gemm_fwd_epilogue(const NF4Dev& w, const uint16_t* X, const float* U, float scale, int r, const uint16_t* Bsrc,
+                             int64_t ld_b, int r_b, uint16_t* Y, int64_t T, int64_t N, int64_t K, float* split_ws,
+                             const Epilogue& ep, hipStream_t stream);
 // dX = dY W' + Gp A over the padded rank rp (Gp [T, rp] bf16, A [r, K]).
 // The forward with U = X A^T computed inside the GEMM launch (its first
 // workgroups; no separate projection launch): whether it applies to a
@@ -295,7 +300,8 @@ int launch_q4g_linear(const Q4GDev& w, const uint16_t* X, int64_t T, int64_t N, 
 // and dB = sum over rows of it, N a multiple of 8.
 struct EpilogueBwdArgs {
     const uint16_t* dY;
-    const uint16_t* Z;
+    const void* Z;
+    int z_f32;
     int64_t T, N;
     int act;
     uint16_t* dZ;

@@ -687,15 +687,20 @@ int q4g_linear_fwd(const ql_q4g_weight* w, const uint16_t* X, int64_t T, uint16_
  *             normal distribution function, to 1.1e-5 of it) or
  *             QL_ACT_GELU_TANH (z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2)
  *   residual  [T, N] bf16, or NULL; may be Y itself
- *   Z         out [T, N] bf16, z rounded, which qlora_epilogue_bwd takes; or NULL
+ *   Z         out [T, N], z for qlora_epilogue_bwd, fp32 (z_dtype QL_F32) or
+ *             rounded to bf16 (QL_BF16: half the memory; z off by up to 2^-9 of
+ *             itself then moves dZ and dbias); or NULL
  *
  * The struct is host memory; its pointers are device pointers, 16-byte aligned.
  *
  * qlora_linear_fwd_epilogue — qlora_linear_fwd (keep NULL, p 0) or
- * qlora_linear_fwd_dropout (keep and p as there) with an epilogue: the same
- * products, workspace (that call's query), limits and errors; U_out is bitwise
- * that call's, and without bias, activation and residual so is Y. QL_ERR_UNSUPPORTED
- * also for an unknown activation and for p without keep.
+ * qlora_linear_fwd_dropout (keep and p as there) with an epilogue, limits and
+ * errors as there; U_out is bitwise that call's. For T <= 16 without bias,
+ * activation and residual so is Y; past it s U enters the product as two bf16
+ * terms (16 bits, there one of 8). The workspace is
+ * qlora_linear_fwd_epilogue_workspace(...) bytes, dropout nonzero when keep is
+ * given. QL_ERR_UNSUPPORTED also for an unknown activation or Z dtype and for p
+ * without keep.
  *
  * q4g_linear_fwd_epilogue — q4g_linear_fwd with an epilogue (Z must be NULL).
  * Where the sum is not finite it is formed as there, then the epilogue follows.
@@ -711,8 +716,10 @@ typedef struct ql_epilogue {
     const uint16_t* bias;
     int32_t act;
     const uint16_t* residual;
-    uint16_t* Z;
+    void* Z;
+    int32_t z_dtype;
 } ql_epilogue;
+size_t qlora_linear_fwd_epilogue_workspace(int64_t rows, int64_t cols, int64_t T, int32_t r, int dropout);
 int qlora_linear_fwd_epilogue(const ql_nf4_weight* w, const uint16_t* X, int64_t T, const uint16_t* A,
                               const uint16_t* B, int32_t r, float scale, const uint8_t* keep, float p,
                               const ql_epilogue* e, uint16_t* Y, float* U_out, void* ws, size_t ws_bytes, void* stream);
@@ -725,19 +732,20 @@ int q4g_linear_fwd_epilogue(const ql_q4g_weight* w, const uint16_t* X, int64_t T
  *   dZ = dY act'(Z)      (the dY of qlora_linear_bwd; the residual's gradient is dY)
  *   dbias = sum over rows of dZ, before its rounding
  *
- *   dY, Z  [rows, cols] bf16, cols a multiple of 8; Z may be NULL with QL_ACT_NONE
- *   dZ     out [rows, cols] bf16, or NULL; may be dY or Z
+ *   dY     [rows, cols] bf16, cols a multiple of 8
+ *   Z      [rows, cols] fp32 or bf16 (z_dtype); may be NULL with QL_ACT_NONE
+ *   dZ     out [rows, cols] bf16, or NULL; may be dY, or a bf16 Z
  *   dbias  out [cols] fp32, or NULL; added to with accumulate 1
  *   ws     qlora_epilogue_bwd_workspace(rows, cols) bytes where dbias is wanted
  *
  * rows == 0: dbias is an empty sum. Sums are fp32 in a fixed order.
  * Errors: QL_ERR_NULL, QL_ERR_SHAPE (rows < 0 or over 2^31, cols, more than 2^40
- * values), QL_ERR_UNSUPPORTED (act, accumulate), QL_ERR_ALIGN, QL_ERR_WORKSPACE,
- * QL_ERR_HIP.
+ * values), QL_ERR_UNSUPPORTED (act, z_dtype, accumulate), QL_ERR_ALIGN,
+ * QL_ERR_WORKSPACE, QL_ERR_HIP.
  */
 size_t qlora_epilogue_bwd_workspace(int64_t rows, int64_t cols);
-int qlora_epilogue_bwd(const uint16_t* dY, const uint16_t* Z, int64_t rows, int64_t cols, int act, uint16_t* dZ,
-                       float* dbias, int accumulate, void* ws, size_t ws_bytes, void* stream);
+int qlora_epilogue_bwd(const uint16_t* dY, const void* Z, int z_dtype, int64_t rows, int64_t cols, int act,
+                       uint16_t* dZ, float* dbias, int accumulate, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * qlora_norm_fwd / qlora_norm_bwd — layer norm and root-mean-square norm over

@@ -26,8 +26,8 @@ def lib(L):
     return L.load(LIB)
 
 
-def _e(L, bias=P, act=2, residual=P, Z=P):
-    return L.QlEpilogue(bias, act, residual, Z)
+def _e(L, bias=P, act=2, residual=P, Z=P, z_dtype=0):
+    return L.QlEpilogue(bias, act, residual, Z, z_dtype)
 
 
 def test_linear(lib, L):
@@ -39,7 +39,7 @@ def test_linear(lib, L):
     for status, cases in (
             ("QL_ERR_NULL", [dict(w=None), dict(X=None), dict(e=None), dict(Y=None), dict(A=None), dict(B=None)]),
             ("QL_ERR_SHAPE", [dict(T=-1), dict(r=-1), dict(r=1000), dict(w=L.QlNf4Weight(60, 128, 64, 256, P, P, P, P, P))]),
-            ("QL_ERR_UNSUPPORTED", [dict(e=_e(L, act=4)), dict(e=_e(L, act=-1)), dict(p=0.1), dict(keep=P, p=1.0),
+            ("QL_ERR_UNSUPPORTED", [dict(e=_e(L, act=4)), dict(e=_e(L, act=-1)), dict(e=_e(L, z_dtype=2)), dict(p=0.1), dict(keep=P, p=1.0),
                                     dict(e=_e(L, act=9), T=0)]),
             ("QL_ERR_ALIGN", [dict(e=_e(L, bias=MIS)), dict(e=_e(L, residual=MIS)), dict(e=_e(L, Z=MIS)), dict(X=MIS),
                               dict(Y=MIS), dict(ws=MIS), dict(U=MIS)]),
@@ -66,8 +66,8 @@ def test_q4g(lib, L):
 
 
 def test_backward(lib, L):
-    def call(dY=P, Z=P, rows=4, cols=64, act=2, dZ=P, db=P, acc=0, ws=P, n=1 << 40):
-        return lib.qlora_epilogue_bwd(dY, Z, rows, cols, act, dZ, db, acc, ws, n, None)
+    def call(dY=P, Z=P, zd=1, rows=4, cols=64, act=2, dZ=P, db=P, acc=0, ws=P, n=1 << 40):
+        return lib.qlora_epilogue_bwd(dY, Z, zd, rows, cols, act, dZ, db, acc, ws, n, None)
 
     need = lib.qlora_epilogue_bwd_workspace(4, 64)
     assert need >= 256
@@ -75,7 +75,7 @@ def test_backward(lib, L):
             ("QL_ERR_NULL", [dict(dY=None), dict(Z=None)]),
             ("QL_ERR_SHAPE", [dict(rows=-1), dict(rows=1 << 32), dict(cols=0), dict(cols=12), dict(cols=1 << 40),
                               dict(rows=1 << 20, cols=1 << 21)]),
-            ("QL_ERR_UNSUPPORTED", [dict(act=4), dict(act=-1), dict(acc=3)]),
+            ("QL_ERR_UNSUPPORTED", [dict(act=4), dict(act=-1), dict(zd=2), dict(acc=3)]),
             ("QL_ERR_ALIGN", [dict(dY=MIS), dict(Z=MIS), dict(dZ=MIS), dict(db=MIS), dict(ws=MIS)]),
             ("QL_ERR_WORKSPACE", [dict(ws=None), dict(n=need - 1)]),
             ("QL_OK", [dict(dZ=None, db=None, dY=None, Z=None), dict(rows=0, db=None, dY=None)])):
@@ -86,7 +86,7 @@ def test_backward(lib, L):
 
 
 def test_the_struct_has_the_headers_layout(L):
-    assert ctypes.sizeof(L.QlEpilogue) == 32 and L.QlEpilogue.residual.offset == 16
+    assert ctypes.sizeof(L.QlEpilogue) == 40 and L.QlEpilogue.residual.offset == 16
 
 
 def test_python_refusals_need_no_gpu():

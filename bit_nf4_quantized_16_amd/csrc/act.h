@@ -96,6 +96,18 @@ struct Epilogue {
         else
             static_cast<uint16_t*>(z)[at] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
     }
+    // eight values at a multiple of eight
+    __device__ __forceinline__ void keep8(int64_t at, const float (&v)[8]) const {
+        if (z == nullptr) return;
+        if (z_f32) {
+            float4* const o = reinterpret_cast<float4*>(static_cast<float*>(z) + at);
+            o[0] = make_float4(v[0], v[1], v[2], v[3]);
+            o[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(z) + at) =
+                make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+        }
+    }
     // four values at a multiple of four
     __device__ __forceinline__ void keep4(int64_t at, float a, float b, float c, float d) const {
         if (z == nullptr) return;

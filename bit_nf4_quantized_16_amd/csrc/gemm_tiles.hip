@@ -806,6 +806,93 @@ __global__ __launch_bounds__(64 * WA * WT, 512 / (64 * WA * WT)) void tile_gemm_
                 }
         return;
     }
+    if constexpr (EPI) {
+        // The sums through the (now idle) LDS stages in fp32, ST times 64 rows
+        // of tokens, so that a thread then has eight outputs of one token: its
+        // bias, residual, z and result are whole 16-byte pieces of rows, and
+        // the activation's code is short (unrolled over the accumulators it
+        // spilled 132 registers and took 174 us for 131 at 11008 x 4096, T =
+        // 1000). Piece of four sums c of row t at c ^ (t % 32); even and odd turns
+        // alternate between the stages, so a turn has one barrier.
+        constexpr int TPP = TA / 8, RPI = NTHR / TPP, NI = 64 / RPI;  // threads a row, rows a pass, passes a turn
+        static_assert(WT == 2 && NI * RPI == 64 && 32 * TA * 4 <= TT * kStep * 2 && 32 * TA * 4 <= S::ROWS_A * LDA * 2,
+                      "a turn's sums fit in the stages");
+        const int c8 = tid % TPP, prow = tid / TPP;
+        const int64_t gm = m0 + 8 * c8;
+        const bool in = gm < MA;  // MA is a multiple of 8: a piece is whole or outside
+        auto unpack = [](const uint4& u, float (&f)[8]) {
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                f[2 * q] = __uint_as_float(w[q] << 16);
+                f[2 * q + 1] = __uint_as_float(w[q] & 0xFFFF0000u);
+            }
+        };
+        uint4 bias = make_uint4(0, 0, 0, 0);
+        if (p.ep.bias != nullptr && in) bias = ld16(p.ep.bias + gm);
+        auto half = [&](int turn, int h) {  // 32 tokens' sums
+            return reinterpret_cast<char*>(h == 0 ? (turn & 1 ? sA1 : sA0) : (turn & 1 ? sX1 : sX0));
+        };
+        auto put = [&](int turn, const f32x16 (&v)[SA]) {
+            char* const row = half(turn, wt) + (lane & 31) * (TA * 4);
+#pragma unroll
+            for (int a = 0; a < SA; ++a)
+#pragma unroll
+                for (int qq = 0; qq < 4; ++qq) {
+                    const int c = (wa * MW + a * 32 + 8 * qq) / 4 + (lane >> 5);
+                    *reinterpret_cast<float4*>(row + 16 * (c ^ (lane & 31))) =
+                        make_float4(v[a][4 * qq], v[a][4 * qq + 1], v[a][4 * qq + 2], v[a][4 * qq + 3]);
+                }
+        };
+        __syncthreads();  // every wave is done reading the stages
+#pragma unroll 1
+        for (int turn = 0; turn < ST; ++turn) {
+            auto token = [&](int i) {  // of this thread in pass i
+                const int r = prow + i * RPI;
+                return t0 + (r >> 5) * TW + turn * 32 + (r & 31);
+            };
+            uint4 res[NI];
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                res[i] = make_uint4(0, 0, 0, 0);
+                if (p.ep.res != nullptr && in && token(i) < p.T) res[i] = ld16(p.ep.res + token(i) * MA + gm);
+            }
+#pragma unroll
+            for (int b = 0; b < ST; ++b)
+                if (b == turn) {
+                    f32x16 v[SA];
+#pragma unroll
+                    for (int a = 0; a < SA; ++a) v[a] = acc[a][b];
+                    put(turn, v);
+                }
+            __syncthreads();
+            with_act(p.ep.act, [&](auto act) {
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    const int r = prow + i * RPI;
+                    const int64_t t = token(i);
+                    const char* const row = half(turn, r >> 5) + (r & 31) * (TA * 4);
+                    const float4 z0 = *reinterpret_cast<const float4*>(row + 16 * ((2 * c8) ^ (r & 31)));
+                    const float4 z1 = *reinterpret_cast<const float4*>(row + 16 * ((2 * c8 + 1) ^ (r & 31)));
+                    float y[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w}, f[8];
+                    unpack(bias, f);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) y[q] += f[q];
+                    if (!in || t >= p.T) continue;
+                    p.ep.keep8(t * MA + gm, y);
+                    unpack(res[i], f);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        y[q] = act_value<decltype(act)::value>(y[q]);
+                        if (p.ep.res != nullptr) y[q] += f[q];
+                    }
+                    st16(p.out + t * MA + gm, make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
+                                                         pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7])));
+                }
+            });
+        }
+        return;
+    }
     // bf16 tile through the (now idle) LDS stages, transposed to [t][m], so
     // that every global store writes whole 16-byte chunks of output rows
     // (lanes 8 bytes each in 32 different rows would scatter the writes).
@@ -818,109 +905,31 @@ __global__ __launch_bounds__(64 * WA * WT, 512 / (64 * WA * WT)) void tile_gemm_
         uint16_t* const base = g == 0 ? sA0 : g == 1 ? sA1 : g == 2 ? sX0 : sX1;
         return reinterpret_cast<char*>(base) + (t % RPA) * (TA * 2);
     };
-    // the tile's pieces c of rows t, 16 bytes of a global row a thread and turn
-    auto pieces = [&](auto f) {
-#pragma unroll
-        for (int i = 0; i < TT * CPR / NTHR; ++i) {
-            const int q = i * NTHR + tid;
-            const int t = q / CPR, c = q % CPR;
-            const int64_t gt = t0 + t, gm = m0 + 8 * c;
-            if (gt >= p.T || gm >= MA) continue;  // MA is a multiple of 8: a chunk is whole or outside
-            f(reinterpret_cast<uint4*>(out_row(t) + (c ^ (t % RPA % CPR)) * 16), gt * MA + gm);
-        }
-    };
-    // f(a, b, qq, where these four values of the tile are staged)
-    auto quads = [&](auto f) {
-#pragma unroll
-        for (int a = 0; a < SA; ++a)
-#pragma unroll
-            for (int b = 0; b < ST; ++b)
-#pragma unroll
-                for (int qq = 0; qq < 4; ++qq) {
-                    const int m = wa * MW + a * 32 + 8 * qq + 4 * (lane >> 5);
-                    const int t = wt * TW + b * 32 + (lane & 31);
-                    const int c = (m / 8) ^ (t % RPA % CPR);
-                    f(a, b, qq, reinterpret_cast<uint2*>(out_row(t) + c * 16 + (m % 8) * 2));
-                }
-    };
     __syncthreads();  // every wave is done reading the stages
-    if constexpr (EPI) {
-        // Bias in the accumulators; z through the stages where it is kept; the
-        // residual into the stages as it comes (whole pieces), from where each
-        // lane takes its values and puts the sums in their place: everything
-        // is fp32 until the one rounding.
-        if (p.ep.bias != nullptr) {
 #pragma unroll
-            for (int a = 0; a < SA; ++a)
+    for (int a = 0; a < SA; ++a)
 #pragma unroll
-                for (int qq = 0; qq < 4; ++qq) {
-                    const int64_t m = std::min<int64_t>(m0 + wa * MW + a * 32 + 8 * qq + 4 * (lane >> 5), MA - 4);
-                    const uint2 bv = *reinterpret_cast<const uint2*>(p.ep.bias + m);
-                    const float bf[4] = {__uint_as_float(bv.x << 16), __uint_as_float(bv.x & 0xFFFF0000u),
-                                         __uint_as_float(bv.y << 16), __uint_as_float(bv.y & 0xFFFF0000u)};
+        for (int b = 0; b < ST; ++b)
 #pragma unroll
-                    for (int b = 0; b < ST; ++b)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[a][b][4 * qq + i] += bf[i];
-                }
-        }
-        if (p.ep.z != nullptr && p.ep.z_f32) {
-            // as the split partials, straight from the registers
-#pragma unroll
-            for (int a = 0; a < SA; ++a)
-#pragma unroll
-                for (int b = 0; b < ST; ++b)
-#pragma unroll
-                    for (int qq = 0; qq < 4; ++qq) {
-                        const int64_t m = m0 + wa * MW + a * 32 + 8 * qq + 4 * (lane >> 5);
-                        const int64_t t = t0 + wt * TW + b * 32 + (lane & 31);
-                        if (t < p.T && m < MA)
-                            p.ep.keep4(t * MA + m, acc[a][b][4 * qq], acc[a][b][4 * qq + 1], acc[a][b][4 * qq + 2],
-                                       acc[a][b][4 * qq + 3]);
-                    }
-        } else if (p.ep.z != nullptr) {
-            quads([&](int a, int b, int qq, uint2* at) {
-                *at = make_uint2(pack_bf16x2(acc[a][b][4 * qq], acc[a][b][4 * qq + 1]),
-                                 pack_bf16x2(acc[a][b][4 * qq + 2], acc[a][b][4 * qq + 3]));
-            });
-            __syncthreads();
-            pieces([&](const uint4* at, int64_t g) {
-                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.ep.z) + g) = *at;
-            });
-            __syncthreads();
-        }
-        const bool res = p.ep.res != nullptr;
-        if (res) {
-            pieces([&](uint4* at, int64_t g) { *at = *reinterpret_cast<const uint4*>(p.ep.res + g); });
-            __syncthreads();
-        }
-        with_act(p.ep.act, [&](auto act) {
-            quads([&](int a, int b, int qq, uint2* at) {
-                float y[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) y[i] = act_value<decltype(act)::value>(acc[a][b][4 * qq + i]);
-                if (res) {
-                    const uint2 v = *at;
-                    y[0] += __uint_as_float(v.x << 16);
-                    y[1] += __uint_as_float(v.x & 0xFFFF0000u);
-                    y[2] += __uint_as_float(v.y << 16);
-                    y[3] += __uint_as_float(v.y & 0xFFFF0000u);
-                }
-                *at = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
-            });
-        });
-    } else {
-        quads([&](int a, int b, int qq, uint2* at) {
-            uint2 v;
-            v.x = pack_bf16x2(acc[a][b][4 * qq], acc[a][b][4 * qq + 1]);
-            v.y = pack_bf16x2(acc[a][b][4 * qq + 2], acc[a][b][4 * qq + 3]);
-            *at = v;
-        });
-    }
+            for (int qq = 0; qq < 4; ++qq) {
+                const int m = wa * MW + a * 32 + 8 * qq + 4 * (lane >> 5);
+                const int t = wt * TW + b * 32 + (lane & 31);
+                uint2 v;
+                v.x = pack_bf16x2(acc[a][b][4 * qq], acc[a][b][4 * qq + 1]);
+                v.y = pack_bf16x2(acc[a][b][4 * qq + 2], acc[a][b][4 * qq + 3]);
+                const int c = (m / 8) ^ (t % RPA % CPR);
+                *reinterpret_cast<uint2*>(out_row(t) + c * 16 + (m % 8) * 2) = v;
+            }
     __syncthreads();
-    pieces([&](const uint4* at, int64_t g) {
-        *reinterpret_cast<uint4*>((kGfwd ? p.gl[fl].out : p.out) + g) = *at;
-    });
+#pragma unroll
+    for (int i = 0; i < TT * CPR / NTHR; ++i) {
+        const int q = i * NTHR + tid;
+        const int t = q / CPR, c = q % CPR;
+        const int64_t gt = t0 + t, gm = m0 + 8 * c;
+        if (gt >= p.T || gm >= MA) continue;  // MA is a multiple of 8: a chunk is whole or outside
+        const uint4 v = *reinterpret_cast<const uint4*>(out_row(t) + (c ^ (t % RPA % CPR)) * 16);
+        *reinterpret_cast<uint4*>((kGfwd ? p.gl[fl].out : p.out) + gt * MA + gm) = v;
+    }
 }
 
 namespace {

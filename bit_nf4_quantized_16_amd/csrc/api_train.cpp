@@ -324,7 +324,7 @@ int qlora_distill_loss(const void* logits, int dtype, int64_t T, int64_t V, int6
     if ((s = check_dtype(top_dtype, "top_logits")) != QL_OK) return s;
     if (K < 1 || K > QL_DISTILL_MAX_TOP)
         return set_error(QL_ERR_SHAPE, "K = %lld outside [1, %d]", (long long)K, QL_DISTILL_MAX_TOP);
-    if (!(tau > 0.0f) || std::isinf(tau)) return set_error(QL_ERR_UNSUPPORTED, "tau = %g", (double)tau);
+    if (!(tau >= 0x1p-20f && tau <= 0x1p20f)) return set_error(QL_ERR_UNSUPPORTED, "tau = %g outside [2^-20, 2^20]", (double)tau);
     if (!(a >= 0.0f && a <= 1.0f)) return set_error(QL_ERR_UNSUPPORTED, "a = %g outside [0, 1]", (double)a);
     if (T == 0 || (loss == nullptr && dlogits == nullptr)) return QL_OK;
     if ((s = check_logits(logits, dtype)) != QL_OK) return s;

@@ -345,8 +345,10 @@ int grad_slices(int64_t V, bool f32) {
 // the row / tau:
 //   loss = (1 - a) tau^2 sum_k p_k (log p_k - log q_k) + a (lse(z) - z[label])
 //   dz   = w ((1 - a) tau (q - p) + a (softmax(z) - onehot))
-// A workgroup a row, the row in registers (NV pieces a thread) between its
-// sums and its gradient, so it is read once; NV = 0 reads a longer one again.
+// A workgroup takes a row at a time, the row in registers (NV pieces a thread)
+// between its sums and its gradient, so it is read once; NV = 0 reads a longer
+// one again. As a piece's gradient is written, the next row's piece is loaded
+// into its registers, so that the CU's memory works while its sums are formed.
 // The gradient is written without the p and the onehot first; then a thread
 // per teacher entry (and one for the label) writes its column's value with
 // everything that falls on this column, so that equal entries write equal
@@ -354,189 +356,285 @@ int grad_slices(int64_t V, bool f32) {
 // ---------------------------------------------------------------------------
 constexpr int kTop = QL_DISTILL_MAX_TOP;
 
-// BOTH: the row's softmax at temperature 1 besides the one at tau.
-template <bool F32, int NV, bool BOTH>
-__global__ __launch_bounds__(1024) void distill_kernel(DistillArgs p) {
+// Exponentials against the maximum m: 2^(z c - m c), one multiply-add. The
+// rounding of m c is the same for all and is taken off the logarithm of their
+// sum (delta). Past |m c| = 2^28 that rounding could be more than 16, but
+// then values next to each other are at least 32 apart in z c, so that only
+// those equal to m count: a power of two that brings m to 2^30 in c's place
+// gives them exactly 1 and the others 0.
+struct Scale {
+    float c, mc, delta;
+};
+__device__ __forceinline__ Scale scale_of(float m, float c) {
+    Scale s;
+    const float mc = m * c;
+    const bool far = !(fabsf(mc) <= 0x1p28f);
+    s.c = far ? __uint_as_float((284u - (__float_as_uint(m) >> 23 & 255u)) << 23) : c;
+    s.mc = far ? m * s.c : mc;
+    s.delta = far ? 0.0f : __builtin_fmaf(m, c, -mc);
+    return s;
+}
+__device__ __forceinline__ float exp_of(float z, const Scale& s) { return exp2_(__builtin_fmaf(z, s.c, -s.mc)); }
+
+// The larger of m and a piece's values. bf16 in the upper halves of words is
+// compared as it is, the lower value's bits behind it: exact after on_grid.
+// (+inf with bits behind it is a NaN, which a maximum passes over; the sum
+// then finds it.)
+template <bool F32>
+__device__ __forceinline__ float near_max(const Piece<F32>& v, float m) {
+    const uint32_t w[4] = {v.u.x, v.u.y, v.u.z, v.u.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        m = fmaxf(m, __uint_as_float(w[q]));
+        if constexpr (!F32) m = fmaxf(m, __uint_as_float(w[q] << 16));
+    }
+    return m;
+}
+template <bool F32>
+__device__ __forceinline__ float on_grid(float m) {
+    return F32 ? m : __uint_as_float(__float_as_uint(m) & 0xFFFF0000u);
+}
+
+// Keeps the compiler from holding a piece's values unpacked from one use to
+// the next, which takes twice the registers.
+template <bool F32>
+__device__ __forceinline__ void forget(Piece<F32>& v) {
+    if constexpr (!F32) asm volatile("" : "+v"(v.u.x), "+v"(v.u.y), "+v"(v.u.z), "+v"(v.u.w));
+}
+
+// What a thread has of a row besides its pieces.
+struct RowEnds {
+    RowShape sh;
+    bool on;   // the row counts
+    int edge;  // column of its edge value or -1
+    float ze;  // and the value
+    int k;     // column of its teacher entry (or the label's), or -1
+    float zk;  // the row's value there
+    float top; // the teacher's
+};
+
+// GRAD: the gradient too. BOTH: the row's softmax at temperature 1 besides the
+// one at tau.
+template <bool F32, int THREADS, int NV, bool GRAD, bool BOTH>
+__global__ __launch_bounds__(THREADS, NV == 16 || NV == 0 ? 4 : 6) void distill_kernel(DistillArgs p) {
     using P = Piece<F32>;
-    constexpr int E = P::E;
+    constexpr int E = P::E, WAVES = THREADS / 64, B = F32 ? 4 : 2;
     __shared__ float red[3][48];
     __shared__ float s_p[kTop + 1];
     __shared__ int s_k[kTop + 1];
-    const int tid = threadIdx.x, wave = tid >> 6, threads = blockDim.x, waves = threads >> 6;
-    const int64_t t = blockIdx.x, bytes = t * p.ld * (F32 ? 4 : 2);
-    const char* const row = static_cast<const char*>(p.z) + bytes;
-    char* const out = p.dz != nullptr ? static_cast<char*>(p.dz) + bytes : nullptr;
-    const RowShape sh = row_shape<F32>(row, p.V);
-    const int64_t body = sh.body - row;
-    const int edge = edge_column(sh, p.V, tid);
-    const int64_t label = p.labels != nullptr ? p.labels[t] : 0;
-    if (label < 0 || label >= p.V) {  // not counted
-        if (tid == 0 && p.loss != nullptr) p.loss[t] = 0.0f;
-        if (out != nullptr) {
-            if (edge >= 0) store_one<F32>(out, edge, 0.0f);
-            for (int c = tid; c < sh.pieces; c += threads)
-                *reinterpret_cast<uint4*>(out + body + 16 * static_cast<int64_t>(c)) = make_uint4(0, 0, 0, 0);
-        }
-        return;
-    }
+    const int tid = threadIdx.x, wave = tid >> 6;
+    const uint32_t mine = 16u * tid;
     const float ninf = -__builtin_inff();
     const float ct = kLog2e / p.tau;
+
+    auto begin_row = [&](int64_t t) {
+        RowEnds r;
+        const char* const row = static_cast<const char*>(p.z) + t * p.ld * B;
+        r.sh = row_shape<F32>(row, p.V);
+        const int64_t label = p.labels != nullptr ? p.labels[t] : 0;
+        r.on = label >= 0 && label < p.V;
+        r.edge = edge_column(r.sh, p.V, tid);
+        r.ze = ninf;
+        r.k = -1;
+        r.top = ninf;
+        r.zk = 0.0f;
+        if (r.on) {
+            if (r.edge >= 0) r.ze = load_one<F32>(row, r.edge);
+            if (tid < p.K) {
+                const int64_t at = p.index[t * p.K + tid];
+                if (at >= 0 && at < p.V) {
+                    r.k = static_cast<int>(at);
+                    r.top = p.top_f32 ? static_cast<const float*>(p.top)[t * p.K + tid]
+                                      : bf16_to_f32(static_cast<const uint16_t*>(p.top)[t * p.K + tid]);
+                }
+            } else if (tid == p.K && p.alpha > 0.0f) {
+                r.k = static_cast<int>(label);
+            }
+            if (r.k >= 0) r.zk = load_one<F32>(row, r.k);
+        }
+        return r;
+    };
+    // piece j of this thread: a base that is the same for all and 32 bits of its own
+    auto load_piece = [&](const RowEnds& r, int j) {
+        P u;
+        u.clear();
+        if (r.on && tid + j * THREADS < r.sh.pieces)
+            u.u = *reinterpret_cast<const uint4*>(r.sh.body + static_cast<int64_t>(j) * THREADS * 16 + mine);
+        return u;
+    };
+
+    int64_t t = blockIdx.x;
+    RowEnds cur = begin_row(t);
     P v[NV > 0 ? NV : 1];
     if constexpr (NV > 0) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            v[j].clear();
-            const int c = tid + j * threads;
-            if (c < sh.pieces) v[j].u = *reinterpret_cast<const uint4*>(sh.body + 16 * static_cast<int64_t>(c));
-        }
+        for (int j = 0; j < NV; ++j) v[j] = load_piece(cur, j);
     }
-    const float ze = edge >= 0 ? load_one<F32>(row, edge) : ninf;
-    // the teacher's entry of this thread; the thread after them has the label
-    float top = ninf, zk = 0.0f;
-    int k = -1;
-    if (tid < p.K) {
-        const int64_t at = p.index[t * p.K + tid];
-        if (at >= 0 && at < p.V) {
-            k = static_cast<int>(at);
-            top = p.top_f32 ? static_cast<const float*>(p.top)[t * p.K + tid]
-                            : bf16_to_f32(static_cast<const uint16_t*>(p.top)[t * p.K + tid]);
-        }
-    } else if (tid == p.K && p.alpha > 0.0f) {
-        k = static_cast<int>(label);
-    }
-    if (k >= 0) zk = load_one<F32>(row, k);
-
-    float mx[2] = {ze, top};
-    Running r1, rt;  // NV = 0: running sums
-    if constexpr (NV > 0) {
+    while (true) {
+        const int64_t tn = t + gridDim.x;
+        const bool more = tn < p.T;
+        float loss = 0.0f, ft = 0.0f, f1 = 0.0f, w = 0.0f;
+        Scale st{}, s1{};
+        if (cur.on) {
+            float mx[2] = {cur.ze, cur.top};
+            Running r1, rt;  // NV = 0: running sums
+            if constexpr (NV > 0) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+                for (int j = 0; j < NV; ++j) mx[0] = near_max(v[j], mx[0]);
+                mx[0] = on_grid<F32>(mx[0]);
 #pragma unroll
-            for (int i = 0; i < E; ++i) mx[0] = fmaxf(mx[0], v[j].at(i));
-    } else {
-        constexpr int U = 4;
-        for (int c0 = tid; c0 < sh.pieces; c0 += threads * U) {
-            P u[U];
+                for (int j = 0; j < NV; ++j) forget(v[j]);
+            } else {
+                constexpr int U = 4;
+                for (int c0 = 0; c0 * THREADS < cur.sh.pieces; c0 += U) {
+                    P u[U];
 #pragma unroll
-            for (int j = 0; j < U; ++j) {
-                u[j].clear();
-                const int c = c0 + j * threads;
-                if (c < sh.pieces) u[j].u = *reinterpret_cast<const uint4*>(sh.body + 16 * static_cast<int64_t>(c));
-            }
-            float m = ninf;
+                    for (int j = 0; j < U; ++j) u[j] = load_piece(cur, c0 + j);
+                    float m = ninf;
 #pragma unroll
-            for (int j = 0; j < U; ++j)
+                    for (int j = 0; j < U; ++j) m = near_max(u[j], m);
+                    m = on_grid<F32>(m);
+                    rescale(rt, m, ct);
+                    if constexpr (BOTH) rescale(r1, m, kLog2e);
+                    const Scale a = scale_of(reference(rt.m), ct), b = scale_of(reference(rt.m), kLog2e);
 #pragma unroll
-                for (int i = 0; i < E; ++i) m = fmaxf(m, u[j].at(i));
-            rescale(rt, m, ct);
-            rescale(r1, m, kLog2e);
-            const float ref = reference(rt.m);
+                    for (int j = 0; j < U; ++j)
 #pragma unroll
-            for (int j = 0; j < U; ++j)
-#pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    const float d = u[j].at(i) - ref;
-                    rt.s += exp2_(d * ct);
-                    if constexpr (BOTH) r1.s += exp2_(d * kLog2e);
+                        for (int i = 0; i < E; ++i) {
+                            rt.s += exp_of(u[j].at(i), a);
+                            if constexpr (BOTH) r1.s += exp_of(u[j].at(i), b);
+                        }
                 }
-        }
-        mx[0] = fmaxf(mx[0], rt.m);
-    }
-    block_reduce(mx, red[0], wave, waves, MaxOp{}, MaxOp{});
-    const float m = reference(mx[0]);
-    // sums: at tau, at 1, of the teacher's exponentials
-    float s[3] = {exp2_((ze - m) * ct), BOTH ? exp2_((ze - m) * kLog2e) : 0.0f, 0.0f};
-    const float lt = (top - reference(mx[1])) * ct;  // log2 of the unnormalised p
-    const float et = exp2_(lt);
-    s[2] = tid < p.K ? et : 0.0f;
-    if constexpr (NV > 0) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-            for (int i = 0; i < E; ++i) {
-                const float d = v[j].at(i) - m;
-                s[0] += exp2_(d * ct);
-                if constexpr (BOTH) s[1] += exp2_(d * kLog2e);
+                mx[0] = fmaxf(mx[0], rt.m);
             }
-    } else {
-        rescale(rt, mx[0], ct);
-        s[0] += rt.s;
-        if constexpr (BOTH) {
-            rescale(r1, mx[0], kLog2e);
-            s[1] += r1.s;
+            block_reduce(mx, red[0], wave, WAVES, MaxOp{}, MaxOp{});
+            const float m = reference(mx[0]);
+            st = scale_of(m, ct);
+            if constexpr (BOTH) s1 = scale_of(m, kLog2e);
+            // sums: at tau, at 1, of the teacher's exponentials
+            float s[3] = {exp_of(cur.ze, st), BOTH ? exp_of(cur.ze, s1) : 0.0f, 0.0f};
+            const float lt = (cur.top - reference(mx[1])) * ct;  // log2 of the unnormalised p
+            const float et = exp2_(lt);
+            s[2] = tid < p.K ? et : 0.0f;
+            if constexpr (NV > 0) {
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+#pragma unroll
+                    for (int i = 0; i < E; ++i) {
+                        s[0] += exp_of(v[j].at(i), st);
+                        if constexpr (BOTH) s[1] += exp_of(v[j].at(i), s1);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+#pragma unroll
+                for (int j = 0; j < NV; ++j) forget(v[j]);
+            } else {
+                // a thread's sums against its own maximum: their rounding, and m's
+                auto join = [&](Running& r, float c, const Scale& to) {
+                    const Scale own = scale_of(reference(r.m), c);
+                    return r.s == 0.0f ? 0.0f : r.s * exp2_((reference(r.m) - m) * c - own.delta + to.delta);
+                };
+                s[0] += join(rt, ct, st);
+                if constexpr (BOTH) s[1] += join(r1, kLog2e, s1);
+            }
+            block_reduce(s, red[1], wave, WAVES, AddOp{}, AddOp{}, AddOp{});
+            if constexpr (!BOTH) s[1] = s[0];  // tau = 1, or not used
+            if (!(s[0] < __builtin_inff())) s[0] = s[1] = __builtin_nanf("");  // an infinite logit
+            const float kl = s[2] != 0.0f ? (1.0f - p.alpha) * p.tau : 0.0f;  // no entry: no such term
+            // this thread's part of the loss, and what its column's gradient loses
+            float part[1] = {0.0f}, loses = 0.0f;
+            if (tid < p.K && et != 0.0f && kl != 0.0f) {
+                const float pk = et / s[2];
+                const float log_p = lt - __builtin_amdgcn_logf(s[2]);
+                const float log_q = (cur.zk - m) * ct - (__builtin_amdgcn_logf(s[0]) - st.delta);
+                part[0] = kl * p.tau * pk * ((log_p - log_q) * kLn2);
+                loses = kl * pk;
+            } else if (tid == p.K && cur.k >= 0) {
+                part[0] = p.alpha * (kLn2 * (__builtin_amdgcn_logf(s[1]) - (BOTH ? s1.delta : st.delta)) - (cur.zk - m));
+                loses = p.alpha;
+            }
+            if (GRAD && tid <= p.K) {
+                s_p[tid] = loses;
+                s_k[tid] = cur.k;
+            }
+            block_reduce(part, red[2], wave, WAVES, AddOp{});
+            loss = part[0];
+            if constexpr (GRAD) {
+                w = p.weight != nullptr ? p.weight[t] : 1.0f;
+                ft = w * (BOTH || p.alpha == 0.0f ? kl : kl + p.alpha) / s[0];
+                if constexpr (BOTH) f1 = w * p.alpha / s[1];
+            }
         }
-    }
-    block_reduce(s, red[1], wave, waves, AddOp{}, AddOp{}, AddOp{});
-    if constexpr (!BOTH) s[1] = s[0];  // tau = 1, or not used
-    const float kl = s[2] != 0.0f ? (1.0f - p.alpha) * p.tau : 0.0f;  // no entry: no such term
-    // this thread's part of the loss, and what its column's gradient loses
-    float part[1] = {0.0f}, loses = 0.0f;
-    if (tid < p.K && et != 0.0f && kl != 0.0f) {
-        const float pk = et / s[2];
-        const float log_p = lt - __builtin_amdgcn_logf(s[2]), log_q = (zk - m) * ct - __builtin_amdgcn_logf(s[0]);
-        part[0] = kl * p.tau * pk * ((log_p - log_q) * kLn2);
-        loses = kl * pk;
-    } else if (tid == p.K && k >= 0) {
-        part[0] = p.alpha * (kLn2 * __builtin_amdgcn_logf(s[1]) - (zk - m));
-        loses = p.alpha;
-    }
-    if (tid <= p.K) {
-        s_p[tid] = loses;
-        s_k[tid] = k;
-    }
-    block_reduce(part, red[2], wave, waves, AddOp{});
-    if (waves == 1) __syncthreads();
-    if (tid == 0 && p.loss != nullptr) p.loss[t] = part[0];
-    if (out == nullptr) return;
+        if (tid == 0 && p.loss != nullptr) p.loss[t] = loss;
 
-    const float w = p.weight != nullptr ? p.weight[t] : 1.0f;
-    const float ft = w * (BOTH || p.alpha == 0.0f ? kl : kl + p.alpha) / s[0], f1 = BOTH ? w * p.alpha / s[1] : 0.0f;
-    auto value = [&](float z) {
-        const float d = z - m;
-        float g = ft * exp2_(d * ct);
-        if constexpr (BOTH) g = __builtin_fmaf(f1, exp2_(d * kLog2e), g);
-        return g;
-    };
-    auto put = [&](const P& u, int c) {
-        float g[E];
+        RowEnds nxt = cur;
+        nxt.on = false;
+        if (more) nxt = begin_row(tn);
+        char* const out = GRAD ? static_cast<char*>(p.dz) + t * p.ld * B : nullptr;
+        char* const obody = GRAD ? out + (cur.sh.body - (static_cast<const char*>(p.z) + t * p.ld * B)) : nullptr;
+        auto value = [&](float z) {
+            float g = ft * exp_of(z, st);
+            if constexpr (BOTH) g = __builtin_fmaf(f1, exp_of(z, s1), g);
+            return g;
+        };
+        auto put = [&](const P& u, int j) {
+            if (tid + j * THREADS >= cur.sh.pieces) return;
+            uint4 o = make_uint4(0, 0, 0, 0);
+            if (cur.on) {
+                float g[E];
 #pragma unroll
-        for (int i = 0; i < E; ++i) g[i] = value(u.at(i));
-        *reinterpret_cast<uint4*>(out + body + 16 * static_cast<int64_t>(c)) = pack_piece<F32>(g);
-    };
-    if (edge >= 0) store_one<F32>(out, edge, value(ze));
-    if constexpr (NV > 0) {
+                for (int i = 0; i < E; ++i) g[i] = value(u.at(i));
+                o = pack_piece<F32>(g);
+            }
+            *reinterpret_cast<uint4*>(obody + static_cast<int64_t>(j) * THREADS * 16 + mine) = o;
+        };
+        if (GRAD && cur.edge >= 0) store_one<F32>(out, cur.edge, cur.on ? value(cur.ze) : 0.0f);
+        if constexpr (NV > 0) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = tid + j * threads;
-            if (c < sh.pieces) put(v[j], c);
+            for (int j = 0; j < NV; ++j) {
+                if constexpr (GRAD) put(v[j], j);
+                __builtin_amdgcn_sched_barrier(0);  // a piece at a time: few registers besides the row's
+                v[j] = load_piece(nxt, j);
+            }
+        } else if constexpr (GRAD) {
+            for (int j = 0; j * THREADS < cur.sh.pieces; ++j) put(load_piece(cur, j), j);
         }
-    } else {
-        for (int c = tid; c < sh.pieces; c += threads) {
-            P u;
-            u.u = *reinterpret_cast<const uint4*>(sh.body + 16 * static_cast<int64_t>(c));
-            put(u, c);
+        if constexpr (GRAD) {
+            __syncthreads();  // the row's values before its entries'
+            if (cur.on && cur.k >= 0) {
+                float sum = 0.0f;
+                for (int i = 0; i <= p.K; ++i) sum += s_k[i] == cur.k ? s_p[i] : 0.0f;
+                store_one<F32>(out, cur.k, __builtin_fmaf(-w, sum, value(cur.zk)));
+            }
         }
+        if (!more) return;
+        cur = nxt;
+        t = tn;
     }
-    __syncthreads();  // the row's values before its entries'
-    if (k >= 0) {
-        float sum = 0.0f;
-        for (int i = 0; i <= p.K; ++i) sum += s_k[i] == k ? s_p[i] : 0.0f;
-        store_one<F32>(out, k, __builtin_fmaf(-w, sum, value(zk)));
-    }
+}
+
+// Workgroups: as many as the chip holds, each the same number of rows.
+template <bool F32, int THREADS, int NV, bool BOTH>
+void launch_distill_as(const DistillArgs& a, hipStream_t stream) {
+    constexpr int per_cu = NV == 16 ? 1 : NV == 0 ? 2 : 6 * 4 / (THREADS / 64);
+    const int64_t rounds = ceil_div(a.T, 256 * per_cu);
+    const dim3 grid(static_cast<uint32_t>(ceil_div(a.T, rounds))), block(THREADS);
+    if (a.dz != nullptr)
+        hipLaunchKernelGGL((distill_kernel<F32, THREADS, NV, true, BOTH>), grid, block, 0, stream, a);
+    else
+        hipLaunchKernelGGL((distill_kernel<F32, THREADS, NV, false, BOTH>), grid, block, 0, stream, a);
 }
 
 template <bool F32, bool BOTH>
 void launch_distill_nv(const DistillArgs& a, hipStream_t stream) {
     const int64_t pieces = a.V / (F32 ? 4 : 8);
-    const int threads = pieces <= 1024 ? 512 : 1024;
-    const int64_t need = std::max<int64_t>(1, ceil_div(pieces, threads));
-    const dim3 grid(static_cast<uint32_t>(a.T)), block(threads);
-    if (need <= 1) hipLaunchKernelGGL((distill_kernel<F32, 1, BOTH>), grid, block, 0, stream, a);
-    else if (need <= 2) hipLaunchKernelGGL((distill_kernel<F32, 2, BOTH>), grid, block, 0, stream, a);
-    else if (need <= 4) hipLaunchKernelGGL((distill_kernel<F32, 4, BOTH>), grid, block, 0, stream, a);
-    else if (need <= 8) hipLaunchKernelGGL((distill_kernel<F32, 8, BOTH>), grid, block, 0, stream, a);
-    else if (need <= 16) hipLaunchKernelGGL((distill_kernel<F32, 16, BOTH>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((distill_kernel<F32, 0, BOTH>), grid, block, 0, stream, a);
+    if (pieces <= 256 && a.K < 256) launch_distill_as<F32, 256, 1, BOTH>(a, stream);
+    else if (pieces <= 1024 && a.K < 256) launch_distill_as<F32, 256, 4, BOTH>(a, stream);
+    else if (pieces <= 2048) launch_distill_as<F32, 512, 4, BOTH>(a, stream);
+    else if (pieces <= 4096) launch_distill_as<F32, 512, 8, BOTH>(a, stream);
+    else if (pieces <= 8192) launch_distill_as<F32, 1024, 8, BOTH>(a, stream);
+    else if (pieces <= 16384) launch_distill_as<F32, 1024, 16, BOTH>(a, stream);
+    else launch_distill_as<F32, 1024, 0, BOTH>(a, stream);
 }
 
 }  // namespace

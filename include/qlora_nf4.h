@@ -833,8 +833,8 @@ int qlora_norm_bwd(const void* X, int x_dtype, int64_t rows, int64_t cols, const
  * dlogits may each be NULL.
  *
  * Errors: QL_ERR_NULL, QL_ERR_SHAPE, QL_ERR_UNSUPPORTED (dtypes; beta not
- * positive and finite, label_smoothing outside [0, 1], kind, average; tau not
- * positive and finite, a outside [0, 1]), QL_ERR_ALIGN, QL_ERR_WORKSPACE,
+ * positive and finite, label_smoothing outside [0, 1], kind, average; tau
+ * outside [2^-20, 2^20], a outside [0, 1]), QL_ERR_ALIGN, QL_ERR_WORKSPACE,
  * QL_ERR_HIP.
  */
 #define QL_PREF_SIGMOID 0

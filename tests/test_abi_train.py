@@ -117,7 +117,7 @@ def test_distill(lib, L):
         return lib.qlora_distill_loss(z, dt, T, V, ld, idx, top, td, K, labels, tau, a, w, loss, dz, None)
 
     _each(call, L, **_and(LOGITS, QL_ERR_SHAPE=[dict(K=0), dict(K=257), dict(K=-1)],
-                          QL_ERR_UNSUPPORTED=[dict(td=4), dict(tau=0.0), dict(tau=-1.0), dict(tau=INF), dict(tau=NAN),
+                          QL_ERR_UNSUPPORTED=[dict(td=4), dict(tau=0.0), dict(tau=-1.0), dict(tau=INF), dict(tau=NAN), dict(tau=2.0 ** 21),
                                               dict(a=-0.1), dict(a=1.1), dict(a=NAN)],
                           QL_ERR_NULL=[dict(idx=None), dict(top=None)],
                           QL_ERR_ALIGN=[dict(idx=MIS), dict(top=0x10002), dict(w=ODD), dict(loss=ODD), dict(dz=P + 2),

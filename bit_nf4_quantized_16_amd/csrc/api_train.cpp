@@ -239,7 +239,6 @@ int qlora_preference_loss_fwd(const void* logits, int dtype, int64_t T, int64_t 
     if (T > 0) {
         if ((s = check_logits(logits, dtype)) != QL_OK) return s;
         if ((s = check_array(labels, "labels", 8)) != QL_OK) return s;
-        if ((s = check_array(logp, "logp", 4)) != QL_OK) return s;
         if ((s = check_array(state, "state", 4)) != QL_OK) return s;
         if ((s = check_ws(ws, ws_bytes, logp_ws_bytes(T, V, dtype == QL_F32))) != QL_OK) return s;
     }
@@ -249,38 +248,42 @@ int qlora_preference_loss_fwd(const void* logits, int dtype, int64_t T, int64_t 
         if ((s = check_array(loss, "loss", 4)) != QL_OK) return s;
         if ((s = check_array(seq_logp, "seq_logp", 4)) != QL_OK) return s;
     }
+    if (T > 0 && (s = check_array(logp, "logp", 4)) != QL_OK) return s;
     float* const dlogp = state + 2 * T;
     int* const pair = reinterpret_cast<int*>(state + 3 * T);
-    if (T > 0) {
-        LogpArgs a{};
-        a.z = logits;
-        a.f32 = dtype == QL_F32;
-        a.T = T;
-        a.ld = ld;
-        a.V = static_cast<int>(V);
-        a.labels = labels;
-        a.logp = logp;
-        a.ref = state;
-        a.inv = state + T;
-        a.dlogp = dlogp;
-        a.pair = pair;
-        a.part = static_cast<float*>(ws);
-        if ((s = launch_logp(a, static_cast<hipStream_t>(stream))) != QL_OK) return s;
-    }
+    LogpArgs a{};
+    a.z = logits;
+    a.f32 = dtype == QL_F32;
+    a.T = T;
+    a.ld = ld;
+    a.V = static_cast<int>(V);
+    a.labels = labels;
+    a.dlogp = dlogp;
+    a.pair = pair;
+    a.pair_logp = logp;
+    a.part = static_cast<float*>(ws);
+    if (T > 0 && (s = launch_logp(a, static_cast<hipStream_t>(stream))) != QL_OK) return s;
     if (pairs == 0) return QL_OK;
     PairArgs q{};
-    q.start = seq_start;
-    q.labels = labels;
-    q.logp = logp;
-    q.ref = ref_logp;
+    q.z = logits;
+    q.f32 = a.f32;
     q.T = T;
-    q.V = static_cast<int>(V);
+    q.ld = ld;
+    q.V = a.V;
+    q.labels = labels;
+    q.part = a.part;
+    q.runs = a.runs;
+    q.start = seq_start;
+    q.ref_logp = ref_logp;
     q.beta = beta;
     q.smooth = label_smoothing;
     q.kind = kind;
     q.average = average;
     q.loss = loss;
     q.seq_logp = seq_logp;
+    q.logp = logp;
+    q.ref = state;
+    q.inv = state + T;
     q.dlogp = dlogp;
     q.pair = pair;
     return launch_pairs(q, static_cast<int>(pairs), static_cast<hipStream_t>(stream));

@@ -341,39 +341,45 @@ int launch_norm_bwd(const NormArgs& a, hipStream_t stream);
 void launch_column_sums(const float* part, int64_t parts, int64_t C, float* out0, float* out1, int accumulate,
                         hipStream_t stream);
 
-// Log probabilities of labels: logp[t] = z[t][labels[t]] - lse(z[t]), 0 where
-// the label is outside [0, V). z [T, V] (row stride ld), bf16 or fp32.
+// Each row's maximum and sum of exponentials, in runs: part [T][runs] pairs
+// (none for rows whose label is outside [0, V)); with logp also
+// logp[t] = z[t][labels[t]] - lse(z[t]), 0 for those rows. z [T, V] (row
+// stride ld), bf16 or fp32.
 struct LogpArgs {
     const void* z;
     int f32;
     int64_t T, ld;
     int V;
     const int64_t* labels;
-    float* logp;
-    // for the gradient, null without: softmax = 2^((z - ref) log2 e) inv; and
-    // dlogp, pair of rows in no sequence (zeros)
-    float* ref;
-    float* inv;
-    float* dlogp;
+    float* logp;  // null: the runs alone
+    float* dlogp;  // null, or zeroed for every row, and with it
     int* pair;
+    float* pair_logp;
     float* part;  // logp_ws_bytes
-    int slices;   // set by the launcher
+    int runs;     // set by the launcher
 };
 size_t logp_ws_bytes(int64_t T, int64_t V, bool f32);
-int launch_logp(LogpArgs a, hipStream_t stream);
+int launch_logp(LogpArgs& a, hipStream_t stream);
 
 struct PairArgs {
-    const int64_t* start;  // [2 pairs + 1]
-    const int64_t* labels;
-    const float* logp;
-    const float* ref;  // [2 pairs]
-    int64_t T;
+    const void* z;
+    int f32;
+    int64_t T, ld;
     int V;
+    const int64_t* labels;
+    const float* part;  // the rows' runs
+    int runs;
+    const int64_t* start;   // [2 pairs + 1]
+    const float* ref_logp;  // [2 pairs]
     float beta, smooth;
     int kind, average;
     float* loss;      // [pairs]
     float* seq_logp;  // [2 pairs]
-    float* dlogp;     // [T]
+    float* logp;      // [T], the rows of sequences
+    // for the gradient: softmax = 2^((z - ref) log2 e) inv
+    float* ref;
+    float* inv;
+    float* dlogp;
     int* pair;
 };
 int launch_pairs(const PairArgs& a, int pairs, hipStream_t stream);

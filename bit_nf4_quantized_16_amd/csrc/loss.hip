@@ -98,264 +98,6 @@ __device__ __forceinline__ void rescale(Running& r, float m, float c) {
     }
 }
 
-// ---------------------------------------------------------------------------
-// Preference loss. Rows of the logits are tokens, sequences are runs of rows,
-// pairs are neighbouring sequences.
-//   l_t = z_t[label] - lse(z_t)       a launch over rows (and slices of them)
-//   L_s, the loss and dloss / dl_t    a workgroup per pair
-//   dz_t = dloss dl_t (onehot - softmax)   a launch over rows
-// ---------------------------------------------------------------------------
-constexpr int kStatThreads = 256, kStatUnroll = 4;
-
-// From the label's logit, the reference and the sum: the log probability, and
-// what the gradient takes softmax from (not their sum, the row's log-sum-exp,
-// whose rounding would cost softmax half a unit in the last place of it).
-__device__ __forceinline__ void finish_row(const LogpArgs& p, int64_t t, float z, float ref, float s) {
-    p.logp[t] = (z - ref) - kLn2 * __builtin_amdgcn_logf(s);
-    if (p.ref == nullptr) return;
-    p.ref[t] = ref;
-    p.inv[t] = 1.0f / s;
-}
-
-template <bool F32>
-__global__ __launch_bounds__(kStatThreads) void logp_kernel(LogpArgs p) {
-    using P = Piece<F32>;
-    constexpr int E = P::E;
-    __shared__ float red[2][16];
-    const int tid = threadIdx.x, wave = tid >> 6;
-    const int64_t t = blockIdx.x / p.slices;
-    const int slice = static_cast<int>(blockIdx.x - t * p.slices);
-    const int64_t label = p.labels[t];
-    if (tid == 0 && slice == 0 && p.dlogp != nullptr) {
-        p.dlogp[t] = 0.0f;  // until its pair says otherwise
-        p.pair[t] = 0;
-    }
-    if (label < 0 || label >= p.V) {
-        if (tid == 0 && slice == 0) p.logp[t] = 0.0f;
-        return;
-    }
-    const char* const row = static_cast<const char*>(p.z) + t * p.ld * (F32 ? 4 : 2);
-    const RowShape sh = row_shape<F32>(row, p.V);
-    const int per = (sh.pieces + p.slices - 1) / p.slices;
-    const int first = slice * per, last = min(first + per, sh.pieces);
-    Running r;
-    const int edge = slice == 0 ? edge_column(sh, p.V, tid) : -1;
-    if (edge >= 0) {
-        r.m = load_one<F32>(row, edge);
-        r.s = exp2_((r.m - reference(r.m)) * kLog2e);
-    }
-    for (int c0 = first + tid; c0 < last; c0 += kStatThreads * kStatUnroll) {
-        P v[kStatUnroll];
-#pragma unroll
-        for (int j = 0; j < kStatUnroll; ++j) {
-            v[j].clear();
-            const int c = c0 + j * kStatThreads;
-            if (c < last) v[j].u = *reinterpret_cast<const uint4*>(sh.body + 16 * static_cast<int64_t>(c));
-        }
-        float m = -__builtin_inff();
-#pragma unroll
-        for (int j = 0; j < kStatUnroll; ++j)
-#pragma unroll
-            for (int i = 0; i < E; ++i) m = fmaxf(m, v[j].at(i));
-        rescale(r, m, kLog2e);
-        const float ref = reference(r.m);
-#pragma unroll
-        for (int j = 0; j < kStatUnroll; ++j)
-#pragma unroll
-            for (int i = 0; i < E; ++i) r.s += exp2_((v[j].at(i) - ref) * kLog2e);
-    }
-    float m[1] = {r.m};
-    block_reduce(m, red[0], wave, kStatThreads / 64, MaxOp{});
-    rescale(r, m[0], kLog2e);
-    float s[1] = {r.s};
-    block_reduce(s, red[1], wave, kStatThreads / 64, AddOp{});
-    if (tid != 0) return;
-    if (p.slices > 1) {
-        p.part[2 * (t * p.slices + slice)] = m[0];
-        p.part[2 * (t * p.slices + slice) + 1] = s[0];
-        return;
-    }
-    finish_row(p, t, load_one<F32>(row, label), reference(m[0]), s[0]);
-}
-
-// The slices of a row joined, a thread a row.
-template <bool F32>
-__global__ __launch_bounds__(256) void logp_join_kernel(LogpArgs p) {
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (t >= p.T) return;
-    const int64_t label = p.labels[t];
-    if (label < 0 || label >= p.V) return;  // written already
-    Running r;
-    for (int i = 0; i < p.slices; ++i) r.m = fmaxf(r.m, p.part[2 * (t * p.slices + i)]);
-    const float ref = reference(r.m);
-    for (int i = 0; i < p.slices; ++i) {
-        const float m = p.part[2 * (t * p.slices + i)], s = p.part[2 * (t * p.slices + i) + 1];
-        r.s += s == 0.0f ? 0.0f : s * exp2_((m - ref) * kLog2e);
-    }
-    finish_row(p, t, load_one<F32>(static_cast<const char*>(p.z) + t * p.ld * (F32 ? 4 : 2), label), ref, r.s);
-}
-
-constexpr int kPairThreads = 1024;
-
-// log(1 + e^-|x|) and the two logistic values in 64 bits: one thread a pair.
-__device__ void pair_loss(const PairArgs& p, double d, double& loss, double& slope) {
-    const double x = p.beta * d;
-    if (p.kind == QL_PREF_SIGMOID) {
-        const double e = exp(-fabs(x)), soft = log1p(e);
-        const double lo = e / (1.0 + e), hi = 1.0 / (1.0 + e);  // sigmoid(-|x|), sigmoid(|x|)
-        const double up = x >= 0 ? hi : lo, down = x >= 0 ? lo : hi;  // sigmoid(x), sigmoid(-x)
-        // -log sigmoid(x) = soft + max(-x, 0)
-        loss = (1.0 - p.smooth) * (soft + fmax(-x, 0.0)) + (p.smooth > 0.0f ? p.smooth * (soft + fmax(x, 0.0)) : 0.0);
-        slope = p.beta * (p.smooth * up - (1.0 - p.smooth) * down);
-        if (x != x) loss = slope = x;
-    } else if (p.kind == QL_PREF_HINGE) {
-        loss = x < 1.0 ? 1.0 - x : (x != x ? x : 0.0);
-        slope = x < 1.0 ? -static_cast<double>(p.beta) : (x != x ? x : 0.0);
-    } else {
-        const double e = d - 0.5 / p.beta;
-        loss = e * e;
-        slope = 2.0 * e;
-    }
-}
-
-__global__ __launch_bounds__(kPairThreads) void pair_kernel(PairArgs p) {
-    __shared__ double sums[2][kPairThreads / 64];
-    __shared__ int64_t counts[2][kPairThreads / 64];
-    __shared__ float slopes[2];
-    const int tid = threadIdx.x, wave = tid >> 6, pair = blockIdx.x;
-    int64_t at[3];
-    for (int i = 0; i < 3; ++i) {
-        const int64_t a = p.start[2 * pair + i];
-        at[i] = a < 0 ? 0 : (a > p.T ? p.T : a);
-    }
-    for (int q = 0; q < 2; ++q) {
-        double s = 0.0;
-        int64_t n = 0;
-        for (int64_t t = at[q] + tid; t < at[q + 1]; t += kPairThreads) {
-            const int64_t label = p.labels[t];
-            if (label < 0 || label >= p.V) continue;
-            s += p.logp[t];
-            ++n;
-        }
-        for (int d = 32; d > 0; d >>= 1) {
-            s += __shfl_xor(s, d);
-            n += __shfl_xor(n, d);
-        }
-        if ((tid & 63) == 0) {
-            sums[q][wave] = s;
-            counts[q][wave] = n;
-        }
-    }
-    __syncthreads();
-    if (tid == 0) {
-        double L[2], per[2];
-        for (int q = 0; q < 2; ++q) {
-            double s = 0.0;
-            int64_t n = 0;
-            for (int w = 0; w < kPairThreads / 64; ++w) {
-                s += sums[q][w];
-                n += counts[q][w];
-            }
-            per[q] = p.average && n > 0 ? 1.0 / static_cast<double>(n) : 1.0;
-            L[q] = s * per[q];
-            p.seq_logp[2 * pair + q] = static_cast<float>(L[q]);
-        }
-        double loss, slope;
-        pair_loss(p, (L[0] - p.ref[2 * pair]) - (L[1] - p.ref[2 * pair + 1]), loss, slope);
-        p.loss[pair] = static_cast<float>(loss);
-        slopes[0] = static_cast<float>(slope * per[0]);
-        slopes[1] = static_cast<float>(-slope * per[1]);
-    }
-    __syncthreads();
-    for (int q = 0; q < 2; ++q)
-        for (int64_t t = at[q] + tid; t < at[q + 1]; t += kPairThreads) {
-            const int64_t label = p.labels[t];
-            if (label < 0 || label >= p.V) continue;
-            p.dlogp[t] = slopes[q];
-            p.pair[t] = pair;
-        }
-}
-
-// dz = f (onehot - softmax), f = dloss dlogp; a row that counts nothing is
-// written as zeros without being read.
-constexpr int kGradThreads = 256, kGradUnroll = 4;
-
-template <bool F32>
-__global__ __launch_bounds__(kGradThreads) void logp_grad_kernel(LogpGradArgs p) {
-    using P = Piece<F32>;
-    constexpr int E = P::E;
-    const int tid = threadIdx.x;
-    const int64_t t = blockIdx.x / p.slices;
-    const int slice = static_cast<int>(blockIdx.x - t * p.slices);
-    const int64_t bytes = t * p.ld * (F32 ? 4 : 2);
-    const char* const row = static_cast<const char*>(p.z) + bytes;
-    char* const out = static_cast<char*>(p.dz) + bytes;
-    const int64_t label = p.labels[t];
-    const bool on = label >= 0 && label < p.V && p.pairs > 0;
-    const float f = on ? p.dlogp[t] * p.dloss[p.pair[t]] : 0.0f;
-    const float ref = on ? p.ref[t] : 0.0f, fq = on ? -f * p.inv[t] : 0.0f;
-    const RowShape sh = row_shape<F32>(out, p.V);
-    const int64_t body = sh.body - out;
-    const int per = (sh.pieces + p.slices - 1) / p.slices;
-    const int first = slice * per, last = min(first + per, sh.pieces);
-    const int edge = slice == 0 ? edge_column(sh, p.V, tid) : -1;
-    auto value = [&](float z, int col) {
-        return __builtin_fmaf(fq, exp2_((z - ref) * kLog2e), col == label ? f : 0.0f);
-    };
-    const bool zero = !on || f == 0.0f;
-    if (edge >= 0) store_one<F32>(out, edge, zero ? 0.0f : value(load_one<F32>(row, edge), edge));
-    for (int c0 = first + tid; c0 < last; c0 += kGradThreads * kGradUnroll) {
-        P v[kGradUnroll];
-        if (!zero) {
-#pragma unroll
-            for (int j = 0; j < kGradUnroll; ++j) {
-                const int c = c0 + j * kGradThreads;
-                if (c < last) v[j].u = *reinterpret_cast<const uint4*>(row + body + 16 * static_cast<int64_t>(c));
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < kGradUnroll; ++j) {
-            const int c = c0 + j * kGradThreads;
-            if (c >= last) continue;
-            uint4 o = make_uint4(0, 0, 0, 0);
-            if (!zero) {
-                float g[E];
-#pragma unroll
-                for (int i = 0; i < E; ++i) g[i] = value(v[j].at(i), sh.head + c * E + i);
-                o = pack_piece<F32>(g);
-            }
-            *reinterpret_cast<uint4*>(out + body + 16 * static_cast<int64_t>(c)) = o;
-        }
-    }
-}
-
-// Slices of a row where there are few rows.
-int logp_slices(int64_t T, int64_t V, bool f32) {
-    const int64_t pieces = V / (f32 ? 4 : 8);
-    const int64_t most = std::max<int64_t>(1, pieces / (kStatThreads * 2));
-    return static_cast<int>(std::min(most, std::max<int64_t>(1, 512 / std::max<int64_t>(T, 1))));
-}
-int grad_slices(int64_t V, bool f32) {
-    const int64_t pieces = V / (f32 ? 4 : 8);
-    return static_cast<int>(std::max<int64_t>(1, pieces / (kGradThreads * kGradUnroll)));
-}
-
-// ---------------------------------------------------------------------------
-// Distillation. p = softmax over the teacher's K logits / tau, q = softmax of
-// the row / tau:
-//   loss = (1 - a) tau^2 sum_k p_k (log p_k - log q_k) + a (lse(z) - z[label])
-//   dz   = w ((1 - a) tau (q - p) + a (softmax(z) - onehot))
-// A workgroup takes a row at a time, the row in registers (NV pieces a thread)
-// between its sums and its gradient, so it is read once; NV = 0 reads a longer
-// one again. As a piece's gradient is written, the next row's piece is loaded
-// into its registers, so that the CU's memory works while its sums are formed.
-// The gradient is written without the p and the onehot first; then a thread
-// per teacher entry (and one for the label) writes its column's value with
-// everything that falls on this column, so that equal entries write equal
-// values.
-// ---------------------------------------------------------------------------
-constexpr int kTop = QL_DISTILL_MAX_TOP;
-
 // Exponentials against the maximum m: 2^(z c - m c), one multiply-add. The
 // rounding of m c is the same for all and is taken off the logarithm of their
 // sum (delta). Past |m c| = 2^28 that rounding could be more than 16, but
@@ -376,24 +118,271 @@ __device__ __forceinline__ Scale scale_of(float m, float c) {
 }
 __device__ __forceinline__ float exp_of(float z, const Scale& s) { return exp2_(__builtin_fmaf(z, s.c, -s.mc)); }
 
-// The larger of m and a piece's values. bf16 in the upper halves of words is
-// compared as it is, the lower value's bits behind it: exact after on_grid.
-// (+inf with bits behind it is a NaN, which a maximum passes over; the sum
-// then finds it.)
+// The largest of m and a piece's values.
 template <bool F32>
-__device__ __forceinline__ float near_max(const Piece<F32>& v, float m) {
-    const uint32_t w[4] = {v.u.x, v.u.y, v.u.z, v.u.w};
+__device__ __forceinline__ float piece_max(const Piece<F32>& v, float m) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        m = fmaxf(m, __uint_as_float(w[q]));
-        if constexpr (!F32) m = fmaxf(m, __uint_as_float(w[q] << 16));
-    }
+    for (int i = 0; i < Piece<F32>::E; ++i) m = fmaxf(m, v.at(i));
     return m;
 }
+
+// ---------------------------------------------------------------------------
+// Preference loss. Rows of the logits are tokens, sequences are runs of rows,
+// pairs are neighbouring sequences.
+//   l_t = z_t[label] - lse(z_t)       a wave per 512 pieces of a row
+//   L_s, the loss and dloss / dl_t    a workgroup per pair
+//   dz_t = dloss dl_t (onehot - softmax)   workgroups of 1024 pieces of a row
+// A pair's sums must be known before any of its gradient, so the logits are
+// read twice. The second pass takes the rows from the last to the first, which
+// the first pass has left in the last-level cache.
+// ---------------------------------------------------------------------------
+constexpr int kLogpThreads = 256, kLogpPieces = 8;  // pieces a lane
+constexpr int kLogpRun = 64 * kLogpPieces;          // and a wave
+
+// Maximum and sum of 2^((z - m) log2 e) of a row's runs of pieces, a wave
+// each, all its loads in flight at once; no wave waits for another. (A row a
+// workgroup of 256, two barriers: 45.8 us for 2450 rows of 32000, 1.2 rounds of
+// the chip.)
 template <bool F32>
-__device__ __forceinline__ float on_grid(float m) {
-    return F32 ? m : __uint_as_float(__float_as_uint(m) & 0xFFFF0000u);
+__global__ __launch_bounds__(kLogpThreads) void logp_kernel(LogpArgs p) {
+    using P = Piece<F32>;
+    constexpr int E = P::E;
+    const int lane = threadIdx.x & 63;
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kLogpThreads / 64) + (threadIdx.x >> 6);
+    const int64_t t = unit / p.runs;
+    if (t >= p.T) return;
+    const int run = static_cast<int>(unit - t * p.runs);
+    const int64_t label = p.labels[t];
+    if (run == 0 && lane == 0 && p.dlogp != nullptr) {
+        p.dlogp[t] = 0.0f;  // until its pair says otherwise
+        p.pair[t] = 0;
+        p.pair_logp[t] = 0.0f;
+    }
+    if (label < 0 || label >= p.V) return;
+    const char* const row = static_cast<const char*>(p.z) + t * p.ld * (F32 ? 4 : 2);
+    const RowShape sh = row_shape<F32>(row, p.V);
+    const int first = run * kLogpRun + lane;
+    P v[kLogpPieces];
+#pragma unroll
+    for (int j = 0; j < kLogpPieces; ++j) {
+        v[j].clear();
+        const int c = first + 64 * j;
+        if (c < sh.pieces) v[j].u = *reinterpret_cast<const uint4*>(sh.body + 16 * static_cast<int64_t>(c));
+    }
+    float m = -__builtin_inff();
+    const int edge = run == 0 ? edge_column(sh, p.V, lane) : -1;
+    const float ze = edge >= 0 ? load_one<F32>(row, edge) : m;
+#pragma unroll
+    for (int j = 0; j < kLogpPieces; ++j) m = piece_max(v[j], m);
+    m = wave_reduce(fmaxf(m, ze), MaxOp{});
+    const Scale sc = scale_of(reference(m), kLog2e);
+    float s = exp_of(ze, sc);
+#pragma unroll
+    for (int j = 0; j < kLogpPieces; ++j)
+#pragma unroll
+        for (int i = 0; i < E; ++i) s += exp_of(v[j].at(i), sc);
+    s = wave_reduce(s, AddOp{});
+    // of the exact argument: the scale's rounding off
+    if (lane == 0) reinterpret_cast<float2*>(p.part)[unit] = make_float2(m, s * exp2_(-sc.delta));
 }
+
+// A row's runs joined: what exponentials are taken against, their sum.
+__device__ __forceinline__ float2 join_runs(const float* part, int runs, int64_t t) {
+    const float2* const v = reinterpret_cast<const float2*>(part) + t * runs;
+    float m = -__builtin_inff(), s = 0.0f;
+    for (int i = 0; i < runs; ++i) m = fmaxf(m, v[i].x);
+    m = reference(m);
+    for (int i = 0; i < runs; ++i) s += v[i].y == 0.0f ? 0.0f : v[i].y * exp2_((v[i].x - m) * kLog2e);
+    return make_float2(m, s < __builtin_inff() ? s : __builtin_nanf(""));
+}
+__device__ __forceinline__ float label_logit(const void* z, int f32, int64_t at) {
+    return f32 ? static_cast<const float*>(z)[at] : bf16_to_f32(static_cast<const uint16_t*>(z)[at]);
+}
+
+__global__ __launch_bounds__(256) void logp_join_kernel(LogpArgs p) {
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (t >= p.T) return;
+    const int64_t label = p.labels[t];
+    float l = 0.0f;
+    if (label >= 0 && label < p.V) {
+        const float z = label_logit(p.z, p.f32, t * p.ld + label);
+        const float2 r = join_runs(p.part, p.runs, t);
+        l = (z - r.x) - kLn2 * __builtin_amdgcn_logf(r.y);
+    }
+    p.logp[t] = l;
+}
+
+constexpr int kPairThreads = 1024;
+
+// The loss of x = beta d and dloss / dd.
+__device__ __forceinline__ void pair_loss(const PairArgs& p, double d, float& loss, double& slope) {
+    const double x = p.beta * d;
+    if (p.kind == QL_PREF_SIGMOID) {
+        // with e = e^-|x|: -log sigmoid(x) = log1p(e) + max(-x, 0), sigmoid(-|x|) = e / (1 + e)
+        const float xf = static_cast<float>(x), e = expf(-fabsf(xf)), soft = log1pf(e);
+        const float lo = e / (1.0f + e), hi = 1.0f / (1.0f + e);
+        const float up = xf >= 0 ? hi : lo, down = xf >= 0 ? lo : hi;  // sigmoid(x), sigmoid(-x)
+        loss = (1.0f - p.smooth) * (soft + fmaxf(-xf, 0.0f)) + (p.smooth > 0.0f ? p.smooth * (soft + fmaxf(xf, 0.0f)) : 0.0f);
+        slope = p.beta * (p.smooth * up - (1.0f - p.smooth) * down);
+        if (xf != xf) loss = xf, slope = x;
+    } else if (p.kind == QL_PREF_HINGE) {
+        loss = static_cast<float>(x < 1.0 ? 1.0 - x : (x != x ? x : 0.0));
+        slope = x < 1.0 ? -static_cast<double>(p.beta) : (x != x ? x : 0.0);
+    } else {
+        const double e = d - 0.5 / p.beta;
+        loss = static_cast<float>(e * e);
+        slope = 2.0 * e;
+    }
+}
+
+// Joins its rows' runs (their log probabilities, references and sums are kept
+// for the caller and the gradient), sums them, and hands each row its share of
+// the loss's slope.
+__global__ __launch_bounds__(kPairThreads) void pair_kernel(PairArgs p) {
+    __shared__ double sums[2][kPairThreads / 64];
+    __shared__ int counts[2][kPairThreads / 64];
+    __shared__ float slopes[2];
+    const int tid = threadIdx.x, wave = tid >> 6, pair = blockIdx.x;
+    int64_t at[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const int64_t a = p.start[2 * pair + i];
+        at[i] = a < 0 ? 0 : (a > p.T ? p.T : a);
+    }
+    const float ref0 = p.ref_logp[2 * pair], ref1 = p.ref_logp[2 * pair + 1];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        double s = 0.0;
+        int n = 0;
+        for (int64_t t = at[q] + tid; t < at[q + 1]; t += kPairThreads) {
+            const int64_t label = p.labels[t];
+            float l = 0.0f;
+            if (label >= 0 && label < p.V) {
+                const float z = label_logit(p.z, p.f32, t * p.ld + label);
+                const float2 r = join_runs(p.part, p.runs, t);
+                l = (z - r.x) - kLn2 * __builtin_amdgcn_logf(r.y);
+                p.ref[t] = r.x;
+                p.inv[t] = 1.0f / r.y;
+                ++n;
+            }
+            p.logp[t] = l;
+            s += l;
+        }
+        for (int d = 32; d > 0; d >>= 1) {
+            s += __shfl_xor(s, d);
+            n += __shfl_xor(n, d);
+        }
+        if ((tid & 63) == 0) {
+            sums[q][wave] = s;
+            counts[q][wave] = n;
+        }
+    }
+    __syncthreads();
+    if (tid == 0) {
+        double L[2], per[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            double s = 0.0;
+            int n = 0;
+            for (int w = 0; w < kPairThreads / 64; ++w) {
+                s += sums[q][w];
+                n += counts[q][w];
+            }
+            per[q] = p.average && n > 0 ? 1.0 / static_cast<double>(n) : 1.0;
+            L[q] = s * per[q];
+            p.seq_logp[2 * pair + q] = static_cast<float>(L[q]);
+        }
+        float loss;
+        double slope;
+        pair_loss(p, (L[0] - ref0) - (L[1] - ref1), loss, slope);
+        p.loss[pair] = loss;
+        slopes[0] = static_cast<float>(slope * per[0]);
+        slopes[1] = static_cast<float>(-slope * per[1]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+        for (int64_t t = at[q] + tid; t < at[q + 1]; t += kPairThreads) {
+            const int64_t label = p.labels[t];
+            if (label < 0 || label >= p.V) continue;
+            p.dlogp[t] = slopes[q];
+            p.pair[t] = pair;
+        }
+}
+
+// dz = f (onehot - softmax), f = dloss dlogp; a row that counts nothing is
+// written as zeros without being read.
+constexpr int kGradThreads = 256, kGradUnroll = 4;
+
+template <bool F32>
+__global__ __launch_bounds__(kGradThreads) void logp_grad_kernel(LogpGradArgs p) {
+    using P = Piece<F32>;
+    constexpr int E = P::E;
+    const int tid = threadIdx.x;
+    const int64_t back = blockIdx.x / p.slices, t = p.T - 1 - back;
+    const int slice = static_cast<int>(blockIdx.x - back * p.slices);
+    const int64_t bytes = t * p.ld * (F32 ? 4 : 2);
+    const char* const row = static_cast<const char*>(p.z) + bytes;
+    char* const out = static_cast<char*>(p.dz) + bytes;
+    const int64_t label = p.labels[t];
+    const bool on = label >= 0 && label < p.V && p.pairs > 0;
+    const RowShape sh = row_shape<F32>(out, p.V);
+    const int64_t body = sh.body - out;
+    const int first = slice * kGradThreads * kGradUnroll + tid;
+    const int edge = slice == 0 ? edge_column(sh, p.V, tid) : -1;
+    P v[kGradUnroll];
+    float ze = 0.0f;
+    if (on) {
+#pragma unroll
+        for (int j = 0; j < kGradUnroll; ++j) {
+            const int c = first + j * kGradThreads;
+            if (c < sh.pieces) v[j].u = *reinterpret_cast<const uint4*>(row + body + 16 * static_cast<int64_t>(c));
+        }
+        if (edge >= 0) ze = load_one<F32>(row, edge);
+    }
+    const float f = on ? p.dlogp[t] * p.dloss[p.pair[t]] : 0.0f;
+    const bool zero = f == 0.0f;
+    const Scale sc = scale_of(zero ? 0.0f : p.ref[t], kLog2e);
+    const float fq = zero ? 0.0f : -f * p.inv[t] * exp2_(-sc.delta);
+    const int at = on ? static_cast<int>(label) : -1;
+    auto value = [&](float z, int col) { return __builtin_fmaf(fq, exp_of(z, sc), col == at ? f : 0.0f); };
+    if (edge >= 0) store_one<F32>(out, edge, zero ? 0.0f : value(ze, edge));
+#pragma unroll
+    for (int j = 0; j < kGradUnroll; ++j) {
+        const int c = first + j * kGradThreads;
+        if (c >= sh.pieces) continue;
+        uint4 o = make_uint4(0, 0, 0, 0);
+        if (!zero) {
+            float g[E];
+#pragma unroll
+            for (int i = 0; i < E; ++i) g[i] = value(v[j].at(i), sh.head + c * E + i);
+            o = pack_piece<F32>(g);
+        }
+        *reinterpret_cast<uint4*>(out + body + 16 * static_cast<int64_t>(c)) = o;
+    }
+}
+
+// Waves and workgroups along a row.
+int logp_runs(int64_t V, bool f32) { return static_cast<int>(std::max<int64_t>(1, ceil_div(V / (f32 ? 4 : 8), kLogpRun))); }
+int grad_slices(int64_t V, bool f32) {
+    return static_cast<int>(std::max<int64_t>(1, ceil_div(V / (f32 ? 4 : 8), kGradThreads * kGradUnroll)));
+}
+
+// ---------------------------------------------------------------------------
+// Distillation. p = softmax over the teacher's K logits / tau, q = softmax of
+// the row / tau:
+//   loss = (1 - a) tau^2 sum_k p_k (log p_k - log q_k) + a (lse(z) - z[label])
+//   dz   = w ((1 - a) tau (q - p) + a (softmax(z) - onehot))
+// A workgroup takes a row at a time, the row in registers (NV pieces a thread)
+// between its sums and its gradient, so it is read once; NV = 0 reads a longer
+// one again. As a piece's gradient is written, the next row's piece is loaded
+// into its registers, so that the CU's memory works while its sums are formed.
+// The gradient is written without the p and the onehot first; then a thread
+// per teacher entry (and one for the label) writes its column's value with
+// everything that falls on this column, so that equal entries write equal
+// values.
+// ---------------------------------------------------------------------------
+constexpr int kTop = QL_DISTILL_MAX_TOP;
 
 // Keeps the compiler from holding a piece's values unpacked from one use to
 // the next, which takes twice the registers.
@@ -413,12 +402,20 @@ struct RowEnds {
     float top; // the teacher's
 };
 
+// One workgroup a CU with the chip's longest rows in registers: a workgroup goes
+// from row to row. Shorter rows leave room for several workgroups, which hide
+// each other's sums, and a workgroup a row is faster (us, a row each | in turns):
+// bf16 8192 x 32000 205 | 226 to 248, 2000 x 65536 114 | 117, 4000 x 128000 474 |
+// 454.
+constexpr bool distill_loops(int threads, int nv) { return threads == 1024 && nv == 16; }
+
 // GRAD: the gradient too. BOTH: the row's softmax at temperature 1 besides the
 // one at tau.
 template <bool F32, int THREADS, int NV, bool GRAD, bool BOTH>
-__global__ __launch_bounds__(THREADS, NV == 16 || NV == 0 ? 4 : 6) void distill_kernel(DistillArgs p) {
+__global__ __launch_bounds__(THREADS, NV == 16 || NV == 0 ? 4 : NV == 8 ? (BOTH ? 6 : 7) : 8) void distill_kernel(DistillArgs p) {
     using P = Piece<F32>;
     constexpr int E = P::E, WAVES = THREADS / 64, B = F32 ? 4 : 2;
+    constexpr bool LOOP = distill_loops(THREADS, NV);
     __shared__ float red[3][48];
     __shared__ float s_p[kTop + 1];
     __shared__ int s_k[kTop + 1];
@@ -472,7 +469,7 @@ __global__ __launch_bounds__(THREADS, NV == 16 || NV == 0 ? 4 : 6) void distill_
     }
     while (true) {
         const int64_t tn = t + gridDim.x;
-        const bool more = tn < p.T;
+        const bool more = LOOP && tn < p.T;
         float loss = 0.0f, ft = 0.0f, f1 = 0.0f, w = 0.0f;
         Scale st{}, s1{};
         if (cur.on) {
@@ -480,8 +477,7 @@ __global__ __launch_bounds__(THREADS, NV == 16 || NV == 0 ? 4 : 6) void distill_
             Running r1, rt;  // NV = 0: running sums
             if constexpr (NV > 0) {
 #pragma unroll
-                for (int j = 0; j < NV; ++j) mx[0] = near_max(v[j], mx[0]);
-                mx[0] = on_grid<F32>(mx[0]);
+                for (int j = 0; j < NV; ++j) mx[0] = piece_max(v[j], mx[0]);
 #pragma unroll
                 for (int j = 0; j < NV; ++j) forget(v[j]);
             } else {
@@ -492,8 +488,7 @@ __global__ __launch_bounds__(THREADS, NV == 16 || NV == 0 ? 4 : 6) void distill_
                     for (int j = 0; j < U; ++j) u[j] = load_piece(cur, c0 + j);
                     float m = ninf;
 #pragma unroll
-                    for (int j = 0; j < U; ++j) m = near_max(u[j], m);
-                    m = on_grid<F32>(m);
+                    for (int j = 0; j < U; ++j) m = piece_max(u[j], m);
                     rescale(rt, m, ct);
                     if constexpr (BOTH) rescale(r1, m, kLog2e);
                     const Scale a = scale_of(reference(rt.m), ct), b = scale_of(reference(rt.m), kLog2e);
@@ -568,8 +563,10 @@ __global__ __launch_bounds__(THREADS, NV == 16 || NV == 0 ? 4 : 6) void distill_
         if (tid == 0 && p.loss != nullptr) p.loss[t] = loss;
 
         RowEnds nxt = cur;
-        nxt.on = false;
-        if (more) nxt = begin_row(tn);
+        if constexpr (LOOP) {
+            nxt.on = false;
+            if (more) nxt = begin_row(tn);
+        }
         char* const out = GRAD ? static_cast<char*>(p.dz) + t * p.ld * B : nullptr;
         char* const obody = GRAD ? out + (cur.sh.body - (static_cast<const char*>(p.z) + t * p.ld * B)) : nullptr;
         auto value = [&](float z) {
@@ -594,7 +591,7 @@ __global__ __launch_bounds__(THREADS, NV == 16 || NV == 0 ? 4 : 6) void distill_
             for (int j = 0; j < NV; ++j) {
                 if constexpr (GRAD) put(v[j], j);
                 __builtin_amdgcn_sched_barrier(0);  // a piece at a time: few registers besides the row's
-                v[j] = load_piece(nxt, j);
+                if constexpr (LOOP) v[j] = load_piece(nxt, j);
             }
         } else if constexpr (GRAD) {
             for (int j = 0; j * THREADS < cur.sh.pieces; ++j) put(load_piece(cur, j), j);
@@ -608,16 +605,17 @@ __global__ __launch_bounds__(THREADS, NV == 16 || NV == 0 ? 4 : 6) void distill_
             }
         }
         if (!more) return;
-        cur = nxt;
-        t = tn;
+        if constexpr (LOOP) {
+            cur = nxt;
+            t = tn;
+        }
     }
 }
 
-// Workgroups: as many as the chip holds, each the same number of rows.
 template <bool F32, int THREADS, int NV, bool BOTH>
 void launch_distill_as(const DistillArgs& a, hipStream_t stream) {
-    constexpr int per_cu = NV == 16 ? 1 : NV == 0 ? 2 : 6 * 4 / (THREADS / 64);
-    const int64_t rounds = ceil_div(a.T, 256 * per_cu);
+    // in turns: a workgroup a CU, each the same number of rows
+    const int64_t rounds = distill_loops(THREADS, NV) ? ceil_div(a.T, 256) : 1;
     const dim3 grid(static_cast<uint32_t>(ceil_div(a.T, rounds))), block(THREADS);
     if (a.dz != nullptr)
         hipLaunchKernelGGL((distill_kernel<F32, THREADS, NV, true, BOTH>), grid, block, 0, stream, a);
@@ -632,7 +630,7 @@ void launch_distill_nv(const DistillArgs& a, hipStream_t stream) {
     else if (pieces <= 1024 && a.K < 256) launch_distill_as<F32, 256, 4, BOTH>(a, stream);
     else if (pieces <= 2048) launch_distill_as<F32, 512, 4, BOTH>(a, stream);
     else if (pieces <= 4096) launch_distill_as<F32, 512, 8, BOTH>(a, stream);
-    else if (pieces <= 8192) launch_distill_as<F32, 1024, 8, BOTH>(a, stream);
+    else if (pieces <= 8192) launch_distill_as<F32, 512, 16, BOTH>(a, stream);
     else if (pieces <= 16384) launch_distill_as<F32, 1024, 16, BOTH>(a, stream);
     else launch_distill_as<F32, 1024, 0, BOTH>(a, stream);
 }
@@ -640,21 +638,19 @@ void launch_distill_nv(const DistillArgs& a, hipStream_t stream) {
 }  // namespace
 
 size_t logp_ws_bytes(int64_t T, int64_t V, bool f32) {
-    const int n = logp_slices(T, V, f32);
-    return n > 1 ? static_cast<size_t>(T) * n * 2 * sizeof(float) : 0;
+    return static_cast<size_t>(T) * logp_runs(V, f32) * 2 * sizeof(float);
 }
 
-int launch_logp(LogpArgs a, hipStream_t stream) {
-    a.slices = logp_slices(a.T, a.V, a.f32);
+int launch_logp(LogpArgs& a, hipStream_t stream) {
+    a.runs = logp_runs(a.V, a.f32);
     timer_begin(QL_KERNEL_LOGP, stream);
-    const dim3 grid(static_cast<uint32_t>(a.T * a.slices)), rows(static_cast<uint32_t>(ceil_div(a.T, 256)));
-    if (a.f32) {
-        hipLaunchKernelGGL(logp_kernel<true>, grid, dim3(kStatThreads), 0, stream, a);
-        if (a.slices > 1) hipLaunchKernelGGL(logp_join_kernel<true>, rows, dim3(256), 0, stream, a);
-    } else {
-        hipLaunchKernelGGL(logp_kernel<false>, grid, dim3(kStatThreads), 0, stream, a);
-        if (a.slices > 1) hipLaunchKernelGGL(logp_join_kernel<false>, rows, dim3(256), 0, stream, a);
-    }
+    const dim3 grid(static_cast<uint32_t>(ceil_div(a.T * a.runs, kLogpThreads / 64)));
+    if (a.f32)
+        hipLaunchKernelGGL(logp_kernel<true>, grid, dim3(kLogpThreads), 0, stream, a);
+    else
+        hipLaunchKernelGGL(logp_kernel<false>, grid, dim3(kLogpThreads), 0, stream, a);
+    if (a.logp != nullptr)
+        hipLaunchKernelGGL(logp_join_kernel, dim3(static_cast<uint32_t>(ceil_div(a.T, 256))), dim3(256), 0, stream, a);
     timer_end(QL_KERNEL_LOGP, stream);
     return check_launch("token log probabilities");
 }

@@ -53,8 +53,16 @@ __device__ __forceinline__ void store_vec(void* p, int64_t at, const float (&v)[
     }
 }
 
+template <bool F32, int VEC>
+__device__ __forceinline__ void unpack_vec(const uint4& u, float (&v)[VEC]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+        v[i] = __uint_as_float(F32 ? w[i] : i % 2 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+}
+
 // A row by `waves` waves (the workgroup's, or one of its four), a lane NV
-// pieces of 16 bytes of x.
+// pieces of 16 bytes of x; weight and bias are on their way with it.
 template <bool XF32, bool WF32, int NV>
 __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs p, int waves) {
     constexpr int VEC = XF32 ? 4 : 8;
@@ -66,14 +74,18 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs p, int waves) {
     const int C = p.C;
     const int64_t base = row * C;
 
-    float x[NV][VEC];
+    float x[NV][VEC], w[NV][VEC], b[NV][VEC];
     float s[1] = {0.0f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int c = (first + j * step) * VEC;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) x[j][i] = 0.0f;
-        if (c < C) load_vec<XF32, VEC>(p.X, base + c, x[j]);
+        for (int i = 0; i < VEC; ++i) x[j][i] = b[j][i] = 0.0f;
+        if (c < C) {
+            load_vec<XF32, VEC>(p.X, base + c, x[j]);
+            load_vec<WF32, VEC>(p.w, c, w[j]);
+            if (p.b != nullptr) load_vec<WF32, VEC>(p.b, c, b[j]);
+        }
     }
     float mu = 0.0f;
     const float inv = 1.0f / static_cast<float>(C);
@@ -101,13 +113,9 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs p, int waves) {
     for (int j = 0; j < NV; ++j) {
         const int c = (first + j * step) * VEC;
         if (c >= C) continue;
-        float w[VEC], b[VEC], y[VEC];
-        load_vec<WF32, VEC>(p.w, c, w);
+        float y[VEC];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) b[i] = 0.0f;
-        if (p.b != nullptr) load_vec<WF32, VEC>(p.b, c, b);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) y[i] = __builtin_fmaf(x[j][i] * r, w[i], b[i]);
+        for (int i = 0; i < VEC; ++i) y[i] = __builtin_fmaf(x[j][i] * r, w[j][i], b[j][i]);
         store_vec<XF32, VEC>(p.Y, base + c, y);
     }
     if (first == 0) {
@@ -116,84 +124,117 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs p, int waves) {
     }
 }
 
-// A workgroup takes rows blockIdx, blockIdx + gridDim, ...; a thread keeps its
-// columns' sums of dy h and dy over them and leaves them in part.
+// A workgroup takes `slots` rows at a time, `waves` waves each, and goes on
+// gridDim turns further; a row's loads are under way while the one before is
+// worked on. A thread keeps its columns' sums of dy h and dy over its rows; the
+// slots' are added through LDS, the workgroups' left in part: one array of C
+// sums a CU, so that they cost little beside the rows (with 512 workgroups of a
+// row a time the sums of 1001 x 4096 were two thirds of the rows' bytes: 14.1
+// and 6.5 us).
 template <bool XF32, bool WF32, int NV, bool GRADS>
-__global__ __launch_bounds__(1024) void norm_bwd_kernel(NormArgs p) {
+__global__ __launch_bounds__(1024) void norm_bwd_kernel(NormArgs p, int waves, int slots) {
     constexpr int VEC = XF32 ? 4 : 8;
-    __shared__ float red[2][32];
-    const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-    const int C = p.C, step = blockDim.x;
+    constexpr bool AHEAD = !XF32 || NV < 4;  // else out of registers
+    __shared__ float red[2][16][2][16];  // a slot's two sums over its waves
+    extern __shared__ float sums[];      // [slots][C], where slots > 1
+    const int tid = threadIdx.x, slot = tid / (64 * waves), first = tid - slot * 64 * waves, wave = first >> 6;
+    const int C = p.C, step = 64 * waves;
     const float inv = 1.0f / static_cast<float>(C);
     const bool rms = p.rms;
-    float sw[NV][VEC], sb[NV][VEC];
-    if constexpr (GRADS) {
+    float sw[NV][VEC], sb[NV][VEC], w[NV][VEC];
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
+        const int c = (first + j * step) * VEC;
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) sw[j][i] = sb[j][i] = 0.0f;
+        for (int i = 0; i < VEC; ++i) sw[j][i] = sb[j][i] = w[j][i] = 0.0f;
+        if (c < C && p.dX != nullptr) load_vec<WF32, VEC>(p.w, c, w[j]);
     }
-    int turn = 0;
-    for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x, turn ^= 1) {
-        const int64_t base = row * C;
-        const float r = p.rstd[row], mu = rms ? 0.0f : p.mean[row];
+    uint4 xr[NV], dr[NV];
+    float r = 0.0f, mu = 0.0f;
+    auto load = [&](int64_t row) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (first + j * step) * VEC;
+            xr[j] = dr[j] = make_uint4(0, 0, 0, 0);
+            if (c < C && row < p.T) {
+                const int64_t at = (row * C + c) * (XF32 ? 4 : 2);
+                xr[j] = *reinterpret_cast<const uint4*>(static_cast<const char*>(p.X) + at);
+                dr[j] = *reinterpret_cast<const uint4*>(static_cast<const char*>(p.dY) + at);
+            }
+        }
+        r = row < p.T ? p.rstd[row] : 0.0f;
+        mu = row < p.T && !rms ? p.mean[row] : 0.0f;
+    };
+    const int64_t turn_rows = static_cast<int64_t>(gridDim.x) * slots;
+    int64_t r0 = static_cast<int64_t>(blockIdx.x) * slots;
+    if (AHEAD) load(r0 + slot);
+    for (int turn = 0; r0 < p.T; r0 += turn_rows, turn ^= 1) {
+        const int64_t row = r0 + slot, base = row * C;
+        const bool live = row < p.T;
+        if (!AHEAD) load(row);
+        const float rr = r, m = mu;
         float h[NV][VEC], g[NV][VEC];
         float s[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (threadIdx.x + j * step) * VEC;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) h[j][i] = g[j][i] = 0.0f;
-            if (c < C) {
-                load_vec<XF32, VEC>(p.X, base + c, h[j]);
-                load_vec<XF32, VEC>(p.dY, base + c, g[j]);
-            }
+            unpack_vec<XF32, VEC>(xr[j], h[j]);
+            unpack_vec<XF32, VEC>(dr[j], g[j]);
         }
+        if (AHEAD) load(row + turn_rows);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (threadIdx.x + j * step) * VEC;
-            float w[VEC];
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) w[i] = 0.0f;
-            if (c < C && p.dX != nullptr) load_vec<WF32, VEC>(p.w, c, w);
+            const bool in = live && (first + j * step) * VEC < C;
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                h[j][i] = c < C ? (h[j][i] - mu) * r : 0.0f;
+                h[j][i] = in ? (h[j][i] - m) * rr : 0.0f;
                 if constexpr (GRADS) {
                     sw[j][i] = __builtin_fmaf(g[j][i], h[j][i], sw[j][i]);
                     sb[j][i] += g[j][i];
                 }
-                g[j][i] *= w[i];
+                g[j][i] *= w[j][i];
                 s[0] = __builtin_fmaf(g[j][i], h[j][i], s[0]);
                 s[1] += g[j][i];
             }
         }
         if (p.dX == nullptr) continue;
-        block_reduce(s, red[turn], wave, waves, AddOp{}, AddOp{});
+        block_reduce(s, red[turn][slot][0], wave, waves, AddOp{}, AddOp{});
         const float gh = s[0] * inv, gm = rms ? 0.0f : s[1] * inv;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (threadIdx.x + j * step) * VEC;
-            if (c >= C) continue;
+            const int c = (first + j * step) * VEC;
+            if (c >= C || !live) continue;
             float d[VEC];
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) d[i] = r * (__builtin_fmaf(-gh, h[j][i], g[j][i]) - gm);
+            for (int i = 0; i < VEC; ++i) d[i] = rr * (__builtin_fmaf(-gh, h[j][i], g[j][i]) - gm);
             store_vec<XF32, VEC>(p.dX, base + c, d);
         }
     }
     if constexpr (GRADS) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = (threadIdx.x + j * step) * VEC;
-            if (c >= C) continue;
-            float* const o = p.part + static_cast<int64_t>(blockIdx.x) * C + c;
-            float* const ob = o + static_cast<int64_t>(gridDim.x) * C;
+        for (int a = 0; a < 2; ++a) {
+            if ((a == 0 ? p.dW : p.dB) == nullptr) continue;
+            float* const o = p.part + (static_cast<int64_t>(a) * gridDim.x + blockIdx.x) * C;
+            if (a == 1 && slots > 1) __syncthreads();  // dW's sums have been read
 #pragma unroll
-            for (int i = 0; i < VEC; i += 4) {
-                if (p.dW != nullptr)
-                    *reinterpret_cast<float4*>(o + i) = make_float4(sw[j][i], sw[j][i + 1], sw[j][i + 2], sw[j][i + 3]);
-                if (p.dB != nullptr)
-                    *reinterpret_cast<float4*>(ob + i) = make_float4(sb[j][i], sb[j][i + 1], sb[j][i + 2], sb[j][i + 3]);
+            for (int j = 0; j < NV; ++j) {
+                const int c = (first + j * step) * VEC;
+                if (c >= C) continue;
+                float* const at = (slots > 1 ? sums + slot * C : o) + c;
+#pragma unroll
+                for (int i = 0; i < VEC; i += 4) {
+                    const float* const q = (a == 0 ? sw[j] : sb[j]) + i;
+                    *reinterpret_cast<float4*>(at + i) = make_float4(q[0], q[1], q[2], q[3]);
+                }
+            }
+            if (slots == 1) continue;
+            __syncthreads();
+            for (int c = 4 * tid; c < C; c += 4 * blockDim.x) {
+                float4 t = *reinterpret_cast<const float4*>(sums + c);
+                for (int i = 1; i < slots; ++i) {
+                    const float4 u = *reinterpret_cast<const float4*>(sums + i * C + c);
+                    t.x += u.x, t.y += u.y, t.z += u.z, t.w += u.w;
+                }
+                *reinterpret_cast<float4*>(o + c) = t;
             }
         }
     }
@@ -226,11 +267,10 @@ __global__ __launch_bounds__(256) void column_sums_kernel(const float* part, int
 template <typename F>
 void norm_dispatch(const NormArgs& a, int nv, F f) {
     auto by_nv = [&](auto xf, auto wf) {
-        switch (nv) {
-            case 1: f(xf, wf, std::integral_constant<int, 1>{}); break;
-            case 2: f(xf, wf, std::integral_constant<int, 2>{}); break;
-            default: f(xf, wf, std::integral_constant<int, 4>{}); break;
-        }
+        // at most 16 values a lane: two pieces of bf16, four of fp32
+        if (nv == 1) f(xf, wf, std::integral_constant<int, 1>{});
+        else if (nv == 2 || !decltype(xf)::value) f(xf, wf, std::integral_constant<int, 2>{});
+        else f(xf, wf, std::integral_constant<int, decltype(xf)::value ? 4 : 2>{});
     };
     if (a.x_f32)
         a.w_f32 ? by_nv(std::true_type{}, std::true_type{}) : by_nv(std::true_type{}, std::false_type{});
@@ -238,20 +278,30 @@ void norm_dispatch(const NormArgs& a, int nv, F f) {
         a.w_f32 ? by_nv(std::false_type{}, std::true_type{}) : by_nv(std::false_type{}, std::false_type{});
 }
 
-// Pieces of 16 bytes in a row; waves that take them, at most four pieces a lane.
+// How a row is dealt out: pieces of 16 bytes a lane (`want` where the row is
+// long enough, so that few waves have to meet; more where 16 waves ask for it),
+// waves.
 struct RowPlan {
     int nv, waves;
 };
 RowPlan row_plan(int64_t C, bool f32, int want) {
     const int pieces = static_cast<int>(ceil_div(C, f32 ? 4 : 8));
     RowPlan r{1, 1};
-    for (r.nv = 1; r.nv < want && 64 * r.nv < pieces; r.nv *= 2) {}
+    while (r.nv < want && 64 * r.nv < pieces) r.nv *= 2;
     while (r.waves < 16 && 64 * r.nv * r.waves < pieces) r.waves *= 2;
     while (64 * r.nv * r.waves < pieces) r.nv *= 2;
     return r;
 }
 
-int64_t norm_bwd_groups(int64_t T) { return std::min<int64_t>(T, 512); }
+constexpr int kBwdPieces = 2;
+
+// Rows at a time of a workgroup of 16 waves; workgroups: one a CU.
+int norm_bwd_slots(int64_t T, int waves) {
+    int slots = 1;
+    while (slots * waves < 16 && slots < T) slots *= 2;
+    return slots;
+}
+int64_t norm_bwd_groups(int64_t T, int slots) { return std::min<int64_t>(ceil_div(T, slots), 256); }
 
 }  // namespace
 
@@ -274,22 +324,31 @@ int launch_norm_fwd(const NormArgs& a, hipStream_t stream) {
     return check_launch("norm forward");
 }
 
-size_t norm_bwd_ws_bytes(int64_t T, int64_t C) { return static_cast<size_t>(norm_bwd_groups(T)) * C * 2 * sizeof(float); }
+// (the larger of the two types' plans: fp32 rows take more waves, fewer slots)
+size_t norm_bwd_ws_bytes(int64_t T, int64_t C) {
+    int64_t groups = 0;
+    for (bool f32 : {false, true})
+        groups = std::max(groups, norm_bwd_groups(T, norm_bwd_slots(T, row_plan(C, f32, kBwdPieces).waves)));
+    return static_cast<size_t>(groups) * C * 2 * sizeof(float);
+}
 
 int launch_norm_bwd(const NormArgs& a, hipStream_t stream) {
-    const RowPlan r = row_plan(a.C, a.x_f32, 2);
-    const int64_t groups = norm_bwd_groups(a.T);
+    const RowPlan r = row_plan(a.C, a.x_f32, kBwdPieces);
+    const int slots = norm_bwd_slots(a.T, r.waves);
+    const int64_t groups = norm_bwd_groups(a.T, slots);
     const bool grads = a.dW != nullptr || a.dB != nullptr;
     timer_begin(QL_KERNEL_NORM, stream);
-    if (groups > 0) norm_dispatch(a, r.nv, [&](auto xf, auto wf, auto nv) {
-        const dim3 grid(static_cast<uint32_t>(groups)), block(64 * r.waves);
-        if (grads)
-            hipLaunchKernelGGL((norm_bwd_kernel<decltype(xf)::value, decltype(wf)::value, decltype(nv)::value, true>), grid,
-                               block, 0, stream, a);
-        else
-            hipLaunchKernelGGL((norm_bwd_kernel<decltype(xf)::value, decltype(wf)::value, decltype(nv)::value, false>),
-                               grid, block, 0, stream, a);
-    });
+    if (groups > 0)
+        norm_dispatch(a, r.nv, [&](auto xf, auto wf, auto nv) {
+            const dim3 grid(static_cast<uint32_t>(groups)), block(64 * r.waves * slots);
+            const uint32_t lds = grads && slots > 1 ? slots * a.C * sizeof(float) : 0;  // at most 64 KiB
+            if (grads)
+                hipLaunchKernelGGL((norm_bwd_kernel<decltype(xf)::value, decltype(wf)::value, decltype(nv)::value, true>),
+                                   grid, block, lds, stream, a, r.waves, slots);
+            else
+                hipLaunchKernelGGL((norm_bwd_kernel<decltype(xf)::value, decltype(wf)::value, decltype(nv)::value, false>),
+                                   grid, block, lds, stream, a, r.waves, slots);
+        });
     if (grads) launch_column_sums(a.part, groups, a.C, a.dW, a.dB, a.accumulate, stream);
     timer_end(QL_KERNEL_NORM, stream);
     return check_launch("norm backward");

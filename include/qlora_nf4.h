@@ -814,6 +814,7 @@ int qlora_norm_bwd(const void* X, int x_dtype, int64_t rows, int64_t cols, const
  *   loss, dloss  [pairs] fp32;  seq_logp  out [2 pairs] fp32, the L_s
  *   state  out of the forward, QL_PREF_STATE_ROWS x T fp32, for the backward
  *          on the same logits and labels; rows in no sequence get no gradient
+ *   logp   out [T] fp32, each row's as qlora_token_logp's, 0 in no sequence
  *   ws     qlora_token_logp_workspace(T, V, dtype) bytes
  * pairs = 0 or T = 0 are allowed.
  *

@@ -186,14 +186,24 @@ __global__ __launch_bounds__(kLogpThreads) void logp_kernel(LogpArgs p) {
     if (lane == 0) reinterpret_cast<float2*>(p.part)[unit] = make_float2(m, s * exp2_(-sc.delta));
 }
 
-// A row's runs joined: what exponentials are taken against, their sum.
+// A row's runs joined, eight loads under way at a time: what exponentials are
+// taken against, their sum.
 __device__ __forceinline__ float2 join_runs(const float* part, int runs, int64_t t) {
     const float2* const v = reinterpret_cast<const float2*>(part) + t * runs;
-    float m = -__builtin_inff(), s = 0.0f;
-    for (int i = 0; i < runs; ++i) m = fmaxf(m, v[i].x);
-    m = reference(m);
-    for (int i = 0; i < runs; ++i) s += v[i].y == 0.0f ? 0.0f : v[i].y * exp2_((v[i].x - m) * kLog2e);
-    return make_float2(m, s < __builtin_inff() ? s : __builtin_nanf(""));
+    Running r;
+    for (int i0 = 0; i0 < runs; i0 += 8) {
+        float2 u[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] = i0 + i < runs ? v[i0 + i] : make_float2(-__builtin_inff(), 0.0f);
+        float m = r.m;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, u[i].x);
+        rescale(r, m, kLog2e);
+        const float ref = reference(m);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r.s += u[i].y == 0.0f ? 0.0f : u[i].y * exp2_((u[i].x - ref) * kLog2e);
+    }
+    return make_float2(reference(r.m), r.s < __builtin_inff() ? r.s : __builtin_nanf(""));
 }
 __device__ __forceinline__ float label_logit(const void* z, int f32, int64_t at) {
     return f32 ? static_cast<const float*>(z)[at] : bf16_to_f32(static_cast<const uint16_t*>(z)[at]);

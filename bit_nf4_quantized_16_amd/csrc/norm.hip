@@ -240,26 +240,31 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormArgs p, int waves, i
     }
 }
 
-// Column sums of part [arrays][parts][C], in order: 16 columns a workgroup by
-// 16 threads each.
-__global__ __launch_bounds__(256) void column_sums_kernel(const float* part, int64_t parts, int64_t C, float* out0,
-                                                          float* out1, int accumulate) {
-    __shared__ float red[16][17];
-    const int col = threadIdx.x & 15, k = threadIdx.x >> 4;
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * 16 + col;
+// Column sums of part [arrays][parts][C], in order: 32 columns (a line) a
+// workgroup by 32 threads each, which have eight loads under way.
+__global__ __launch_bounds__(1024) void column_sums_kernel(const float* part, int64_t parts, int64_t C, float* out0,
+                                                           float* out1, int accumulate) {
+    __shared__ float red[32][33];
+    const int col = threadIdx.x & 31, k = threadIdx.x >> 5;
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + col;
     float* const out = blockIdx.y == 0 ? out0 : out1;
     if (out == nullptr) return;
     const float* const src = part + blockIdx.y * parts * C;
     float s = 0.0f;
     if (c < C) {
-#pragma unroll 8
-        for (int64_t g = k; g < parts; g += 16) s += src[g * C + c];
+        for (int64_t g = k; g < parts; g += 256) {
+            float v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[u] = g + 32 * u < parts ? src[(g + 32 * u) * C + c] : 0.0f;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) s += v[u];
+        }
     }
     red[k][col] = s;
     __syncthreads();
-    if (threadIdx.x < 16 && c < C) {
+    if (threadIdx.x < 32 && c < C) {
         float t = red[0][col];
-        for (int i = 1; i < 16; ++i) t += red[i][col];
+        for (int i = 1; i < 32; ++i) t += red[i][col];
         out[c] = accumulate ? out[c] + t : t;
     }
 }
@@ -293,7 +298,10 @@ RowPlan row_plan(int64_t C, bool f32, int want) {
     return r;
 }
 
-constexpr int kBwdPieces = 2;
+// Pieces a lane in the backward: one where two such rows fit a workgroup, else
+// two (us, one | two: 1001 x 4096 20.0 | 22.6, 4096 x 4096 29.3 | 32.0, 16384 x 8192
+// 182 | 169).
+int bwd_pieces(int64_t C, bool f32) { return ceil_div(C, f32 ? 4 : 8) <= 512 ? 1 : 2; }
 
 // Rows at a time of a workgroup of 16 waves; workgroups: one a CU.
 int norm_bwd_slots(int64_t T, int waves) {
@@ -307,7 +315,7 @@ int64_t norm_bwd_groups(int64_t T, int slots) { return std::min<int64_t>(ceil_di
 
 void launch_column_sums(const float* part, int64_t parts, int64_t C, float* out0, float* out1, int accumulate,
                         hipStream_t stream) {
-    hipLaunchKernelGGL(column_sums_kernel, dim3(static_cast<uint32_t>(ceil_div(C, 16)), out1 != nullptr ? 2 : 1), dim3(256),
+    hipLaunchKernelGGL(column_sums_kernel, dim3(static_cast<uint32_t>(ceil_div(C, 32)), out1 != nullptr ? 2 : 1), dim3(1024),
                        0, stream, part, parts, C, out0, out1, accumulate);
 }
 
@@ -328,12 +336,12 @@ int launch_norm_fwd(const NormArgs& a, hipStream_t stream) {
 size_t norm_bwd_ws_bytes(int64_t T, int64_t C) {
     int64_t groups = 0;
     for (bool f32 : {false, true})
-        groups = std::max(groups, norm_bwd_groups(T, norm_bwd_slots(T, row_plan(C, f32, kBwdPieces).waves)));
+        groups = std::max(groups, norm_bwd_groups(T, norm_bwd_slots(T, row_plan(C, f32, bwd_pieces(C, f32)).waves)));
     return static_cast<size_t>(groups) * C * 2 * sizeof(float);
 }
 
 int launch_norm_bwd(const NormArgs& a, hipStream_t stream) {
-    const RowPlan r = row_plan(a.C, a.x_f32, kBwdPieces);
+    const RowPlan r = row_plan(a.C, a.x_f32, bwd_pieces(a.C, a.x_f32));
     const int slots = norm_bwd_slots(a.T, r.waves);
     const int64_t groups = norm_bwd_groups(a.T, slots);
     const bool grads = a.dW != nullptr || a.dB != nullptr;

@@ -698,26 +698,45 @@ __global__ __launch_bounds__(64 * WA * WT, 512 / (64 * WA * WT)) void tile_gemm_
         }
     };
 
-    // The same operand from U in memory, eight ranks a thread and turn.
+    // The same operand from U in memory, eight ranks a thread and turn (as whole
+    // pieces where U's rows are), two turns' loads at a time.
     auto stage_u_terms = [&](int j0, bool both, bool rest_term) {
         if constexpr (EPI) {
+            constexpr int NU = TT * 8 / NTHR;
+            const int lc = tid & 7;  // the same in every turn
+            const int j = j0 + 8 * (both ? lc & 3 : lc);
+            const bool low = both ? lc >= 4 : rest_term;
+#pragma unroll 1
+            for (int i0 = 0; i0 < NU; i0 += 2) {  // all at once cost the main loop registers (121 -> 127 us)
+                float v[2][8];
 #pragma unroll
-            for (int i = 0; i < TT * 8 / NTHR; ++i) {
-                const int c = tid + NTHR * i;
-                const int row = c >> 3, lc = c & 7;
-                const int64_t t = t0 + row;
-                const int j = j0 + 8 * (both ? lc & 3 : lc);
-                const bool low = both ? lc >= 4 : rest_term;
-                float v[8];
+                for (int i = 0; i < 2; ++i) {
+                    // rows past T: the last one's, not stored
+                    const int64_t t = min(t0 + (tid + NTHR * (i0 + i)) / 8, p.T - 1);
+                    const float* const u = p.uf + t * p.r_f + j;
+                    if (p.r_f % 8 == 0) {
+                        const bool in = j < p.r_f;
+                        const float4 a = in ? *reinterpret_cast<const float4*>(u) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        const float4 b = in ? *reinterpret_cast<const float4*>(u + 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        v[i][0] = a.x, v[i][1] = a.y, v[i][2] = a.z, v[i][3] = a.w;
+                        v[i][4] = b.x, v[i][5] = b.y, v[i][6] = b.z, v[i][7] = b.w;
+                    } else {
 #pragma unroll
-                for (int q = 0; q < 8; ++q) v[q] = t < p.T && j + q < p.r_f ? p.s_u * p.uf[t * p.r_f + j + q] : 0.0f;
-                if (low) {
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) v[q] -= bf16_to_f32(to_bf16_bits(v[q]));
+                        for (int q = 0; q < 8; ++q) v[i][q] = j + q < p.r_f ? u[q] : 0.0f;
+                    }
                 }
-                st16(sX0 + row * kStep + 8 * (lc ^ swz(row)),
-                     make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                                pack_bf16x2(v[6], v[7])));
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int row = (tid + NTHR * (i0 + i)) >> 3;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        v[i][q] *= p.s_u;
+                        if (low) v[i][q] -= bf16_to_f32(to_bf16_bits(v[i][q]));
+                    }
+                    st16(sX0 + row * kStep + 8 * (lc ^ swz(row)),
+                         make_uint4(pack_bf16x2(v[i][0], v[i][1]), pack_bf16x2(v[i][2], v[i][3]),
+                                    pack_bf16x2(v[i][4], v[i][5]), pack_bf16x2(v[i][6], v[i][7])));
+                }
             }
         }
     };
@@ -828,8 +847,8 @@ __global__ __launch_bounds__(64 * WA * WT, 512 / (64 * WA * WT)) void tile_gemm_
                 f[2 * q + 1] = __uint_as_float(w[q] & 0xFFFF0000u);
             }
         };
-        uint4 bias = make_uint4(0, 0, 0, 0);
-        if (p.ep.bias != nullptr && in) bias = ld16(p.ep.bias + gm);
+        float bias[8];
+        unpack(p.ep.bias != nullptr && in ? ld16(p.ep.bias + gm) : make_uint4(0, 0, 0, 0), bias);
         auto half = [&](int turn, int h) {  // 32 tokens' sums
             return reinterpret_cast<char*>(h == 0 ? (turn & 1 ? sA1 : sA0) : (turn & 1 ? sX1 : sX0));
         };
@@ -874,17 +893,18 @@ __global__ __launch_bounds__(64 * WA * WT, 512 / (64 * WA * WT)) void tile_gemm_
                     const char* const row = half(turn, r >> 5) + (r & 31) * (TA * 4);
                     const float4 z0 = *reinterpret_cast<const float4*>(row + 16 * ((2 * c8) ^ (r & 31)));
                     const float4 z1 = *reinterpret_cast<const float4*>(row + 16 * ((2 * c8 + 1) ^ (r & 31)));
-                    float y[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w}, f[8];
-                    unpack(bias, f);
+                    float y[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) y[q] += f[q];
+                    for (int q = 0; q < 8; ++q) y[q] += bias[q];
                     if (!in || t >= p.T) continue;
                     p.ep.keep8(t * MA + gm, y);
-                    unpack(res[i], f);
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        y[q] = act_value<decltype(act)::value>(y[q]);
-                        if (p.ep.res != nullptr) y[q] += f[q];
+                    for (int q = 0; q < 8; ++q) y[q] = act_value<decltype(act)::value>(y[q]);
+                    if (p.ep.res != nullptr) {
+                        float f[8];
+                        unpack(res[i], f);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) y[q] += f[q];
                     }
                     st16(p.out + t * MA + gm, make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
                                                          pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7])));

@@ -837,7 +837,8 @@ def _typed(t, name, shape, device=None):
     code = _DTYPES.get(t.dtype)
     if code is None:
         _refuse(_lib.QL_ERR_UNSUPPORTED, "%s is %s, expected bf16 or fp32" % (name, t.dtype))
-    _tensor(t, name, t.dtype, shape, device)
+    if t.shape != shape or not t.is_contiguous() or not (t.is_cuda if device is None else t.device == device):
+        _tensor(t, name, t.dtype, shape, device)
     return code
 
 
@@ -945,8 +946,13 @@ class PreferenceState:
     """What preference_loss_fwd leaves for preference_loss_bwd."""
 
     pairs: int
-    rows: torch.Tensor  # fp32 [4, T]
-    logp: torch.Tensor  # fp32 [T], the labels' log probabilities
+    rows: torch.Tensor  # fp32 [5, T]
+
+    @property
+    def logp(self):
+        """Log probability of each row's label, fp32 [T]; 0 for rows in no
+        sequence and those not counted."""
+        return self.rows[4]
 
 
 def preference_loss_fwd(logits, labels, seq_start, ref_logp, beta=0.1, label_smoothing=0.0, kind="sigmoid",
@@ -970,14 +976,12 @@ def preference_loss_fwd(logits, labels, seq_start, ref_logp, beta=0.1, label_smo
         _refuse(_lib.QL_ERR_UNSUPPORTED, "kind %r (%s)" % (kind, ", ".join(_PREFERENCES)))
     loss = torch.empty(pairs, dtype=torch.float32, device=dev)
     seq_logp = torch.empty(2 * pairs, dtype=torch.float32, device=dev)
-    state = PreferenceState(pairs, torch.empty(_lib.QL_PREF_STATE_ROWS, T, dtype=torch.float32, device=dev),
-                            torch.empty(T, dtype=torch.float32, device=dev))
+    rows = torch.empty(_lib.QL_PREF_STATE_ROWS, T, dtype=torch.float32, device=dev)
     ws, wsb = _workspace(lib.qlora_token_logp_workspace(T, V, code), dev)
     _launch(dev, lib.qlora_preference_loss_fwd, logits.data_ptr(), code, T, V, ld, labels.data_ptr(),
             seq_start.data_ptr(), pairs, ref_logp.data_ptr(), float(beta), float(label_smoothing), _PREFERENCES[kind],
-            1 if average else 0, loss.data_ptr(), seq_logp.data_ptr(), state.rows.data_ptr(), state.logp.data_ptr(),
-            _addr(ws), wsb)
-    return loss, seq_logp, state
+            1 if average else 0, loss.data_ptr(), seq_logp.data_ptr(), rows.data_ptr(), _addr(ws), wsb)
+    return loss, seq_logp, PreferenceState(pairs, rows)
 
 
 def preference_loss_bwd(logits, labels, state, dloss, dlogits=None):

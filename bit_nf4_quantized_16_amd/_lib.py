@@ -53,7 +53,7 @@ QL_NORM_MAX_COLS = 16384
 QL_PREF_SIGMOID = 0
 QL_PREF_HINGE = 1
 QL_PREF_SQUARED = 2
-QL_PREF_STATE_ROWS = 4
+QL_PREF_STATE_ROWS = 5
 QL_DISTILL_MAX_TOP = 256
 QL_ACT8_BLOCK = 32
 QL_OUT_DX = 1
@@ -175,8 +175,8 @@ SIGNATURES = {
     "qlora_norm_bwd": (_I, [_P, _I, _I64, _I64, _P, _I, _P, _P, _P, _P, _P, _P, _I, _P, _SZ, _P]),
     "qlora_token_logp_workspace": (_SZ, [_I64, _I64, _I]),
     "qlora_token_logp": (_I, [_P, _I, _I64, _I64, _I64, _P, _P, _P, _SZ, _P]),
-    "qlora_preference_loss_fwd": (_I, [_P, _I, _I64, _I64, _I64, _P, _P, _I64, _P, _F, _F, _I, _I, _P, _P, _P, _P, _P,
-                                       _SZ, _P]),
+    "qlora_preference_loss_fwd": (_I, [_P, _I, _I64, _I64, _I64, _P, _P, _I64, _P, _F, _F, _I, _I, _P, _P, _P, _P, _SZ,
+                                       _P]),
     "qlora_preference_loss_bwd": (_I, [_P, _I, _I64, _I64, _I64, _P, _P, _P, _I64, _P, _P]),
     "qlora_distill_loss": (_I, [_P, _I, _I64, _I64, _I64, _P, _P, _I, _I64, _P, _F, _F, _P, _P, _P, _P]),
     "qlora_paged_adamw_workspace": (_SZ, [_I64]),

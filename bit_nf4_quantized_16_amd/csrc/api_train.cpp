@@ -223,7 +223,7 @@ int qlora_token_logp(const void* logits, int dtype, int64_t T, int64_t V, int64_
 int qlora_preference_loss_fwd(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld, const int64_t* labels,
                               const int64_t* seq_start, int64_t pairs, const float* ref_logp, float beta,
                               float label_smoothing, int kind, int average, float* loss, float* seq_logp, float* state,
-                              float* logp, void* ws, size_t ws_bytes, void* stream) {
+                              void* ws, size_t ws_bytes, void* stream) {
     clear_error();
     int s;
     if ((s = check_logits_shape(T, V, ld, dtype)) != QL_OK) return s;
@@ -248,9 +248,10 @@ int qlora_preference_loss_fwd(const void* logits, int dtype, int64_t T, int64_t 
         if ((s = check_array(loss, "loss", 4)) != QL_OK) return s;
         if ((s = check_array(seq_logp, "seq_logp", 4)) != QL_OK) return s;
     }
-    if (T > 0 && (s = check_array(logp, "logp", 4)) != QL_OK) return s;
     float* const dlogp = state + 2 * T;
     int* const pair = reinterpret_cast<int*>(state + 3 * T);
+    float* const logp = state + 4 * T;
+    static_assert(QL_PREF_STATE_ROWS == 5, "references, sums, slopes, pairs, log probabilities");
     LogpArgs a{};
     a.z = logits;
     a.f32 = dtype == QL_F32;

@@ -269,13 +269,18 @@ __global__ __launch_bounds__(1024) void column_sums_kernel(const float* part, in
     }
 }
 
+// f(x fp32, w fp32, pieces a lane): at most 16 values a lane, two pieces of bf16
+// or four of fp32.
 template <typename F>
 void norm_dispatch(const NormArgs& a, int nv, F f) {
     auto by_nv = [&](auto xf, auto wf) {
-        // at most 16 values a lane: two pieces of bf16, four of fp32
-        if (nv == 1) f(xf, wf, std::integral_constant<int, 1>{});
-        else if (nv == 2 || !decltype(xf)::value) f(xf, wf, std::integral_constant<int, 2>{});
-        else f(xf, wf, std::integral_constant<int, decltype(xf)::value ? 4 : 2>{});
+        if (nv == 1) {
+            f(xf, wf, std::integral_constant<int, 1>{});
+        } else if (nv == 2) {
+            f(xf, wf, std::integral_constant<int, 2>{});
+        } else if constexpr (decltype(xf)::value) {
+            f(xf, wf, std::integral_constant<int, 4>{});
+        }
     };
     if (a.x_f32)
         a.w_f32 ? by_nv(std::true_type{}, std::true_type{}) : by_nv(std::true_type{}, std::false_type{});
@@ -303,10 +308,13 @@ RowPlan row_plan(int64_t C, bool f32, int want) {
 // 182 | 169).
 int bwd_pieces(int64_t C, bool f32) { return ceil_div(C, f32 ? 4 : 8) <= 512 ? 1 : 2; }
 
-// Rows at a time of a workgroup of 16 waves; workgroups: one a CU.
+// Rows at a time of a workgroup (up to 16 waves); workgroups: one a CU. More
+// than one row where a CU has eight turns' rows and over, since adding the
+// slots' sums costs about a row's time (us, one | two: 1001 x 4096 18.6 | 20.1,
+// 4096 x 4096 33.8 | 29.3), or where it costs little.
 int norm_bwd_slots(int64_t T, int waves) {
     int slots = 1;
-    while (slots * waves < 16 && slots < T) slots *= 2;
+    while (slots * waves < 16 && slots < T && (waves <= 2 || T >= 256 * 8 * slots)) slots *= 2;
     return slots;
 }
 int64_t norm_bwd_groups(int64_t T, int slots) { return std::min<int64_t>(ceil_div(T, slots), 256); }

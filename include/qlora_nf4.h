@@ -813,8 +813,8 @@ int qlora_norm_bwd(const void* X, int x_dtype, int64_t rows, int64_t cols, const
  *
  *   loss, dloss  [pairs] fp32;  seq_logp  out [2 pairs] fp32, the L_s
  *   state  out of the forward, QL_PREF_STATE_ROWS x T fp32, for the backward
- *          on the same logits and labels; rows in no sequence get no gradient
- *   logp   out [T] fp32, each row's as qlora_token_logp's, 0 in no sequence
+ *          on the same logits and labels (its last row is each row's log
+ *          probability, 0 for rows in no sequence; they get no gradient)
  *   ws     qlora_token_logp_workspace(T, V, dtype) bytes
  * pairs = 0 or T = 0 are allowed.
  *
@@ -841,7 +841,7 @@ int qlora_norm_bwd(const void* X, int x_dtype, int64_t rows, int64_t cols, const
 #define QL_PREF_SIGMOID 0
 #define QL_PREF_HINGE 1
 #define QL_PREF_SQUARED 2
-#define QL_PREF_STATE_ROWS 4
+#define QL_PREF_STATE_ROWS 5
 #define QL_DISTILL_MAX_TOP 256
 size_t qlora_token_logp_workspace(int64_t T, int64_t V, int dtype);
 int qlora_token_logp(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld, const int64_t* labels,
@@ -849,7 +849,7 @@ int qlora_token_logp(const void* logits, int dtype, int64_t T, int64_t V, int64_
 int qlora_preference_loss_fwd(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld, const int64_t* labels,
                               const int64_t* seq_start, int64_t pairs, const float* ref_logp, float beta,
                               float label_smoothing, int kind, int average, float* loss, float* seq_logp, float* state,
-                              float* logp, void* ws, size_t ws_bytes, void* stream);
+                              void* ws, size_t ws_bytes, void* stream);
 int qlora_preference_loss_bwd(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld, const int64_t* labels,
                               const float* state, const float* dloss, int64_t pairs, void* dlogits, void* stream);
 int qlora_distill_loss(const void* logits, int dtype, int64_t T, int64_t V, int64_t ld, const int64_t* top_index,

@@ -89,17 +89,15 @@ def test_token_logp(lib, L):
 
 def test_preference(lib, L):
     def fwd(z=P, dt=L.QL_BF16, T=4, V=100, ld=100, labels=P, start=P, pairs=2, ref=P, beta=0.1, e=0.0, kind=0, avg=0, loss=P,
-            sl=P, state=P, lp=P, ws=P, n=1 << 40):
+            sl=P, state=P, ws=P, n=1 << 40):
         return lib.qlora_preference_loss_fwd(z, dt, T, V, ld, labels, start, pairs, ref, beta, e, kind, avg, loss, sl, state,
-                                             lp, ws, n, None)
+                                             ws, n, None)
 
     _each(fwd, L, **_and(LOGITS, QL_ERR_SHAPE=[dict(pairs=-1), dict(pairs=1 << 40)],
                          QL_ERR_UNSUPPORTED=[dict(beta=0.0), dict(beta=-1.0), dict(beta=INF), dict(beta=NAN), dict(e=-0.1),
                                              dict(e=1.5), dict(e=NAN), dict(kind=3), dict(kind=1, e=0.1), dict(avg=2)],
-                         QL_ERR_NULL=[dict(start=None), dict(ref=None), dict(loss=None), dict(sl=None), dict(state=None),
-                                      dict(lp=None)],
-                         QL_ERR_ALIGN=[dict(start=MIS), dict(ref=ODD), dict(loss=ODD), dict(sl=ODD), dict(state=ODD),
-                                       dict(lp=ODD)],
+                         QL_ERR_NULL=[dict(start=None), dict(ref=None), dict(loss=None), dict(sl=None), dict(state=None)],
+                         QL_ERR_ALIGN=[dict(start=MIS), dict(ref=ODD), dict(loss=ODD), dict(sl=ODD), dict(state=ODD)],
                          QL_ERR_WORKSPACE=[dict(V=100000, ld=100000, n=0)],
                          QL_OK=[dict(T=0, pairs=0, z=None, labels=None, start=None, ref=None, loss=None, sl=None, state=None)]))
 

@@ -766,23 +766,26 @@ def qlora_linear_fwd_epilogue(w, X, A=None, B=None, scale=1.0, bias=None, act="n
     fp32 [T, r] and Z = z [T, N] for the backward, fp32 or, with ``save_z``
     torch.bfloat16, rounded (half the memory). ``out``: Y's tensor, which may be
     the residual."""
-    T = _matrix(X, "X").shape[0]
-    dev = w.packed.device
+    if not isinstance(X, torch.Tensor) or X.dim() != 2:
+        _refuse(_lib.QL_ERR_SHAPE, "X is not 2-D")
+    T, dev, rows = X.shape[0], w.packed.device, w.rows
     _tensor(X, "X", torch.bfloat16, (T, w.cols), dev)
-    r = _adapters(A, B, w.rows, w.cols, dev)
+    r = _adapters(A, B, rows, w.cols, dev)
     new = out is None
-    Y = torch.empty(T, w.rows, dtype=torch.bfloat16, device=dev) if new else _tensor(out, "out", torch.bfloat16,
-                                                                                      (T, w.rows), dev)
+    Y = torch.empty(T, rows, dtype=torch.bfloat16, device=dev) if new else _tensor(out, "out", torch.bfloat16, (T, rows),
+                                                                                  dev)
     U = torch.empty(T, r, dtype=torch.float32, device=dev) if save_u and r > 0 else None
-    if save_z not in (False, True, torch.float32, torch.bfloat16):
-        _refuse(_lib.QL_ERR_UNSUPPORTED, "save_z %r (False, True, torch.float32 or torch.bfloat16)" % (save_z,))
-    Z = torch.empty(T, w.rows, dtype=torch.float32 if save_z is True else save_z, device=dev) if save_z else None
-    e = _epilogue(bias, act, residual, Z, T, w.rows, dev)
+    Z = None
+    if save_z:
+        if save_z is not True and save_z not in _DTYPES:
+            _refuse(_lib.QL_ERR_UNSUPPORTED, "save_z %r (False, True, torch.float32 or torch.bfloat16)" % (save_z,))
+        Z = torch.empty(T, rows, dtype=torch.float32 if save_z is True else save_z, device=dev)
+    e = _epilogue(bias, act, residual, Z, T, rows, dev)
     if keep is not None:
         if not isinstance(keep, torch.Tensor) or keep.numel() != T * (w.cols // 8):
             _refuse(_lib.QL_ERR_SHAPE, "keep is no tensor of %d x %d bytes" % (T, w.cols // 8))
         _tensor(keep, "keep", torch.uint8, keep.shape, dev)
-    ws, wsb = _workspace(lib.qlora_linear_fwd_epilogue_workspace(w.rows, w.cols, max(T, 1), r, keep is not None), dev)
+    ws, wsb = _workspace(lib.qlora_linear_fwd_epilogue_workspace(rows, w.cols, max(T, 1), r, keep is not None), dev)
     _launch(dev, lib.qlora_linear_fwd_epilogue, w.descriptor(), X.data_ptr(), T, _addr(A), _addr(B), r, float(scale),
             _addr(keep), float(p), e, Y.data_ptr(), _addr(U), _addr(ws), wsb)
     if not new:

@@ -364,7 +364,10 @@ __global__ __launch_bounds__(kGradThreads) void logp_grad_kernel(LogpGradArgs p)
         }
         if (edge >= 0) ze = load_one<F32>(row, edge);
     }
-    const float f = on ? p.dlogp[t] * p.dloss[p.pair[t]] : 0.0f;
+    // a row in no sequence has no slope and no pair, whatever dloss holds
+    const float slope = on ? p.dlogp[t] : 0.0f;
+    const int pair = on ? p.pair[t] : 0;
+    const float f = slope != 0.0f && pair >= 0 && pair < p.pairs ? slope * p.dloss[pair] : 0.0f;
     const bool zero = f == 0.0f;
     const Scale sc = scale_of(zero ? 0.0f : p.ref[t], kLog2e);
     const float fq = zero ? 0.0f : -f * p.inv[t] * exp2_(-sc.delta);

@@ -136,7 +136,7 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormArgs p, int waves, i
     constexpr int VEC = XF32 ? 4 : 8;
     constexpr bool AHEAD = !XF32 || NV < 4;  // else out of registers
     __shared__ float red[2][16][2][16];  // a slot's two sums over its waves
-    extern __shared__ float sums[];      // [slots][C], where slots > 1
+    extern __shared__ __attribute__((aligned(16))) float sums[];  // [slots - 1][C]
     const int tid = threadIdx.x, slot = tid / (64 * waves), first = tid - slot * 64 * waves, wave = first >> 6;
     const int C = p.C, step = 64 * waves;
     const float inv = 1.0f / static_cast<float>(C);
@@ -210,33 +210,38 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormArgs p, int waves, i
         }
     }
     if constexpr (GRADS) {
-#pragma unroll
-        for (int a = 0; a < 2; ++a) {
-            if ((a == 0 ? p.dW : p.dB) == nullptr) continue;
-            float* const o = p.part + (static_cast<int64_t>(a) * gridDim.x + blockIdx.x) * C;
-            if (a == 1 && slots > 1) __syncthreads();  // dW's sums have been read
+        // the first slot's threads add the others' to theirs
+        auto leave = [&](float* to, const float (&v)[NV][VEC]) {
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int c = (first + j * step) * VEC;
                 if (c >= C) continue;
-                float* const at = (slots > 1 ? sums + slot * C : o) + c;
 #pragma unroll
-                for (int i = 0; i < VEC; i += 4) {
-                    const float* const q = (a == 0 ? sw[j] : sb[j]) + i;
-                    *reinterpret_cast<float4*>(at + i) = make_float4(q[0], q[1], q[2], q[3]);
-                }
+                for (int i = 0; i < VEC; i += 4)
+                    *reinterpret_cast<float4*>(to + c + i) = make_float4(v[j][i], v[j][i + 1], v[j][i + 2], v[j][i + 3]);
             }
-            if (slots == 1) continue;
-            __syncthreads();
-            for (int c = 4 * tid; c < C; c += 4 * blockDim.x) {
-                float4 t = *reinterpret_cast<const float4*>(sums + c);
-                for (int i = 1; i < slots; ++i) {
-                    const float4 u = *reinterpret_cast<const float4*>(sums + i * C + c);
-                    t.x += u.x, t.y += u.y, t.z += u.z, t.w += u.w;
-                }
-                *reinterpret_cast<float4*>(o + c) = t;
+        };
+        auto finish = [&](float (&v)[NV][VEC], bool wanted, int array) {
+            if (!wanted) return;
+            if (slots > 1) {
+                if (slot > 0) leave(sums + (slot - 1) * C, v);
+                __syncthreads();
             }
-        }
+            if (slot == 0) {
+                for (int o = 0; o < slots - 1; ++o)
+#pragma unroll
+                    for (int j = 0; j < NV; ++j) {
+                        const int c = (first + j * step) * VEC;
+                        if (c >= C) continue;
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i) v[j][i] += sums[o * C + c + i];
+                    }
+                leave(p.part + (static_cast<int64_t>(array) * gridDim.x + blockIdx.x) * C, v);
+            }
+        };
+        finish(sw, p.dW != nullptr, 0);
+        if (slots > 1 && p.dW != nullptr && p.dB != nullptr) __syncthreads();  // dW's sums have been read
+        finish(sb, p.dB != nullptr, 1);
     }
 }
 
@@ -357,7 +362,7 @@ int launch_norm_bwd(const NormArgs& a, hipStream_t stream) {
     if (groups > 0)
         norm_dispatch(a, r.nv, [&](auto xf, auto wf, auto nv) {
             const dim3 grid(static_cast<uint32_t>(groups)), block(64 * r.waves * slots);
-            const uint32_t lds = grads && slots > 1 ? slots * a.C * sizeof(float) : 0;  // at most 64 KiB
+            const uint32_t lds = grads ? (slots - 1) * a.C * sizeof(float) : 0;  // at most 60 KiB
             if (grads)
                 hipLaunchKernelGGL((norm_bwd_kernel<decltype(xf)::value, decltype(wf)::value, decltype(nv)::value, true>),
                                    grid, block, lds, stream, a, r.waves, slots);

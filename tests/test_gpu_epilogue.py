@@ -307,3 +307,31 @@ def test_graph_replays_and_two_streams(qn, T):
     side.synchronize()
     torch.cuda.synchronize()
     assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+@pytest.mark.parametrize("N,K,T,r", [(1024, 512, 300, 16), (520, 256, 33, 8)])
+def test_u_inside_the_launch(qn, monkeypatch, N, K, T, r):
+    """The same bits as with U beside the launch; and where a tile does not wait
+    for the words and forms U itself, in two terms as well, the formula."""
+    monkeypatch.setenv("QLORA_NF4_GEMM_TILE", "256")
+    assert qn.lib.qlora_linear_fwd_u_in_launch(N, K, T, r) == 1
+    case = _nf4_case(qn, T, N, K, r, seed=9)
+    w, X, A, B, bias, res = case
+    for act in ("none", "gelu"):
+        call = lambda: qn.qlora_linear_fwd_epilogue(w, X, A, B, 0.7, bias, act, res, save_z=True)
+        inside = call()
+        with monkeypatch.context() as m:
+            m.setenv("QLORA_NF4_FWD_U", "prepass")
+            assert all(torch.equal(p, q) for p, q in zip(inside, call()))
+        for spin in ("-1", "0"):
+            with monkeypatch.context() as m:
+                m.setenv("QLORA_NF4_GEMM_SPIN", spin)
+                Y, U, Z = call()
+            z, tz = _z(qn, w, X, A, B, 0.7, bias)
+            # a tile's U is a chain of K products
+            u = torch.mm(X.double().abs(), A.double().t().abs().contiguous())
+            tz = tz + 0.7 * K * 2.0 ** -24 * torch.mm(u, B.double().t().abs().contiguous())
+            _close("Z", Z, z, tz)
+            v, _ = _act(z, act)
+            want = v + res.double()
+            _close("Y", Y, want, 1.13 * tz + 2.0 ** -16 * v.abs() + 2.0 ** -23 * want.abs())

@@ -432,3 +432,44 @@ def test_more_than_2_to_the_31_logits(qn):
     loss, dz = qn.distill_loss(z, index, top, dlogits=z)  # in place
     _close("loss", loss[rows], wantd["loss"], told["loss"])
     _close("dz", dz[rows], wantd["dz"], told["dz"])
+
+
+def test_a_spoiled_loss_gradient_stays_in_its_pair(qn):
+    """NaN and infinities in dloss: rows in no sequence and of other pairs keep
+    their gradients."""
+    z, _, labels, _, ref, dloss = _pref_case(30, 257, F32, 2, seed=11, masked=0.2)
+    start = torch.tensor([3, 8, 15, 20, 26], device="cuda")
+    _, _, st = qn.preference_loss_fwd(z, labels, start, ref)
+    base = qn.preference_loss_bwd(z, labels, st, dloss)
+    for bad in (NAN, INF):
+        d = dloss.clone()
+        d[0] = bad
+        dz = qn.preference_loss_bwd(z, labels, st, d)
+        assert torch.equal(dz[15:26], base[15:26]) and not bool(dz[:3].any()) and not bool(dz[26:].any())
+        counted = (labels[3:15] >= 0).nonzero()[:, 0] + 3
+        assert not bool(dz[counted].isfinite().all(1).any())
+
+
+def test_timers_count_the_launches(qn):
+    z, _, labels, start, ref, dloss = _pref_case(12, 300, BF16, 1, seed=12)
+    from bit_nf4_quantized_16_amd import _lib
+
+    index, top = torch.randint(0, 300, (12, 3), device="cuda"), torch.randn(12, 3, device="cuda")
+    X, w = torch.randn(4, 64, device="cuda"), torch.ones(64, device="cuda")
+
+    def step():
+        _, _, st = qn.preference_loss_fwd(z, labels, start, ref)
+        qn.preference_loss_bwd(z, labels, st, dloss)
+        qn.distill_loss(z, index, top)
+        _, mean, rstd = qn.norm_fwd(X, w)
+        qn.norm_bwd(X, w, X, mean, rstd)
+        qn.epilogue_bwd(X.to(BF16), X, "silu")
+
+    for kid, n in ((_lib.QL_KERNEL_LOGP, 1), (_lib.QL_KERNEL_PREFERENCE, 1), (_lib.QL_KERNEL_LOGP_GRAD, 1),
+                   (_lib.QL_KERNEL_DISTILL, 1), (_lib.QL_KERNEL_NORM, 2), (_lib.QL_KERNEL_EPILOGUE, 1)):
+        timer = qn.KernelTimer(kid)
+        timer.arm()
+        step()
+        count, ms = timer.read()
+        timer.disarm()
+        assert count == n and ms > 0

@@ -202,3 +202,20 @@ def test_graph_replays_and_a_second_stream(qn):
     side.synchronize()
     torch.cuda.synchronize()
     assert all(torch.equal(p, q) for p, q in zip(a, b2))
+
+
+@pytest.mark.parametrize("xt,wt,T,C", [(BF16, BF16, 4100, 4096), (BF16, F32, 4099, 8192), (F32, F32, 4100, 1024), (F32, BF16, 5000, 4096),
+                                       (BF16, F32, 9000, 2048), (BF16, BF16, 2050, 16384), (F32, F32, 300, 16384)])
+@pytest.mark.parametrize("rms", [False, True])
+def test_many_rows(qn, T, C, xt, wt, rms):
+    """Several rows a workgroup at a time, many turns."""
+    X, w, b, dY = _inputs(T, C, xt, wt, seed=C)
+    want, tol = _exact(X, w, b, dY, 1e-5, rms)
+    Y, mean, rstd = qn.norm_fwd(X, w, b, 1e-5, rms)
+    _close("Y", Y, want["y"], tol["y"])
+    dX, dW, dB = qn.norm_bwd(X, w, dY, mean, rstd)
+    _close("dX", dX, want["dx"], tol["dx"])
+    _close("dW", dW, want["dw"], tol["dw"])
+    _close("dB", dB, want["db"], tol["db"])
+    assert torch.equal(qn.norm_bwd(X, w, dY, mean, rstd, need_dx=False, need_db=False)[1], dW)
+    assert torch.equal(qn.norm_bwd(X, w, dY, mean, rstd, need_dx=False, need_dw=False)[2], dB)

@@ -652,10 +652,18 @@ void launch_distill_as(const DistillArgs& a, hipStream_t stream) {
         hipLaunchKernelGGL((distill_kernel<F32, THREADS, NV, false, BOTH>), grid, block, 0, stream, a);
 }
 
+// The fewest threads that hold the row and have one for every entry and the
+// label. A wave alone meets no barrier: 8192 x 300 bf16, K = 32, 12.0 us, with
+// four waves 27.9. Four to sixteen waves keep the row's registers under 128
+// each, so that two workgroups and more share a CU (2048 x 32000: 8 waves 64.8
+// us, 4 waves 63.3, 16 waves 86; 2000 x 65536: 8 waves 114, 16 waves 134; fp32
+// 2000 x 32000: 108 and 115).
 template <bool F32, bool BOTH>
 void launch_distill_nv(const DistillArgs& a, hipStream_t stream) {
     const int64_t pieces = a.V / (F32 ? 4 : 8);
-    if (pieces <= 256 && a.K < 256) launch_distill_as<F32, 256, 1, BOTH>(a, stream);
+    if (pieces <= 64 && a.K < 64) launch_distill_as<F32, 64, 1, BOTH>(a, stream);
+    else if (pieces <= 256 && a.K < 64) launch_distill_as<F32, 64, 4, BOTH>(a, stream);
+    else if (pieces <= 256 && a.K < 256) launch_distill_as<F32, 256, 1, BOTH>(a, stream);
     else if (pieces <= 1024 && a.K < 256) launch_distill_as<F32, 256, 4, BOTH>(a, stream);
     else if (pieces <= 2048) launch_distill_as<F32, 512, 4, BOTH>(a, stream);
     else if (pieces <= 4096) launch_distill_as<F32, 512, 8, BOTH>(a, stream);

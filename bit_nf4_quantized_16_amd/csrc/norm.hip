@@ -131,7 +131,8 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs p, int waves) {
 // sums a CU, so that they cost little beside the rows (with 512 workgroups of a
 // row a time the sums of 1001 x 4096 were two thirds of the rows' bytes: 14.1
 // and 6.5 us).
-template <bool XF32, bool WF32, int NV, bool GRADS>
+// SUMS: none, dw's, dw's and db's.
+template <bool XF32, bool WF32, int NV, int SUMS>
 __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormArgs p, int waves, int slots) {
     constexpr int VEC = XF32 ? 4 : 8;
     constexpr bool AHEAD = !XF32 || NV < 4;  // else out of registers
@@ -141,29 +142,36 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormArgs p, int waves, i
     const int C = p.C, step = 64 * waves;
     const float inv = 1.0f / static_cast<float>(C);
     const bool rms = p.rms;
-    float sw[NV][VEC], sb[NV][VEC], w[NV][VEC];
+    float sw[NV][VEC], sb[NV][VEC];
+    constexpr int WW = WF32 ? VEC : VEC / 2;  // words of VEC weights, as stored
+    uint32_t w[NV][WW];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int c = (first + j * step) * VEC;
+        const int c = min((first + j * step) * VEC, C - VEC);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) sw[j][i] = sb[j][i] = w[j][i] = 0.0f;
-        if (c < C && p.dX != nullptr) load_vec<WF32, VEC>(p.w, c, w[j]);
+        for (int i = 0; i < VEC; ++i) sw[j][i] = sb[j][i] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < WW; ++i)
+            w[j][i] = reinterpret_cast<const uint32_t*>(static_cast<const char*>(p.w) + c * (WF32 ? 4 : 2))[i];
     }
+    auto weight = [&](int j, int i) {
+        return __uint_as_float(WF32 ? w[j][i] : i % 2 ? w[j][i / 2] & 0xFFFF0000u : w[j][i / 2] << 16);
+    };
+    // Loads without a branch (past the edges the last row's or pieces', not
+    // used): behind one the compiler waits for them at once.
     uint4 xr[NV], dr[NV];
-    float r = 0.0f, mu = 0.0f;
+    float r, mu;
+    const float* const means = rms ? p.rstd : p.mean;
     auto load = [&](int64_t row) {
+        const int64_t at = (row < p.T ? row : p.T - 1);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (first + j * step) * VEC;
-            xr[j] = dr[j] = make_uint4(0, 0, 0, 0);
-            if (c < C && row < p.T) {
-                const int64_t at = (row * C + c) * (XF32 ? 4 : 2);
-                xr[j] = *reinterpret_cast<const uint4*>(static_cast<const char*>(p.X) + at);
-                dr[j] = *reinterpret_cast<const uint4*>(static_cast<const char*>(p.dY) + at);
-            }
+            const int64_t o = (at * C + min((first + j * step) * VEC, C - VEC)) * (XF32 ? 4 : 2);
+            xr[j] = *reinterpret_cast<const uint4*>(static_cast<const char*>(p.X) + o);
+            dr[j] = *reinterpret_cast<const uint4*>(static_cast<const char*>(p.dY) + o);
         }
-        r = row < p.T ? p.rstd[row] : 0.0f;
-        mu = row < p.T && !rms ? p.mean[row] : 0.0f;
+        r = p.rstd[at];
+        mu = means[at];
     };
     const int64_t turn_rows = static_cast<int64_t>(gridDim.x) * slots;
     int64_t r0 = static_cast<int64_t>(blockIdx.x) * slots;
@@ -172,7 +180,7 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormArgs p, int waves, i
         const int64_t row = r0 + slot, base = row * C;
         const bool live = row < p.T;
         if (!AHEAD) load(row);
-        const float rr = r, m = mu;
+        const float rr = r, m = rms ? 0.0f : mu;
         float h[NV][VEC], g[NV][VEC];
         float s[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -187,11 +195,10 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormArgs p, int waves, i
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
                 h[j][i] = in ? (h[j][i] - m) * rr : 0.0f;
-                if constexpr (GRADS) {
-                    sw[j][i] = __builtin_fmaf(g[j][i], h[j][i], sw[j][i]);
-                    sb[j][i] += g[j][i];
-                }
-                g[j][i] *= w[j][i];
+                g[j][i] = in ? g[j][i] : 0.0f;
+                if constexpr (SUMS > 0) sw[j][i] = __builtin_fmaf(g[j][i], h[j][i], sw[j][i]);
+                if constexpr (SUMS > 1) sb[j][i] += g[j][i];
+                g[j][i] *= weight(j, i);
                 s[0] = __builtin_fmaf(g[j][i], h[j][i], s[0]);
                 s[1] += g[j][i];
             }
@@ -209,7 +216,7 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormArgs p, int waves, i
             store_vec<XF32, VEC>(p.dX, base + c, d);
         }
     }
-    if constexpr (GRADS) {
+    if constexpr (SUMS > 0) {
         // the first slot's threads add the others' to theirs
         auto leave = [&](float* to, const float (&v)[NV][VEC]) {
 #pragma unroll
@@ -240,8 +247,10 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormArgs p, int waves, i
             }
         };
         finish(sw, p.dW != nullptr, 0);
-        if (slots > 1 && p.dW != nullptr && p.dB != nullptr) __syncthreads();  // dW's sums have been read
-        finish(sb, p.dB != nullptr, 1);
+        if constexpr (SUMS > 1) {
+            if (slots > 1 && p.dW != nullptr) __syncthreads();  // dW's sums have been read
+            finish(sb, true, 1);
+        }
     }
 }
 
@@ -363,12 +372,14 @@ int launch_norm_bwd(const NormArgs& a, hipStream_t stream) {
         norm_dispatch(a, r.nv, [&](auto xf, auto wf, auto nv) {
             const dim3 grid(static_cast<uint32_t>(groups)), block(64 * r.waves * slots);
             const uint32_t lds = grads ? (slots - 1) * a.C * sizeof(float) : 0;  // at most 60 KiB
-            if (grads)
-                hipLaunchKernelGGL((norm_bwd_kernel<decltype(xf)::value, decltype(wf)::value, decltype(nv)::value, true>),
+            auto launch = [&](auto sums) {
+                hipLaunchKernelGGL((norm_bwd_kernel<decltype(xf)::value, decltype(wf)::value, decltype(nv)::value,
+                                                    decltype(sums)::value>),
                                    grid, block, lds, stream, a, r.waves, slots);
-            else
-                hipLaunchKernelGGL((norm_bwd_kernel<decltype(xf)::value, decltype(wf)::value, decltype(nv)::value, false>),
-                                   grid, block, lds, stream, a, r.waves, slots);
+            };
+            if (a.dB != nullptr) launch(std::integral_constant<int, 2>{});
+            else if (grads) launch(std::integral_constant<int, 1>{});
+            else launch(std::integral_constant<int, 0>{});
         });
     if (grads) launch_column_sums(a.part, groups, a.C, a.dW, a.dB, a.accumulate, stream);
     timer_end(QL_KERNEL_NORM, stream);

@@ -7,6 +7,10 @@
 //
 // Both are bound by HBM: x is read once and kept in registers between the
 // statistics and the output, so the variance is summed from x - mu itself.
+// Measured (a large copy: 5.2 TB/s): forward 4096 x 4096 bf16 12.6 us (5.3 TB/s),
+// 16384 x 8192 96 (5.6); backward 4096 x 4096 with both sums 26.4 (3.8),
+// 16384 x 8192 with dw 150 (5.4). Few rows are bound by their way in and out:
+// 1001 x 4096 6.1 and 16.1 us, 3.9 of them the sums' second launch; one row 2.0.
 #include "common.h"
 #include "internal.h"
 #include "reduce.h"
@@ -128,9 +132,9 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs p, int waves) {
 // gridDim turns further; a row's loads are under way while the one before is
 // worked on. A thread keeps its columns' sums of dy h and dy over its rows; the
 // slots' are added through LDS, the workgroups' left in part: one array of C
-// sums a CU, so that they cost little beside the rows (with 512 workgroups of a
-// row a time the sums of 1001 x 4096 were two thirds of the rows' bytes: 14.1
-// and 6.5 us).
+// sums a CU, so that they cost little beside the rows (512 workgroups' sums for
+// 1001 x 4096 are two thirds of the rows' bytes: 14.1 and 6.5 us for the two
+// launches, with 256 12.4 and 3.9).
 // SUMS: none, dw's, dw's and db's.
 template <bool XF32, bool WF32, int NV, int SUMS>
 __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormArgs p, int waves, int slots) {
@@ -317,21 +321,32 @@ RowPlan row_plan(int64_t C, bool f32, int want) {
     return r;
 }
 
-// Pieces a lane in the backward: one where two such rows fit a workgroup, else
-// two (us, one | two: 1001 x 4096 20.0 | 22.6, 4096 x 4096 29.3 | 32.0, 16384 x 8192
-// 182 | 169).
-int bwd_pieces(int64_t C, bool f32) { return ceil_div(C, f32 ? 4 : 8) <= 512 ? 1 : 2; }
-
-// Rows at a time of a workgroup (up to 16 waves); workgroups: one a CU. More
-// than one row where a CU has eight turns' rows and over, since adding the
-// slots' sums costs about a row's time (us, one | two: 1001 x 4096 18.6 | 20.1,
-// 4096 x 4096 33.8 | 29.3), or where it costs little.
-int norm_bwd_slots(int64_t T, int waves) {
-    int slots = 1;
-    while (slots * waves < 16 && slots < T && (waves <= 2 || T >= 256 * 8 * slots)) slots *= 2;
-    return slots;
+// The backward's: how a row is dealt out, rows at a time of a workgroup,
+// workgroups (at most one a CU). Measured (us, slots x waves of a row, pieces a
+// lane):
+//   1001 x 4096   1x8,1 16.1 | 2x8,1 16.4 | 1x4,2 18.5
+//   4096 x 4096   1x8,1 28.9 | 2x8,1 26.6 | 2x4,2 31.2,  16384 x 4096 92.4 | 87.4 | 102.6
+//   4096 x 8192   1x16,1 50.1 | 1x8,2 60.9;  dw alone 16384 x 8192 166.6 | 150.6 | 2x8,2 157.3
+//   4096 x 1024   1x2,1 18.5 | 2x2,1 13.6 | 4x2,1 12.0 | 8x2,1 12.9
+//   8192 x 512    1x1,1 21.4 | 4x1,1 12.1 | 8x1,1 12.1 | 16x1,1 13.0,  600 x 512 6.9 | 6.8 | 7.4 | 9.4
+// So one piece a lane where 16 waves then hold the row (two sums spill with
+// two), two for the root mean square's long rows, whose db is seldom wanted (the
+// plan takes no notice of what is asked for: the same bits either way); up to
+// four rows and eight waves at a time, 16 where there are many rows of eight.
+struct BwdPlan {
+    RowPlan row;
+    int slots;
+    int64_t groups;
+};
+BwdPlan bwd_plan(int64_t T, int64_t C, bool f32, bool rms) {
+    const int64_t pieces = ceil_div(C, f32 ? 4 : 8);
+    BwdPlan b{row_plan(C, f32, pieces > (rms ? 512 : 1024) ? 2 : 1), 1, 0};
+    const int waves = b.row.waves;
+    const int most = waves < 8 ? 8 : b.row.nv == 1 && T >= 4096 ? 16 : 8;
+    while (b.slots < 4 && b.slots * waves < most && b.slots < T) b.slots *= 2;
+    b.groups = std::min<int64_t>(ceil_div(T, b.slots), 256);
+    return b;
 }
-int64_t norm_bwd_groups(int64_t T, int slots) { return std::min<int64_t>(ceil_div(T, slots), 256); }
 
 }  // namespace
 
@@ -354,24 +369,22 @@ int launch_norm_fwd(const NormArgs& a, hipStream_t stream) {
     return check_launch("norm forward");
 }
 
-// (the larger of the two types' plans: fp32 rows take more waves, fewer slots)
+// (of every plan)
 size_t norm_bwd_ws_bytes(int64_t T, int64_t C) {
-    int64_t groups = 0;
-    for (bool f32 : {false, true})
-        groups = std::max(groups, norm_bwd_groups(T, norm_bwd_slots(T, row_plan(C, f32, bwd_pieces(C, f32)).waves)));
-    return static_cast<size_t>(groups) * C * 2 * sizeof(float);
+    return static_cast<size_t>(std::min<int64_t>(T, 256)) * C * 2 * sizeof(float);
 }
 
 int launch_norm_bwd(const NormArgs& a, hipStream_t stream) {
-    const RowPlan r = row_plan(a.C, a.x_f32, bwd_pieces(a.C, a.x_f32));
-    const int slots = norm_bwd_slots(a.T, r.waves);
-    const int64_t groups = norm_bwd_groups(a.T, slots);
+    const BwdPlan b = bwd_plan(a.T, a.C, a.x_f32, a.rms);
+    const RowPlan r = b.row;
+    const int slots = b.slots;
+    const int64_t groups = b.groups;
     const bool grads = a.dW != nullptr || a.dB != nullptr;
     timer_begin(QL_KERNEL_NORM, stream);
     if (groups > 0)
         norm_dispatch(a, r.nv, [&](auto xf, auto wf, auto nv) {
             const dim3 grid(static_cast<uint32_t>(groups)), block(64 * r.waves * slots);
-            const uint32_t lds = grads ? (slots - 1) * a.C * sizeof(float) : 0;  // at most 60 KiB
+            const uint32_t lds = grads ? (slots - 1) * a.C * sizeof(float) : 0;  // at most 16 KiB
             auto launch = [&](auto sums) {
                 hipLaunchKernelGGL((norm_bwd_kernel<decltype(xf)::value, decltype(wf)::value, decltype(nv)::value,
                                                     decltype(sums)::value>),

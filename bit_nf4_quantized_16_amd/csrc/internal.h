@@ -341,7 +341,7 @@ int launch_norm_bwd(const NormArgs& a, hipStream_t stream);
 void launch_column_sums(const float* part, int64_t parts, int64_t C, float* out0, float* out1, int accumulate,
                         hipStream_t stream);
 
-// Each row's maximum and sum of exponentials, in runs: part [T][runs] pairs
+// Each row's maximum and sum of exponentials, in runs: part [runs][T] pairs
 // (none for rows whose label is outside [0, V)); with logp also
 // logp[t] = z[t][labels[t]] - lse(z[t]), 0 for those rows. z [T, V] (row
 // stride ld), bf16 or fp32.

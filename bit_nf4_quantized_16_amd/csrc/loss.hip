@@ -154,18 +154,20 @@ constexpr int kLogpThreads = 256, kLogpPieces = 8;  // pieces a lane
 constexpr int kLogpRun = 64 * kLogpPieces;          // and a wave
 
 // Maximum and sum of 2^((z - m) log2 e) of a row's runs of pieces, a wave
-// each, all its loads in flight at once; no wave waits for another. (A row a
-// workgroup of 256, two barriers: 45.8 us for 2450 rows of 32000, 1.2 rounds of
-// the chip.)
+// each, all its loads in flight at once; no wave waits for another. HBM-bound:
+// 2450 rows of 32000 bf16 27.6 us (5.7 TB/s), 3000 of 50257 fp32 99 (6.1). (A row
+// a workgroup of 256, two barriers: 45.8 us for the first.) A workgroup's waves
+// take the same run of neighbouring rows, whose results lie side by side (four
+// runs of a row each: 1 to 2 us more for the loss and its gradient).
 template <bool F32>
 __global__ __launch_bounds__(kLogpThreads) void logp_kernel(LogpArgs p) {
     using P = Piece<F32>;
     constexpr int E = P::E;
     const int lane = threadIdx.x & 63;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kLogpThreads / 64) + (threadIdx.x >> 6);
-    const int64_t t = unit / p.runs;
+    const uint32_t rows = blockIdx.x / p.runs;
+    const int run = static_cast<int>(blockIdx.x - rows * p.runs);
+    const int64_t t = static_cast<int64_t>(rows) * (kLogpThreads / 64) + (threadIdx.x >> 6);
     if (t >= p.T) return;
-    const int run = static_cast<int>(unit - t * p.runs);
     const int64_t label = p.labels[t];
     if (run == 0 && lane == 0 && p.dlogp != nullptr) {
         p.dlogp[t] = 0.0f;  // until its pair says otherwise
@@ -197,18 +199,20 @@ __global__ __launch_bounds__(kLogpThreads) void logp_kernel(LogpArgs p) {
         for (int i = 0; i < E; ++i) s += exp_of(v[j].at(i), sc);
     s = wave_reduce(s, AddOp{});
     // of the exact argument: the scale's rounding off
-    if (lane == 0) reinterpret_cast<float2*>(p.part)[unit] = make_float2(m, s * exp2_(-sc.delta));
+    if (lane == 0) reinterpret_cast<float2*>(p.part)[run * p.T + t] = make_float2(m, s * exp2_(-sc.delta));
 }
 
 // A row's runs joined, eight loads under way at a time: what exponentials are
-// taken against, their sum.
-__device__ __forceinline__ float2 join_runs(const float* part, int runs, int64_t t) {
-    const float2* const v = reinterpret_cast<const float2*>(part) + t * runs;
+// taken against, their sum. Neighbouring threads have neighbouring rows, and the
+// runs lie [run][row] so that a wave's load is a few lines (as [row][run] the
+// join of 3000 rows of 25 took 18 us, so 11).
+__device__ __forceinline__ float2 join_runs(const float* part, int runs, int64_t T, int64_t t) {
+    const float2* const v = reinterpret_cast<const float2*>(part) + t;
     Running r;
     for (int i0 = 0; i0 < runs; i0 += 8) {
         float2 u[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] = i0 + i < runs ? v[i0 + i] : make_float2(-__builtin_inff(), 0.0f);
+        for (int i = 0; i < 8; ++i) u[i] = i0 + i < runs ? v[(i0 + i) * T] : make_float2(-__builtin_inff(), 0.0f);
         float m = r.m;
 #pragma unroll
         for (int i = 0; i < 8; ++i) m = fmaxf(m, u[i].x);
@@ -230,7 +234,7 @@ __global__ __launch_bounds__(256) void logp_join_kernel(LogpArgs p) {
     float l = 0.0f;
     if (label >= 0 && label < p.V) {
         const float z = label_logit(p.z, p.f32, t * p.ld + label);
-        const float2 r = join_runs(p.part, p.runs, t);
+        const float2 r = join_runs(p.part, p.runs, p.T, t);
         l = (z - r.x) - kLn2 * __builtin_amdgcn_logf(r.y);
     }
     p.logp[t] = l;
@@ -261,7 +265,9 @@ __device__ __forceinline__ void pair_loss(const PairArgs& p, double d, float& lo
 
 // Joins its rows' runs (their log probabilities, references and sums are kept
 // for the caller and the gradient), sums them, and hands each row its share of
-// the loss's slope.
+// the loss's slope. Bound by latency, a chain of few loads and sums on one CU a
+// pair: one pair of 16 rows 4.0 us, four of 875 (8 runs) 7.5, eight of 750 (25)
+// 11.1; more CUs would take one more launch, 3 us.
 __global__ __launch_bounds__(kPairThreads) void pair_kernel(PairArgs p) {
     __shared__ double sums[2][kPairThreads / 64];
     __shared__ int counts[2][kPairThreads / 64];
@@ -274,31 +280,35 @@ __global__ __launch_bounds__(kPairThreads) void pair_kernel(PairArgs p) {
         at[i] = a < 0 ? 0 : (a > p.T ? p.T : a);
     }
     const float ref0 = p.ref_logp[2 * pair], ref1 = p.ref_logp[2 * pair + 1];
+    // both sequences' rows in one go
+    double s[2] = {0.0, 0.0};
+    int n[2] = {0, 0};
+    for (int64_t t = at[0] + tid; t < at[2]; t += kPairThreads) {
+        const int64_t label = p.labels[t];
+        const int q = t >= at[1];
+        float l = 0.0f;
+        if (label >= 0 && label < p.V) {
+            const float z = label_logit(p.z, p.f32, t * p.ld + label);
+            const float2 r = join_runs(p.part, p.runs, p.T, t);
+            l = (z - r.x) - kLn2 * __builtin_amdgcn_logf(r.y);
+            p.ref[t] = r.x;
+            p.inv[t] = 1.0f / r.y;
+            n[0] += q == 0;
+            n[1] += q;
+        }
+        p.logp[t] = l;
+        s[0] += q == 0 ? l : 0.0f;
+        s[1] += q == 0 ? 0.0f : l;
+    }
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-        double s = 0.0;
-        int n = 0;
-        for (int64_t t = at[q] + tid; t < at[q + 1]; t += kPairThreads) {
-            const int64_t label = p.labels[t];
-            float l = 0.0f;
-            if (label >= 0 && label < p.V) {
-                const float z = label_logit(p.z, p.f32, t * p.ld + label);
-                const float2 r = join_runs(p.part, p.runs, t);
-                l = (z - r.x) - kLn2 * __builtin_amdgcn_logf(r.y);
-                p.ref[t] = r.x;
-                p.inv[t] = 1.0f / r.y;
-                ++n;
-            }
-            p.logp[t] = l;
-            s += l;
-        }
         for (int d = 32; d > 0; d >>= 1) {
-            s += __shfl_xor(s, d);
-            n += __shfl_xor(n, d);
+            s[q] += __shfl_xor(s[q], d);
+            n[q] += __shfl_xor(n[q], d);
         }
         if ((tid & 63) == 0) {
-            sums[q][wave] = s;
-            counts[q][wave] = n;
+            sums[q][wave] = s[q];
+            counts[q][wave] = n[q];
         }
     }
     __syncthreads();
@@ -324,18 +334,19 @@ __global__ __launch_bounds__(kPairThreads) void pair_kernel(PairArgs p) {
         slopes[1] = static_cast<float>(-slope * per[1]);
     }
     __syncthreads();
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-        for (int64_t t = at[q] + tid; t < at[q + 1]; t += kPairThreads) {
-            const int64_t label = p.labels[t];
-            if (label < 0 || label >= p.V) continue;
-            p.dlogp[t] = slopes[q];
-            p.pair[t] = pair;
-        }
+    for (int64_t t = at[0] + tid; t < at[2]; t += kPairThreads) {
+        const int64_t label = p.labels[t];
+        if (label < 0 || label >= p.V) continue;
+        p.dlogp[t] = slopes[t >= at[1]];
+        p.pair[t] = pair;
+    }
 }
 
 // dz = f (onehot - softmax), f = dloss dlogp; a row that counts nothing is
-// written as zeros without being read.
+// written as zeros without being read. HBM-bound, each value on its own, 16 KiB
+// of a row a workgroup: 3500 x 32000 bf16 with 2450 rows read 54 us (7.0 TB/s,
+// the last rows' reads from the last-level cache), 6001 x 50257 fp32 with 3000
+// read 340 (5.3).
 constexpr int kGradThreads = 256, kGradUnroll = 4;
 
 template <bool F32>
@@ -407,7 +418,9 @@ int grad_slices(int64_t V, bool f32) {
 // The gradient is written without the p and the onehot first; then a thread
 // per teacher entry (and one for the label) writes its column's value with
 // everything that falls on this column, so that equal entries write equal
-// values.
+// values. HBM-bound where there are many rows (2048 x 32000 bf16, K = 64, 63 us,
+// 4.1 TB/s; 4000 x 128000, K = 32 with the cross entropy, 433, 4.7), one row by
+// its barriers and loads in a row (32000: 6.9 us).
 // ---------------------------------------------------------------------------
 constexpr int kTop = QL_DISTILL_MAX_TOP;
 
@@ -681,7 +694,7 @@ size_t logp_ws_bytes(int64_t T, int64_t V, bool f32) {
 int launch_logp(LogpArgs& a, hipStream_t stream) {
     a.runs = logp_runs(a.V, a.f32);
     timer_begin(QL_KERNEL_LOGP, stream);
-    const dim3 grid(static_cast<uint32_t>(ceil_div(a.T * a.runs, kLogpThreads / 64)));
+    const dim3 grid(static_cast<uint32_t>(ceil_div(a.T, kLogpThreads / 64) * a.runs));
     if (a.f32)
         hipLaunchKernelGGL(logp_kernel<true>, grid, dim3(kLogpThreads), 0, stream, a);
     else

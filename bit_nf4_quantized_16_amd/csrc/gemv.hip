@@ -145,7 +145,9 @@ constexpr int gemv_min_waves() {
 
 // NS > 0: every wave has NS steps, or NS - 1 (all issued up front);
 // NS == 0: a ring of gemv_ring_depth<TX>() steps, refilled as they are used.
-// EPI: act(sum + bias) + residual in place of the sum.
+// EPI: act(sum + bias) + residual in place of the sum; the bias and residual are
+// on their way while the weight is read (us, without and with both, r = 16:
+// 4096 x 4096 T = 1 9.6, 9.9, T = 16 10.8, 11.7; 11008 x 4096 T = 1 14.5, 15.1).
 template <int TX, int NS, bool EPI>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(gemv_min_waves<TX, NS>()))) void gemv_kernel(
     GemvArgs p) {

@@ -324,7 +324,9 @@ struct Q4GLinearArgs {
     int epilogue;
 };
 
-// act(y + bias) + residual for output n of a row, at i of Y.
+// act(y + bias) + residual for output n of a row, at i of Y. The loads come last
+// (issued ahead of the weight they gained nothing): bias and residual add 0.4 us
+// to 14.3 at 4096 x 11008, T = 24, and 0.25 to 4.9 at 4096 x 4096, T = 1.
 __device__ __forceinline__ float q4g_epilogue(const Epilogue& ep, float y, int64_t n, int64_t i) {
     if (ep.bias != nullptr) y += bf16_to_f32(ep.bias[n]);
     with_act(ep.act, [&](auto act) { y = act_value<decltype(act)::value>(y); });

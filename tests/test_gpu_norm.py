@@ -219,3 +219,21 @@ def test_many_rows(qn, T, C, xt, wt, rms):
     _close("dB", dB, want["db"], tol["db"])
     assert torch.equal(qn.norm_bwd(X, w, dY, mean, rstd, need_dx=False, need_db=False)[1], dW)
     assert torch.equal(qn.norm_bwd(X, w, dY, mean, rstd, need_dx=False, need_dw=False)[2], dB)
+
+
+@pytest.mark.parametrize("T,C", [(9001, 512), (4099, 4096), (700, 8192)])
+@pytest.mark.parametrize("rms", [False, True])
+def test_gradient_in_place_over_many_turns(qn, T, C, rms):
+    """dX in dY's place while later rows are loaded ahead, sums beside it: the
+    bits of a call with arrays of its own."""
+    X, w, b, dY = _inputs(T, C, BF16, F32, seed=T)
+    Y, mean, rstd = qn.norm_fwd(X, w, b, 1e-5, rms)
+    dX, dW, dB = qn.norm_bwd(X, w, dY, mean, rstd)
+    d, sw, sb = dY.clone(), torch.zeros(C, device="cuda"), torch.zeros(C, device="cuda")
+    n = qn.lib.qlora_norm_bwd_workspace(T, C)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    assert qn.lib.qlora_norm_bwd(X.data_ptr(), 1, T, C, w.data_ptr(), 0, d.data_ptr(),
+                                 mean.data_ptr() if mean is not None else None, rstd.data_ptr(), d.data_ptr(),
+                                 sw.data_ptr(), sb.data_ptr(), 1, ws.data_ptr(), n,
+                                 torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(d, dX) and torch.equal(sw, dW) and torch.equal(sb, dB)

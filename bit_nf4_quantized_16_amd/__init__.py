@@ -766,9 +766,7 @@ def qlora_linear_fwd_epilogue(w, X, A=None, B=None, scale=1.0, bias=None, act="n
     fp32 [T, r] and Z = z [T, N] for the backward, fp32 or, with ``save_z``
     torch.bfloat16, rounded (half the memory). ``out``: Y's tensor, which may be
     the residual."""
-    if not isinstance(X, torch.Tensor) or X.dim() != 2:
-        _refuse(_lib.QL_ERR_SHAPE, "X is not 2-D")
-    T, dev, rows = X.shape[0], w.packed.device, w.rows
+    T, dev, rows = _matrix(X, "X").shape[0], w.packed.device, w.rows
     _tensor(X, "X", torch.bfloat16, (T, w.cols), dev)
     r = _adapters(A, B, rows, w.cols, dev)
     new = out is None

@@ -49,8 +49,9 @@ int check_norm(int64_t rows, int64_t cols, int x_dtype, int w_dtype) {
 
 int check_epilogue_shape(int64_t rows, int64_t cols) {
     if (rows < 0 || rows > (int64_t{1} << 31)) return set_error(QL_ERR_SHAPE, "rows = %lld", (long long)rows);
-    if (cols <= 0 || cols % 8 != 0 || cols > (int64_t{1} << 31))
-        return set_error(QL_ERR_SHAPE, "cols = %lld (a multiple of 8)", (long long)cols);
+    // 1024 threads per 32 column sums, fewer than 2^32 threads a launch
+    if (cols <= 0 || cols % 8 != 0 || cols >= (int64_t{1} << 27))
+        return set_error(QL_ERR_SHAPE, "cols = %lld (a multiple of 8 under 2^27)", (long long)cols);
     if (rows > 0 && cols > (int64_t{1} << 40) / rows)
         return set_error(QL_ERR_SHAPE, "%lld x %lld", (long long)rows, (long long)cols);
     return QL_OK;

@@ -739,7 +739,7 @@ int q4g_linear_fwd_epilogue(const ql_q4g_weight* w, const uint16_t* X, int64_t T
  *   ws     qlora_epilogue_bwd_workspace(rows, cols) bytes where dbias is wanted
  *
  * rows == 0: dbias is an empty sum. Sums are fp32 in a fixed order.
- * Errors: QL_ERR_NULL, QL_ERR_SHAPE (rows < 0 or over 2^31, cols, more than 2^40
+ * Errors: QL_ERR_NULL, QL_ERR_SHAPE (rows < 0 or over 2^31, cols 2^27 and more, over 2^40
  * values), QL_ERR_UNSUPPORTED (act, z_dtype, accumulate), QL_ERR_ALIGN,
  * QL_ERR_WORKSPACE, QL_ERR_HIP.
  */

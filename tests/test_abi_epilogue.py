@@ -102,3 +102,10 @@ def test_python_refusals_need_no_gpu():
                  lambda: qn.q4g_linear_fwd_epilogue(qn.Q4GWeight(64, 64, 32, u8.view(64, 32), z, None), z)):
         with pytest.raises(qn.QLoraError):
             call()
+
+
+def test_backward_refuses_more_columns_than_a_launch_can_add(lib, L):
+    last = (1 << 27) - 8
+    assert lib.qlora_epilogue_bwd_workspace(1, last) == 4 * last
+    assert lib.qlora_epilogue_bwd_workspace(1, last + 8) == 0
+    assert lib.qlora_epilogue_bwd(P, P, 1, 1, last + 8, 2, P, P, 0, P, 1 << 40, None) == L.QL_ERR_SHAPE

@@ -131,6 +131,18 @@ __device__ __forceinline__ Scale scale_of(float m, float c) {
     return s;
 }
 __device__ __forceinline__ float exp_of(float z, const Scale& s) { return exp2_(__builtin_fmaf(z, s.c, -s.mc)); }
+// A running sum of such exponentials, which carries 2^delta of its maximum's
+// scale, brought to a new maximum: delta changes with it. (fp32 logits around
+// 1e6 have deltas of up to 2^-4; without them the sums of rows that a maximum
+// rises over many times were off by 1e-3.) Two maxima lie at least a delta apart
+// in z c, so the exponent's roundings are under 2^-21 of that distance.
+__device__ __forceinline__ void rescale(Running& r, Scale& s, float m, float c) {
+    if (!(m > r.m)) return;
+    const Scale to = scale_of(reference(m), c);
+    r.s = r.s == 0.0f ? 0.0f : r.s * exp2_((r.m - m) * c - s.delta + to.delta);
+    r.m = m;
+    s = to;
+}
 
 // The largest of m and a piece's values.
 template <bool F32>
@@ -516,7 +528,8 @@ __global__ __launch_bounds__(THREADS, NV == 16 || NV == 0 ? 4 : NV == 8 ? (BOTH 
         Scale st{}, s1{};
         if (cur.on) {
             float mx[2] = {cur.ze, cur.top};
-            Running r1, rt;  // NV = 0: running sums
+            Running r1, rt;  // NV = 0: running sums and their scales
+            Scale u1 = scale_of(0.0f, kLog2e), ut = scale_of(0.0f, ct);
             if constexpr (NV > 0) {
 #pragma unroll
                 for (int j = 0; j < NV; ++j) mx[0] = piece_max(v[j], mx[0]);
@@ -531,15 +544,14 @@ __global__ __launch_bounds__(THREADS, NV == 16 || NV == 0 ? 4 : NV == 8 ? (BOTH 
                     float m = ninf;
 #pragma unroll
                     for (int j = 0; j < U; ++j) m = piece_max(u[j], m);
-                    rescale(rt, m, ct);
-                    if constexpr (BOTH) rescale(r1, m, kLog2e);
-                    const Scale a = scale_of(reference(rt.m), ct), b = scale_of(reference(rt.m), kLog2e);
+                    rescale(rt, ut, m, ct);
+                    if constexpr (BOTH) rescale(r1, u1, m, kLog2e);
 #pragma unroll
                     for (int j = 0; j < U; ++j)
 #pragma unroll
                         for (int i = 0; i < E; ++i) {
-                            rt.s += exp_of(u[j].at(i), a);
-                            if constexpr (BOTH) r1.s += exp_of(u[j].at(i), b);
+                            rt.s += exp_of(u[j].at(i), ut);
+                            if constexpr (BOTH) r1.s += exp_of(u[j].at(i), u1);
                         }
                 }
                 mx[0] = fmaxf(mx[0], rt.m);
@@ -566,13 +578,13 @@ __global__ __launch_bounds__(THREADS, NV == 16 || NV == 0 ? 4 : NV == 8 ? (BOTH 
 #pragma unroll
                 for (int j = 0; j < NV; ++j) forget(v[j]);
             } else {
-                // a thread's sums against its own maximum: their rounding, and m's
-                auto join = [&](Running& r, float c, const Scale& to) {
-                    const Scale own = scale_of(reference(r.m), c);
-                    return r.s == 0.0f ? 0.0f : r.s * exp2_((reference(r.m) - m) * c - own.delta + to.delta);
-                };
-                s[0] += join(rt, ct, st);
-                if constexpr (BOTH) s[1] += join(r1, kLog2e, s1);
+                // a thread's sums against its own maximum, brought to the row's
+                rescale(rt, ut, m, ct);
+                s[0] += rt.s;
+                if constexpr (BOTH) {
+                    rescale(r1, u1, m, kLog2e);
+                    s[1] += r1.s;
+                }
             }
             block_reduce(s, red[1], wave, WAVES, AddOp{}, AddOp{}, AddOp{});
             if constexpr (!BOTH) s[1] = s[0];  // tau = 1, or not used

@@ -114,17 +114,18 @@ __device__ __forceinline__ void rescale(Running& r, float m, float c) {
 
 // Exponentials against the maximum m: 2^(z c - m c), one multiply-add. The
 // rounding of m c is the same for all and is taken off the logarithm of their
-// sum (delta). Past |m c| = 2^28 that rounding could be more than 16, but
-// then values next to each other are at least 32 apart in z c, so that only
-// those equal to m count: a power of two that brings m to 2^30 in c's place
-// gives them exactly 1 and the others 0.
+// sum (delta). Up to |m c| = 2^30 that rounding is at most 32, so the sum keeps
+// its bits. Past it, values next to each other (an fp32 step is over 2^-24 of the
+// value) are at least 64 apart in z c, so that only those equal to m count (a
+// row's others together are under 2^30 2^-64): a power of two that brings m to
+// 2^30 or more in c's place gives them exactly 1 and the others as little.
 struct Scale {
     float c, mc, delta;
 };
 __device__ __forceinline__ Scale scale_of(float m, float c) {
     Scale s;
     const float mc = m * c;
-    const bool far = !(fabsf(mc) <= 0x1p28f);
+    const bool far = !(fabsf(mc) <= 0x1p30f);
     s.c = far ? __uint_as_float((284u - (__float_as_uint(m) >> 23 & 255u)) << 23) : c;
     s.mc = far ? m * s.c : mc;
     s.delta = far ? 0.0f : __builtin_fmaf(m, c, -mc);

@@ -6,7 +6,7 @@ test_gpu_losses'."""
 import pytest
 import torch
 
-from test_gpu_losses import BF16, F32, _distill_case, _distill_check
+from test_gpu_losses import BF16, F32, _close, _distill_case, _distill_check, _e, _pref_check
 
 pytestmark = pytest.mark.gpu
 
@@ -30,3 +30,49 @@ def test_distill_long_rows_far_from_zero(qn, dt, V, offset):
     z[1] = z[1].sort().values  # a new maximum at nearly every turn
     for tau, alpha in ((1.0, 0.0), (0.7, 0.3), (2.0, 0.0), (1.0, 0.4)):
         _distill_check(qn, z, index, top, labels, tau, alpha, weight)
+
+
+@pytest.mark.parametrize("V", [9, 40, 1500, 9000, 70001])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_distill_neighbours_of_a_far_maximum(qn, V, sign):
+    """Values one to three steps under the maximum where a step is 16 of the
+    exponent: 2^-16 of the sum, and the whole of their own gradients."""
+    tau = float(torch.tensor(2.7e-6, dtype=F32))
+    g = torch.Generator(device="cuda").manual_seed(V)
+    # under 512 (or over -512) steps of 2^-15, / tau = 11.3; m log2 e / tau = 2^28.03
+    top_value = 512 - 2.0 ** -15 if sign > 0 else -512 + 2.0 ** -15 * 8
+    z = top_value - 2.0 ** -15 * torch.randint(0, 4, (6, V), generator=g, device="cuda").double()
+    z[:, 3] = top_value
+    z = z.float()
+    index = torch.randint(0, V, (6, 3), generator=g, device="cuda")
+    labels = torch.randint(0, V, (6,), generator=g, device="cuda")
+    top = tau * torch.randn(6, 3, generator=g, device="cuda")
+    weight = torch.rand(6, generator=g, device="cuda") + 0.1
+    _distill_check(qn, z, index, top, None, tau, 0.0, weight)
+    z[:, :3] = top_value
+    _distill_check(qn, z, index, top, labels, tau, 0.0, None)
+
+
+@pytest.mark.parametrize("dt,V", [(F32, 20001), (F32, 65540), (F32, 131080), (F32, 128001), (BF16, 140001)])
+def test_distill_offset_whose_steps_are_far_apart(qn, dt, V):
+    """fp32 logits 16 apart: a neighbour of the maximum is 2^-33 of the sum, and
+    has that gradient."""
+    z, _, index, top, labels, weight = _distill_case(3, V, 9, dt, seed=V)
+    z.add_(1.5e8)
+    z[1] = z[1].sort().values
+    for tau, alpha in ((1.0, 0.0), (0.7, 0.3), (2.0, 0.0), (1.0, 0.4)):
+        _distill_check(qn, z, index, top, labels, tau, alpha, weight)
+
+
+@pytest.mark.parametrize("top_value", [2.5e8, -2.5e8])
+def test_preference_neighbours_of_a_far_maximum(qn, top_value):
+    """512 values a step of 16 under the maximum: 5.8e-5 of the sum."""
+    z = torch.full((8, 513), top_value - 16, device="cuda")
+    at = torch.arange(8, device="cuda")
+    z[at, 60 * at] = top_value
+    assert bool((z.amin(1) == top_value - 16).all())
+    labels = 60 * at
+    want = torch.log_softmax(z.double(), 1).gather(1, labels[:, None])[:, 0]
+    _close("logp", qn.token_logp(z, labels), want, _e(z) + 2.0 ** -22 * (want.abs() + 40))
+    start = torch.tensor([0, 3, 4, 6, 8], device="cuda")
+    _pref_check(qn, z, labels, start, torch.randn(4, device="cuda"), torch.rand(2, device="cuda") + 0.5)

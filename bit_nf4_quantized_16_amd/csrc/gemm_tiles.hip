@@ -592,6 +592,10 @@ __global__ __launch_bounds__(64 * WA * WT, 512 / (64 * WA * WT)) void tile_gemm_
     }
     }  // sb < se
 
+    // EPI: what bf16 leaves of v; nothing of a v that it makes infinite (inf - inf
+    // would make NaN of every output of the token)
+    auto rest_of = [](float v, uint16_t hi) { return (hi & 0x7F80u) == 0x7F80u ? 0.0f : v - bf16_to_f32(hi); };
+
     // U (forward) or G (dX) inside the launch: the token operand of the rank
     // step from the words of this tile's tokens (TT x r_u, at most 8 a
     // thread), each converted as the separate projection converts it, bf16(s_u v), and
@@ -608,7 +612,7 @@ __global__ __launch_bounds__(64 * WA * WT, 512 / (64 * WA * WT)) void tile_gemm_
         const uint16_t hi = to_bf16_bits(v);
         sX0[row * kStep + 8 * ((j >> 3) ^ swz(row)) + (j & 7)] = hi;
         if constexpr (EPI)
-            sX0[row * kStep + 8 * ((4 + (j >> 3)) ^ swz(row)) + (j & 7)] = to_bf16_bits(v - bf16_to_f32(hi));
+            sX0[row * kStep + 8 * ((4 + (j >> 3)) ^ swz(row)) + (j & 7)] = to_bf16_bits(rest_of(v, hi));
     };
     auto stage_u_words = [&]() {
         if constexpr (kUin) {
@@ -731,7 +735,7 @@ __global__ __launch_bounds__(64 * WA * WT, 512 / (64 * WA * WT)) void tile_gemm_
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
                         v[i][q] *= p.s_u;
-                        if (low) v[i][q] -= bf16_to_f32(to_bf16_bits(v[i][q]));
+                        if (low) v[i][q] = rest_of(v[i][q], to_bf16_bits(v[i][q]));
                     }
                     st16(sX0 + row * kStep + 8 * (lc ^ swz(row)),
                          make_uint4(pack_bf16x2(v[i][0], v[i][1]), pack_bf16x2(v[i][2], v[i][3]),

@@ -65,12 +65,65 @@ __device__ __forceinline__ void unpack_vec(const uint4& u, float (&v)[VEC]) {
         v[i] = __uint_as_float(F32 ? w[i] : i % 2 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
 }
 
+// 2^e for e in [-126, 127].
+__device__ __forceinline__ float power2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
+// A row whose squares (or sum) leave fp32's range, or whose squares that count
+// and v_rsq_f32's argument are flushed to zero: its values are read again, times the
+// power of two that brings the largest (or eps's root) to [2, 4), for each of its
+// sums and for its output. Rows of zeros and with infinite values keep what
+// they have. All waves of a row come here together, and no wave reads red[2].
+template <bool XF32, bool WF32>
+__device__ __forceinline__ void norm_fwd_scaled(const NormArgs& p, int64_t row, int first, int step, int wave, int waves,
+                                             float (*red)[16]) {
+    constexpr int VEC = XF32 ? 4 : 8;
+    const int64_t base = row * p.C;
+    float k = 1.0f;
+    auto sum = [&](auto f, float start, auto op, int at) {
+        float s[1] = {start};
+#pragma unroll 1
+        for (int c = first * VEC; c < p.C; c += step * VEC) {
+            float x[VEC];
+            load_vec<XF32, VEC>(p.X, base + c, x);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) s[0] = f(x[i] * k, s[0]);
+        }
+        block_reduce(s, red[at], wave, waves, op);
+        return s[0];
+    };
+    const float m = sum([](float x, float s) { return fmaxf(fabsf(x), s); }, __builtin_sqrtf(p.eps), MaxOp{}, 2);
+    const int e = static_cast<int>(__float_as_uint(m) >> 23);
+    const int up = m > 0.0f && e < 255 ? 128 - max(1, e) : 0;
+    k = power2(up);
+    const float inv = 1.0f / static_cast<float>(p.C);
+    float mu = 0.0f;
+    if (!p.rms) mu = inv * sum([](float x, float s) { return s + x; }, 0.0f, AddOp{}, 0);
+    const float var = sum([&](float x, float s) { return __builtin_fmaf(x - mu, x - mu, s); }, 0.0f, AddOp{}, 1);
+    const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(var, inv, p.eps * k * k));
+#pragma unroll 1
+    for (int c = first * VEC; c < p.C; c += step * VEC) {
+        float x[VEC], w[VEC], b[VEC];
+        load_vec<XF32, VEC>(p.X, base + c, x);
+        load_vec<WF32, VEC>(p.w, c, w);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) b[i] = 0.0f;
+        if (p.b != nullptr) load_vec<WF32, VEC>(p.b, c, b);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) x[i] = __builtin_fmaf((x[i] * k - mu) * r, w[i], b[i]);
+        store_vec<XF32, VEC>(p.Y, base + c, x);
+    }
+    if (first == 0) {
+        if (p.mean != nullptr) p.mean[row] = ldexpf(mu, -up);
+        if (p.rstd != nullptr) p.rstd[row] = ldexpf(r, up);
+    }
+}
+
 // A row by `waves` waves (the workgroup's, or one of its four), a lane NV
 // pieces of 16 bytes of x; weight and bias are on their way with it.
 template <bool XF32, bool WF32, int NV>
 __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs p, int waves) {
     constexpr int VEC = XF32 ? 4 : 8;
-    __shared__ float red[2][16];
+    __shared__ float red[3][16];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t row = waves == 1 ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 6) + wave : blockIdx.x;
     if (row >= p.T) return;  // a whole wave, and only where no barrier follows
@@ -112,7 +165,10 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs p, int waves) {
         }
     }
     block_reduce(s, red[1], wave, waves, AddOp{});
-    const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(s[0], inv, p.eps));
+    const float var = __builtin_fmaf(s[0], inv, p.eps);
+    if (!(var >= 0x1p-100f && var < __builtin_inff()))
+        return norm_fwd_scaled<XF32, WF32>(p, row, first, step, wave, waves, red);
+    const float r = __builtin_amdgcn_rsqf(var);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int c = (first + j * step) * VEC;

@@ -768,9 +768,14 @@ int qlora_epilogue_bwd(const uint16_t* dY, const void* Z, int z_dtype, int64_t r
  *          wanted (else unused, may be NULL)
  *
  * Sums and statistics are fp32 (the variance from x - mu), outputs rounded
- * once; the order of every sum is fixed. Y may be X and dX may be dY; nothing
- * else may overlap. rows == 0: the forward is a no-op, the backward's sums are
- * empty (zeros without accumulate).
+ * once; the order of every sum is fixed. The forward scales a row by a power of
+ * two where its sum or its squares would leave fp32's range (values from about
+ * 1e17 up; with an eps under 2^-100 also those under 1e-15), so that any finite
+ * row has its norm; with eps 0 a row without spread is 0 / 0, NaN. The backward
+ * takes x - mean and rstd as fp32 holds them (values under 3e-39 with eps 0 have
+ * an infinite rstd). Y may be X and dX may be dY; nothing else may overlap.
+ * rows == 0: the forward is a no-op, the backward's sums are empty (zeros
+ * without accumulate).
  * Errors: QL_ERR_NULL, QL_ERR_SHAPE (rows < 0 or 2^22 and more, cols), QL_ERR_UNSUPPORTED
  * (dtypes, eps negative or not finite, rms or accumulate not 0 or 1), QL_ERR_ALIGN,
  * QL_ERR_WORKSPACE, QL_ERR_HIP.

@@ -263,7 +263,9 @@ __device__ __forceinline__ void pair_loss(const PairArgs& p, double d, float& lo
         const float xf = static_cast<float>(x), e = expf(-fabsf(xf)), soft = log1pf(e);
         const float lo = e / (1.0f + e), hi = 1.0f / (1.0f + e);
         const float up = xf >= 0 ? hi : lo, down = xf >= 0 ? lo : hi;  // sigmoid(x), sigmoid(-x)
-        loss = (1.0f - p.smooth) * (soft + fmaxf(-xf, 0.0f)) + (p.smooth > 0.0f ? p.smooth * (soft + fmaxf(xf, 0.0f)) : 0.0f);
+        // a term of weight 0 is none, also where it is infinite
+        loss = (p.smooth < 1.0f ? (1.0f - p.smooth) * (soft + fmaxf(-xf, 0.0f)) : 0.0f) +
+               (p.smooth > 0.0f ? p.smooth * (soft + fmaxf(xf, 0.0f)) : 0.0f);
         slope = p.beta * (p.smooth * up - (1.0f - p.smooth) * down);
         if (xf != xf) loss = xf, slope = x;
     } else if (p.kind == QL_PREF_HINGE) {

@@ -6,7 +6,7 @@ test_gpu_losses'."""
 import pytest
 import torch
 
-from test_gpu_losses import BF16, F32, _close, _distill_case, _distill_check, _e, _pref_check
+from test_gpu_losses import BF16, F32, INF, NINF, _close, _distill_case, _distill_check, _e, _pref_case, _pref_check
 
 pytestmark = pytest.mark.gpu
 
@@ -76,3 +76,22 @@ def test_preference_neighbours_of_a_far_maximum(qn, top_value):
     _close("logp", qn.token_logp(z, labels), want, _e(z) + 2.0 ** -22 * (want.abs() + 40))
     start = torch.tensor([0, 3, 4, 6, 8], device="cuda")
     _pref_check(qn, z, labels, start, torch.randn(4, device="cuda"), torch.rand(2, device="cuda") + 0.5)
+
+
+def test_preference_smoothing_of_one_at_infinity(qn):
+    """A preferred token that is ruled out (x = -inf): with smoothing 1 the loss
+    is -log sigmoid(-x) alone, zero there and infinite at x = inf; with 0 the
+    other way round. Between them it is infinite."""
+    z, _, labels, _, ref, dloss = _pref_case(8, 65, F32, 2, seed=1, masked=0.0)
+    start = torch.tensor([0, 2, 4, 6, 8], device="cuda")
+    y = z.clone()
+    y[0, labels[0]] = NINF  # pair 0: x = -inf
+    y[7, labels[7]] = NINF  # pair 1: x = inf
+    for smooth, want in ((1.0, (0.0, INF)), (0.0, (INF, 0.0)), (0.5, (INF, INF))):
+        loss, L, st = qn.preference_loss_fwd(y, labels, start, ref, 0.3, smooth)
+        assert loss.tolist() == list(want)
+        dz = qn.preference_loss_bwd(y, labels, st, dloss)
+        assert bool(dz.isfinite().all())
+        for i in range(2):  # its slope is beta or nothing
+            assert bool(dz[4 * i:4 * i + 4].any()) == (want[i] == INF)
+    _pref_check(qn, z, labels, start, ref, dloss, 0.3, 1.0)

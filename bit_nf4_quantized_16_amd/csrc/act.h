@@ -16,9 +16,11 @@ __device__ __forceinline__ float logistic2(float x) {
 // 40] (a linear program over 2100 points). For values, which are rounded to
 // bf16, degree 5: 1.1e-5, 2^-7.5 of the half step (degree 4: 6e-5; a polynomial
 // in a for the logarithm of the odds 3e-4 up to a = 8 for as many operations).
-// For slopes, whose sums over rows stay fp32, degree 8: 7e-8 before fp32's own
-// roundings (with degree 5 a bias's gradient was off by 2.2e-6 of its norm, with
-// 8 by 4e-7).
+// Formed in fp32 it is 1.2e-5 up to a = 6 and 1.8e-5 up to 13, where the result
+// leaves fp32: the exponent, up to 122, is rounded twice.
+// For slopes, whose sums over rows stay fp32, degree 8: 1.2e-7 with the
+// coefficients as fp32 holds them, before fp32's own roundings (with degree 5 a
+// bias's gradient was off by 2.2e-6 of its norm, with 8 by 4e-7).
 template <bool FINE>
 __device__ __forceinline__ float normal_tail(float a) {
     constexpr float kFine[9] = {0.14361748099327087f,   0.14368759095668793f, 0.12394635379314423f,

@@ -684,8 +684,10 @@ int q4g_linear_fwd(const ql_q4g_weight* w, const uint16_t* X, int64_t T, uint16_
  *
  *   bias      [N] bf16, or NULL
  *   act       QL_ACT_NONE, QL_ACT_SILU (z sigmoid(z)), QL_ACT_GELU (z times the
- *             normal distribution function, to 1.1e-5 of it) or
- *             QL_ACT_GELU_TANH (z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2)
+ *             normal distribution function) or QL_ACT_GELU_TANH (z (1 +
+ *             tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2), each to 2^-15 of its
+ *             value (GELU to 1.2e-5 of it from z = -6 up, 1.8e-5 below); factors
+ *             of z under fp32's smallest normal number may be taken for zero
  *   residual  [T, N] bf16, or NULL; may be Y itself
  *   Z         out [T, N], z for qlora_epilogue_bwd, fp32 (z_dtype QL_F32) or
  *             rounded to bf16 (QL_BF16: half the memory; z off by up to 2^-9 of

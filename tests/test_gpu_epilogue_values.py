@@ -1,10 +1,12 @@
 """The linear layer's epilogue at the ends of its range: infinite adapter terms,
 and the activations' values to more bits than the result has."""
 
+import math
+
 import pytest
 import torch
 
-from test_gpu_epilogue import ACTS, BF16
+from test_gpu_epilogue import ACTS, BF16, _act
 
 pytestmark = pytest.mark.gpu
 INF = float("inf")
@@ -73,3 +75,32 @@ def test_adapter_terms_past_the_bf16_range(qn, T):
     U = torch.mm(X.float(), A.float().t())
     Y, _, Z = qn.qlora_linear_fwd_epilogue(w, X, A, B, 3.4e38 / float(U.max()), save_z=True)
     assert not bool(Y.isnan().any()) and not bool(Z.isnan().any())
+
+
+@pytest.mark.parametrize("path", ["decode", "gemm", "q4g"])
+@pytest.mark.parametrize("act", ACTS[1:])
+def test_values_everywhere(qn, act, path):
+    """act at every bf16 z from -30 to 30, beside the residual -bf16(act(z)), so
+    that the sum shows 8 more bits of it: within 2^-15 of the value. The exponent
+    (to 126) is formed with 2.5 roundings for GELU, 1.5 for SiLU, 5 for the tanh
+    form: 2.7e-5 at most, GELU's 1.1e-5 of its polynomial among them. The factor
+    of z may be zero where it is under the smallest normal fp32; bf16 results
+    under 2^-126 are steps of 2^-133, rounded by 2^-134."""
+    bits = torch.arange(1 << 16, dtype=torch.int32, device="cuda").to(torch.int16).view(BF16)
+    bias = bits[bits.float().abs() <= 30]
+    bias = bias[:bias.numel() // 8 * 8].contiguous()
+    N, T = bias.numel(), 17 if path == "gemm" else 2
+    z = bias.double()
+    # torch's normal distribution function loses its lower tail
+    v = z * 0.5 * torch.special.erfc(-z * math.sqrt(0.5)) if act == "gelu" else _act(z, act)[0]
+    res = (-v).to(BF16).expand(T, N).contiguous()
+    if path == "q4g":
+        w = qn.q4g_quantize(torch.ones(N, 32, device="cuda"), 32)
+        Y = qn.q4g_linear_fwd_epilogue(w, torch.zeros(T, 32, dtype=BF16, device="cuda"), bias, act, res)
+    else:
+        w = qn.quantize_weight(torch.ones(N, 64, device="cuda"))
+        Y, _, _ = qn.qlora_linear_fwd_epilogue(w, torch.zeros(T, 64, dtype=BF16, device="cuda"), bias=bias, act=act,
+                                               residual=res)
+    want = v + res[0].double()
+    bad = (Y.double() - want).abs() - (2.0 ** -8 * want.abs() + 2.0 ** -15 * v.abs() + 2.0 ** -126 * z.abs() + 2.0 ** -134)
+    assert float(bad.max()) <= 0, (float(bad.max()), float(bias[int(bad.amax(0).argmax())]))

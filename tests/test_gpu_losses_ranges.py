@@ -6,7 +6,8 @@ test_gpu_losses'."""
 import pytest
 import torch
 
-from test_gpu_losses import BF16, F32, INF, NINF, _close, _distill_case, _distill_check, _e, _pref_case, _pref_check
+from test_gpu_losses import (BF16, F32, INF, NINF, _close, _distill_case, _distill_check, _e, _pref_case, _pref_check,
+                             _pref_exact)
 
 pytestmark = pytest.mark.gpu
 
@@ -95,3 +96,48 @@ def test_preference_smoothing_of_one_at_infinity(qn):
         for i in range(2):  # its slope is beta or nothing
             assert bool(dz[4 * i:4 * i + 4].any()) == (want[i] == INF)
     _pref_check(qn, z, labels, start, ref, dloss, 0.3, 1.0)
+
+
+@pytest.mark.parametrize("V", [300, 1500, 4097, 9000, 20001, 60001, 70001])
+@pytest.mark.parametrize("offset", [1e3, -1e5])
+def test_a_common_offset(qn, V, offset):
+    """The same offset on every logit, each way a row is dealt out: nothing but
+    the offset's own rounding of the inputs changes."""
+    z, _, index, top, labels, weight = _distill_case(4, V, 9, F32, seed=V)
+    z.add_(offset)
+    for tau, alpha in ((1.0, 0.0), (1.0, 0.3), (0.7, 0.3)):
+        _distill_check(qn, z, index, top, labels, tau, alpha, weight)
+    z, _, labels, start, ref, dloss = _pref_case(6, V, F32, 1, seed=V, masked=0.2)
+    z.add_(offset)
+    on = labels >= 0
+    want = torch.where(on, torch.log_softmax(z.double(), 1).gather(1, labels.clamp(min=0)[:, None])[:, 0], 0.0)
+    _close("logp", qn.token_logp(z, labels), want, _e(z) + 2.0 ** -22 * (want.abs() + 40))
+    _pref_check(qn, z, labels, start, ref, dloss)
+
+
+def test_preference_of_more_than_2_to_the_31_logits(qn):
+    """Offsets past 32 bits in the sums and in the gradient, which is written in
+    the logits' place from the last row to the first: rows on both sides of
+    2^31."""
+    T, V = 17000, 128002
+    z = torch.empty(T, V, dtype=BF16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(0)
+    for part in z.split(1000):
+        part.copy_(2 * torch.randn(part.shape, generator=g, device="cuda"))
+    labels = torch.randint(0, V, (T,), generator=g, device="cuda")
+    labels[100:16700] = -100
+    # pair 0: the first rows, pair 1: those around 2^31, and both in pair 2's second sequence
+    start = torch.tensor([0, 40, 100, 16770, 16777, 16800, 17000], device="cuda")
+    rows = torch.cat([torch.arange(100, device="cuda"), torch.arange(16700, T, device="cuda")])
+    ends = torch.tensor([0, 40, 100, 170, 177, 200, 400], device="cuda")
+    ref = -12.0 * (ends[1:] - ends[:-1]).float() + torch.randn(6, generator=g, device="cuda")
+    dloss = torch.rand(3, generator=g, device="cuda") + 0.2
+    zr, lr = z[rows], labels[rows]
+    want, tol = _pref_exact(zr, lr, ends, ref, 0.01, 0.1, "sigmoid", False, dloss)
+    loss, L, st = qn.preference_loss_fwd(z, labels, start, ref, 0.01, 0.1)
+    _close("L", L, want["L"], tol["L"])
+    _close("loss", loss, want["loss"], tol["loss"])
+    dz = qn.preference_loss_bwd(z, labels, st, dloss, dlogits=z)
+    assert dz is z
+    _close("dz", z[rows], want["dz"], tol["dz"])
+    assert not any(bool(part.any()) for part in z[100:16700].split(1000))

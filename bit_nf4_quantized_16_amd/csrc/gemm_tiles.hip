@@ -992,7 +992,8 @@ __global__ void split_reduce_kernel(const float* __restrict__ part, int splits, 
 }
 
 // The same with an epilogue: rows of a quarter of MA values, `blocks`
-// workgroups each.
+// workgroups each. (4096 x 11008, T = 300, both launches: bias and residual 80.4 us
+// against 77.9 without an epilogue.)
 __global__ void split_reduce_epilogue_kernel(const float* __restrict__ part, int splits, int64_t T, int64_t MA,
                                              uint32_t blocks, Epilogue ep, uint16_t* out) {
     const uint32_t t = blockIdx.x / blocks;

@@ -11,6 +11,9 @@
 // 16384 x 8192 96 (5.6); backward 4096 x 4096 with both sums 26.4 (3.8),
 // 16384 x 8192 with dw 150 (5.4). Few rows are bound by their way in and out:
 // 1001 x 4096 6.1 and 16.1 us, 3.9 of them the sums' second launch; one row 2.0.
+// fp32, both launches, graphs of calls with outputs of their own: 16384 x 4096 103
+// and 147 us (5.2 and 5.5 TB/s), 4096 x 4096 29.7 and 43, 1001 x 4096 9.0 and 16.7
+// (bf16 by that method: 4096 x 4096 14.8).
 #include "common.h"
 #include "internal.h"
 #include "reduce.h"
@@ -385,9 +388,11 @@ RowPlan row_plan(int64_t C, bool f32, int want) {
 //   4096 x 8192   1x16,1 50.1 | 1x8,2 60.9;  dw alone 16384 x 8192 166.6 | 150.6 | 2x8,2 157.3
 //   4096 x 1024   1x2,1 18.5 | 2x2,1 13.6 | 4x2,1 12.0 | 8x2,1 12.9
 //   8192 x 512    1x1,1 21.4 | 4x1,1 12.1 | 8x1,1 12.1 | 16x1,1 13.0,  600 x 512 6.9 | 6.8 | 7.4 | 9.4
-// So one piece a lane where 16 waves then hold the row (two sums spill with
-// two), two for the root mean square's long rows, whose db is seldom wanted (the
-// plan takes no notice of what is asked for: the same bits either way); up to
+// So one piece a lane where 16 waves then hold the row (two sums spill 13 registers
+// with two: layer norm rows over 8192 bf16 values, 2000 x 16384 64 us, 3.1 TB/s), two
+// for the root mean square's long rows, whose db is seldom wanted (4096 x 8192 43
+// us, with db 62; the plan takes no notice of what is asked for: the same bits
+// either way); up to
 // four rows and eight waves at a time, 16 where there are many rows of eight.
 struct BwdPlan {
     RowPlan row;

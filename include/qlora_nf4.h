@@ -740,7 +740,8 @@ int q4g_linear_fwd_epilogue(const ql_q4g_weight* w, const uint16_t* X, int64_t T
  *   dbias  out [cols] fp32, or NULL; added to with accumulate 1
  *   ws     qlora_epilogue_bwd_workspace(rows, cols) bytes where dbias is wanted
  *
- * rows == 0: dbias is an empty sum. Sums are fp32 in a fixed order.
+ * rows == 0: dbias is an empty sum. Sums are fp32 in a fixed order. At an
+ * infinite Z an activation's slope may be NaN (infinity times a term that is zero).
  * Errors: QL_ERR_NULL, QL_ERR_SHAPE (rows < 0 or over 2^31, cols 2^27 and more, over 2^40
  * values), QL_ERR_UNSUPPORTED (act, z_dtype, accumulate), QL_ERR_ALIGN,
  * QL_ERR_WORKSPACE, QL_ERR_HIP.
